@@ -1,4 +1,5 @@
-"""N:M activation pruning fused with its linear layer, for MI355X (gfx950).
+"""N:M activation pruning fused with its linear layer, and the attention, cache and norms between such layers,
+for MI355X (gfx950).
 
 The compute runs in ``libspa.so`` (hand-written HIP kernels behind a C ABI,
 declared in ``include/spa.h``); this package is its thin Python binding.
@@ -28,4 +29,13 @@ from ._binding import (  # noqa: F401
     sparse_ffn_relu2_prefill,
     workspace,
     workspace_bytes,
+)
+from ._layer import (  # noqa: F401
+    KvCache,
+    attention_decode,
+    attention_prefill,
+    gated_residual_norm,
+    kv_read,
+    kv_write,
+    new_kv_cache,
 )

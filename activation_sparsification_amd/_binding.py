@@ -48,6 +48,21 @@ class _Weight(ctypes.Structure):
                 ("row_sum", ctypes.c_void_p)]
 
 
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("format", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -101,6 +116,23 @@ def lib() -> ctypes.CDLL:
         L.sparse_linear_decode_static.restype = ctypes.c_int
         L.sparse_linear_decode_static.argtypes = [vp, i32, ctypes.POINTER(_Weight), ctypes.POINTER(_Cfg), vp, vp,
                                                   vp, vp, vp]
+        heads, cache, norm, f32 = (ctypes.POINTER(_Heads), ctypes.POINTER(_KvCache), ctypes.POINTER(_Norm),
+                                   ctypes.c_float)
+        L.spa_kv_write.restype = ctypes.c_int
+        L.spa_kv_write.argtypes = [heads, heads, i32, vp, cache, vp]
+        L.spa_kv_read.restype = ctypes.c_int
+        L.spa_kv_read.argtypes = [cache, vp, i32, i32, vp, i32, vp, vp, vp]
+        L.spa_attention_decode_workspace_bytes.restype = sz
+        L.spa_attention_decode_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.attention_decode.restype = ctypes.c_int
+        L.attention_decode.argtypes = [heads, i32, i32, cache, vp, i32, vp, f32, vp, vp, vp, sz, vp]
+        L.spa_attention_prefill_workspace_bytes.restype = sz
+        L.spa_attention_prefill_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.attention_prefill.restype = ctypes.c_int
+        L.attention_prefill.argtypes = [heads, heads, heads, i32, i32, i32, i32, i32, i32, vp, vp, i32, i32, f32, vp, vp,
+                                        vp, sz, vp]
+        L.gated_residual_norm.restype = ctypes.c_int
+        L.gated_residual_norm.argtypes = [vp, i32, i32, i32, vp, i32, norm, vp, i32, f32, norm, f32, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -109,7 +141,9 @@ EXPORTS = ("prepare_weight", "prune_nm", "sparse_linear_decode", "sparse_linear_
            "spa_workspace_bytes", "spa_status_str", "spa_meta_row_bytes", "spa_encode_meta", "spa_decode_meta",
            "prepare_amber", "spa_amber_workspace_bytes", "spa_eta_calibrate", "spa_eta_table", "spa_eta_lookup",
            "sparse_ffn_relu2_prefill", "spa_ffn_workspace_bytes", "prepare_weight_fp8",
-           "sparse_linear_prefill_fp8", "spa_prefill_layout", "sparse_linear_decode_static")
+           "sparse_linear_prefill_fp8", "spa_prefill_layout", "sparse_linear_decode_static",
+           "spa_kv_write", "spa_kv_read", "attention_decode", "spa_attention_decode_workspace_bytes",
+           "attention_prefill", "spa_attention_prefill_workspace_bytes", "gated_residual_norm")
 
 
 @dataclasses.dataclass(frozen=True)

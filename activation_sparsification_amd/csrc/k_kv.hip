@@ -1,0 +1,205 @@
+// The paged key-value cache: writing tokens' vectors (quantised on the way for the 8-bit formats) and reading
+// the first positions of sequences back as dense rows.
+//
+// Both move every byte once: a vector of head_dim elements is held by a group of LG lanes, 8 elements each, so
+// its largest magnitude is a butterfly over the group and nothing passes through memory twice.  A workgroup
+// handles 16 (or more, for short vectors) consecutive tokens of one head, keys and values together: consecutive
+// tokens are consecutive positions of a page, so the codes and the 4-byte scales of a workgroup leave as runs.
+#include "spa_common.h"
+#include "spa_attn.h"
+#include "spa_layer.h"
+
+namespace spa {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct KvArgs {
+  const void* src[2];        // write: keys, values
+  int64_t row_stride[2], head_stride[2];
+  void* pages[2];
+  float* scale[2];
+  void* out[2];              // read: [total][heads][d]
+  const int32_t* slots;      // write: [t]
+  const int32_t* table;      // read
+  const int32_t* cu;
+  int t, heads, d, n_pages, n_seqs, max_pages;
+  FastDiv page;
+};
+
+template <int LG>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int off = LG / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+
+// Codes of 8 values and their vector's scale: the definition's float32 operations in its order.
+template <int FMT, int LG>
+__device__ __forceinline__ uint2 quantise(const float (&x)[8], float& scale) {
+#pragma clang fp contract(off)
+  constexpr float top = FMT == SPA_KV_FP8 ? 448.f : 127.f;
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+  a = group_max<LG>(a);
+  const bool live = a >= 0x1p-100f;
+  scale = live ? __fdiv_rn(a, top) : 0.f;
+  const float inv = live ? __fdiv_rn(top, a) : 0.f;
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = x[4 * h + e] * inv;
+    if constexpr (FMT == SPA_KV_FP8) {
+      w[h] = fp8_pair(q[0], q[1]) | (fp8_pair(q[2], q[3]) << 16);
+    } else {
+      w[h] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[h] |= ((uint32_t)(int)rintf(q[e]) & 0xFFu) << (8 * e);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <int DT, int FMT, int LG>
+__global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
+  constexpr int ROWS = kThreads / LG;
+  const int lane = threadIdx.x % LG;
+  const int head = blockIdx.x % a.heads;
+  const int tok = (blockIdx.x / a.heads) * ROWS + threadIdx.x / LG;
+  const int slot = tok < a.t ? a.slots[tok] : -1;
+  const int page_size = a.page.d;
+  const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
+  const bool ok = slot >= 0 && pg < a.n_pages;                  // the whole group agrees
+  const bool live = ok && lane * 8 < a.d;
+  const size_t cell = ((size_t)pg * a.heads + head) * page_size + (slot - pg * page_size);
+  uint4 raw[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    raw[s] = make_uint4(0, 0, 0, 0);
+    if (live)
+      raw[s] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[s]) + (size_t)tok * a.row_stride[s] +
+                                               (size_t)head * a.head_stride[s] + lane * 8);
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if constexpr (FMT == SPA_KV_NATIVE) {
+      if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pages[s]) + cell * a.d + lane * 8) = raw[s];
+    } else {
+      float x[8], scale;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = elem16<DT>(raw[s], e);
+      const uint2 codes = quantise<FMT, LG>(x, scale);
+      if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.pages[s]) + cell * a.d + lane * 8) = codes;
+      if (live && lane == 0) a.scale[s][cell] = scale;
+    }
+  }
+}
+
+template <int DT, int FMT, int LG>
+__global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
+  constexpr int ROWS = kThreads / LG, PER_WAVE = kWave / LG;
+  const int lane = threadIdx.x % LG;
+  const int head = blockIdx.x % a.heads;
+  const int row = (blockIdx.x / a.heads) * ROWS + threadIdx.x / LG;
+  // this row's sequence: the number of offsets after the first that are at or below the row
+  const int wl = threadIdx.x % kWave;
+  const int first = row - wl / LG;                              // the wave's first row
+  int seq = 0;
+  for (int base = 0; base < a.n_seqs; base += kWave) {
+    const int end = base + wl < a.n_seqs ? a.cu[base + wl + 1] : INT32_MAX;
+#pragma unroll
+    for (int r = 0; r < PER_WAVE; ++r) {
+      const int n = __popcll(__ballot(end <= first + r));
+      if (wl / LG == r) seq += n;
+    }
+  }
+  const bool mine = row < a.t && seq < a.n_seqs && lane * 8 < a.d;
+  if (!mine) return;
+  const int pos = row - a.cu[seq];
+  const int page_size = a.page.d;
+  const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
+  const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
+  const bool ok = pg >= 0 && pg < a.n_pages;
+  const size_t cell = ok ? ((size_t)pg * a.heads + head) * page_size + (pos - col * page_size) : 0;
+  const size_t to = ((size_t)row * a.heads + head) * a.d + lane * 8;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (ok) {
+      if constexpr (FMT == SPA_KV_NATIVE) {
+        v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.pages[s]) + cell * a.d + lane * 8);
+      } else {
+        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.pages[s]) + cell * a.d + lane * 8);
+        const float sc = a.scale[s][cell];
+        float x[8];
+        codes_to_f32<FMT>(c.x, x);
+        codes_to_f32<FMT>(c.y, x + 4);
+        v = make_uint4(pack2<DT>(x[0] * sc, x[1] * sc), pack2<DT>(x[2] * sc, x[3] * sc),
+                       pack2<DT>(x[4] * sc, x[5] * sc), pack2<DT>(x[6] * sc, x[7] * sc));
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[s]) + to) = v;
+  }
+}
+
+template <int DT, int FMT, int LG>
+hipError_t go(bool write, const KvArgs& a, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.t * LG + kThreads - 1) / kThreads * a.heads;
+  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (write) hipLaunchKernelGGL((k_kv_write<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL((k_kv_read<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+template <int DT, int FMT>
+hipError_t by_width(bool write, const KvArgs& a, hipStream_t st) {
+  if (a.d <= 32) return go<DT, FMT, 4>(write, a, st);
+  if (a.d <= 64) return go<DT, FMT, 8>(write, a, st);
+  if (a.d <= 128) return go<DT, FMT, 16>(write, a, st);
+  return go<DT, FMT, 32>(write, a, st);
+}
+template <int DT>
+hipError_t by_format(int fmt, bool write, const KvArgs& a, hipStream_t st) {
+  if (fmt == SPA_KV_NATIVE) return by_width<DT, SPA_KV_NATIVE>(write, a, st);
+  if (fmt == SPA_KV_FP8) return by_width<DT, SPA_KV_FP8>(write, a, st);
+  return by_width<DT, SPA_KV_INT8>(write, a, st);
+}
+hipError_t dispatch(const spa_kv_cache& c, bool write, KvArgs& a, hipStream_t st) {
+  a.pages[0] = c.k; a.pages[1] = c.v;
+  a.scale[0] = c.k_scale; a.scale[1] = c.v_scale;
+  a.heads = c.n_heads; a.d = c.head_dim; a.n_pages = c.n_pages;
+  a.page = FastDiv((uint32_t)c.page_size);
+  // a native write moves bits: one instance serves both 16-bit types
+  if (c.dtype == SPA_F16) return by_format<SPA_F16>(c.format, write, a, st);
+  return by_format<SPA_BF16>(c.format, write, a, st);
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const spa_heads& k, const spa_heads& v, int t, const int32_t* slots, const spa_kv_cache& c,
+                           hipStream_t st) {
+  KvArgs a{};
+  const spa_heads* h[2] = {&k, &v};
+  for (int s = 0; s < 2; ++s) {
+    a.src[s] = h[s]->data;
+    a.row_stride[s] = h[s]->row_stride;
+    a.head_stride[s] = h[s]->head_stride;
+  }
+  a.slots = slots;
+  a.t = t;
+  return dispatch(c, true, a, st);
+}
+
+hipError_t launch_kv_read(const spa_kv_cache& c, const int32_t* table, int n_seqs, int max_pages, const int32_t* cu,
+                          int total, void* k_out, void* v_out, hipStream_t st) {
+  KvArgs a{};
+  a.out[0] = k_out; a.out[1] = v_out;
+  a.table = table; a.cu = cu;
+  a.t = total; a.n_seqs = n_seqs; a.max_pages = max_pages;
+  return dispatch(c, false, a, st);
+}
+
+}  // namespace spa

@@ -1,0 +1,102 @@
+// Device helpers shared by the cache and attention kernels (gfx950).
+#pragma once
+
+#include "spa_common.h"
+
+namespace spa {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Division of an unsigned number below 2^31 by a divisor of 1..2^31 - 1 fixed for the launch: with s =
+// ceil(log2 d) and m = ceil(2^(31 + s) / d), floor(x * m / 2^(31 + s)) = floor(x / d) for every x < 2^31 (the
+// excess of m over 2^(31+s)/d is below 1, so the product is high by less than x / 2^(31+s) <= 1 / d).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit __host__ __device__ FastDiv(uint32_t div) : d(div) {
+    s = 0;
+    while ((1ull << s) < div) ++s;
+    m = (uint32_t)(((1ull << (31 + s)) + div - 1) / div);       // below 2^32: 2^s < 2 d
+  }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t x) const {
+    return (uint32_t)(((uint64_t)x * m) >> (31 + s));
+  }
+};
+
+// Four 8-bit codes as float32.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f32(uint32_t w, float* out) {
+  if constexpr (FMT == SPA_KV_FP8) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    out[0] = lo[0]; out[1] = lo[1]; out[2] = hi[0]; out[3] = hi[1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = (float)((int)(w << (24 - 8 * e)) >> 24);
+  }
+}
+
+template <int DT> struct Vec8;
+template <> struct Vec8<SPA_BF16> { using T = bf16x8; };
+template <> struct Vec8<SPA_F16> { using T = f16x8; };
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, f32x4 c) {
+  using V = typename Vec8<DT>::T;
+  if constexpr (DT == SPA_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 c) {
+  using V = typename Vec8<DT>::T;
+  if constexpr (DT == SPA_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+}
+
+// 2^x and log2 x on the transcendental unit.  The arguments that occur are 0, finite numbers of ordinary size
+// and -inf (2^-inf = 0); results below 2^-126 may flush to 0.
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int o = __shfl_up(v, off, kWave);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+// The item with this index when sequence s contributes count(s) of them: its sequence and its number within
+// it.  Every wave finds it by itself; seq = n when there is none.
+template <typename Count>
+__device__ __forceinline__ void locate(int index, int n, Count count, int& seq, int& local) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int before = 0;
+  for (int base = 0; base < n; base += kWave) {
+    const int c = base + lane < n ? count(base + lane) : 0;
+    const int incl = wave_scan(c) + before;
+    const uint64_t past = __ballot(incl > index);
+    if (past) {
+      const int at = __ffsll((unsigned long long)past) - 1;
+      seq = base + at;
+      local = index - __shfl(incl - c, at, kWave);
+      return;
+    }
+    before = __shfl(incl, kWave - 1, kWave);
+  }
+  seq = n;
+  local = 0;
+}
+
+}  // namespace spa

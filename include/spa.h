@@ -397,6 +397,160 @@ spa_status spa_prefill_layout(int32_t t, int32_t k, int32_t dtype, const spa_pru
 size_t spa_workspace_bytes(int32_t entry, int32_t t, int32_t k, int32_t n_out, int32_t dtype,
                            const spa_prune_cfg* cfg);
 
+/* ------------------------------------------------------------------------
+ * Between the linear layers: the key-value cache, attention over it and over
+ * prompts, and the norms around a block.  float32 throughout for sums,
+ * softmax statistics and norms; 16-bit dtypes for the vectors.
+ * ------------------------------------------------------------------------ */
+enum { SPA_KV_NATIVE = 0, SPA_KV_FP8 = 1, SPA_KV_INT8 = 2 };
+enum { SPA_NORM_NONE = 0, SPA_NORM_RMS = 1, SPA_NORM_LAYER = 2 };
+
+/* Vectors of several heads: head h of row i is the head_dim consecutive
+ * elements at data + i * row_stride + h * head_stride (strides in elements,
+ * so that a slice of a packed projection needs no copy).  Strides must be
+ * within 0..2^23 (else SPA_ERR_INVALID); the kernels are built for 16-byte
+ * aligned data and strides that are multiples of 8 (else
+ * SPA_ERR_UNSUPPORTED). */
+typedef struct spa_heads {
+  const void* data;         /* [device] */
+  int64_t row_stride;
+  int64_t head_stride;
+} spa_heads;
+
+/* A paged cache of one layer's keys and values.  k and v are
+ * [n_pages][n_heads][page_size][head_dim], 16-byte aligned; slot s is
+ * position s % page_size of page s / page_size.
+ *  SPA_KV_NATIVE  elements of dtype; no scales
+ *  SPA_KV_FP8     e4m3 codes, SPA_KV_INT8 signed bytes, with one float32
+ *                 scale per page, head and position in k_scale and v_scale
+ *                 [n_pages][n_heads][page_size].  With a = max |x| over a
+ *                 vector and Q = 448 (e4m3) or 127 (int8): scale = a / Q,
+ *                 code = x * (Q / a) rounded to nearest even, each division
+ *                 and product one float32 operation; a vector with a < 2^-100
+ *                 is stored as zeros with scale 0.  The value of a code is
+ *                 code * scale.
+ * dtype (SPA_F16 or SPA_BF16) is the type of the vectors that go in and out.
+ * head_dim must be a multiple of 8 up to 256 and n_pages * page_size *
+ * n_heads below 2^31, else SPA_ERR_UNSUPPORTED; any page_size >= 1. */
+typedef struct spa_kv_cache {
+  int32_t dtype;
+  int32_t format;           /* SPA_KV_* */
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_heads;
+  int32_t head_dim;
+  void* k;                  /* [device] */
+  void* v;                  /* [device] */
+  float* k_scale;           /* [device], 8-bit formats */
+  float* v_scale;           /* [device], 8-bit formats */
+} spa_kv_cache;
+
+/*
+ * spa_kv_write -- store t tokens' keys and values (rows of n_heads vectors,
+ * cache->dtype) at the given slots, quantised on the way for the 8-bit
+ * formats.  slots: [device] [t] int32; a slot outside [0, n_pages *
+ * page_size) -- -1 for a padding token, say -- is skipped.  Two tokens of a
+ * call must not name the same slot.  t >= 0 (0 is a no-op).
+ */
+spa_status spa_kv_write(const spa_heads* k, const spa_heads* v, int32_t t, const int32_t* slots,
+                        const spa_kv_cache* cache, void* stream);
+
+/*
+ * spa_kv_read -- the first positions of n_seqs sequences as dense rows, for
+ * attention over a prompt whose beginning is cached.  Sequence s's position p
+ * is slot page_table[s][p / page_size] * page_size + p % page_size; row
+ * cu_seqlens[s] + p of the outputs receives it, for p < cu_seqlens[s + 1] -
+ * cu_seqlens[s].
+ *  page_table [device] [n_seqs][max_pages] int32
+ *  cu_seqlens [device] [n_seqs + 1] int32, ascending from 0
+ *  k_out, v_out [device] [total][n_heads][head_dim] cache->dtype; the float32
+ *             product code * scale rounded once to nearest even
+ * A position past max_pages pages, or on a page outside [0, n_pages), reads
+ * as zeros.  Rows at or past cu_seqlens[n_seqs] are not written.
+ */
+spa_status spa_kv_read(const spa_kv_cache* cache, const int32_t* page_table, int32_t n_seqs, int32_t max_pages,
+                       const int32_t* cu_seqlens, int32_t total, void* k_out, void* v_out, void* stream);
+
+/*
+ * attention_decode -- attention of one new token per sequence over its cache:
+ *   out[s][h] = sum_p softmax_p(scale * q[s][h] . k_p) v_p
+ * over the positions p < seq_lens[s] of key-value head h / (n_q_heads /
+ * n_heads).  Positions past max_pages pages or on a page outside
+ * [0, n_pages) do not count; a sequence without any gets zeros.
+ *  q         rows s < n_seqs of n_q_heads vectors, cache->dtype
+ *  page_table [device] [n_seqs][max_pages] int32, as for spa_kv_read
+ *  seq_lens  [device] [n_seqs] int32, including the new token's own position
+ *            if it is to be seen (write it first)
+ *  out       [device] [n_seqs][n_q_heads][head_dim] cache->dtype
+ *  lse       [device] [n_seqs][n_q_heads] float32 or NULL: the natural
+ *            logarithm of the sum of exp(scale * q . k_p) (-inf for an empty
+ *            sequence)
+ *  workspace [device] spa_attention_decode_workspace_bytes(...) bytes,
+ *            16-byte aligned, no initial contents needed: the partial sums
+ *            of sequences that are split over the chip
+ * n_q_heads must be a multiple of n_heads, scale > 0 and finite.  Lengths
+ * stay on the device: the split adapts to them without a host round trip,
+ * and a captured call serves later lengths.  Results do not depend on timing
+ * (no atomic sums).
+ */
+size_t spa_attention_decode_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+spa_status attention_decode(const spa_heads* q, int32_t n_seqs, int32_t n_q_heads, const spa_kv_cache* cache,
+                            const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, float scale,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attention_prefill -- attention over packed prompts.  Sequence s has the
+ * query rows [cu_q[s], cu_q[s+1]) and the key and value rows [cu_k[s],
+ * cu_k[s+1]); with lq and lk rows of each, query i sees key j when, with
+ * causal != 0, j <= i + lk - lq (the last query sees every key: prompts
+ * whose beginning is cached have lk > lq), and every key otherwise.  A query
+ * that sees none gets zeros and lse -inf.
+ *  q, k, v   tq rows of n_q_heads and tk rows of n_kv_heads vectors of dtype
+ *            (SPA_F16 or SPA_BF16)
+ *  cu_q, cu_k [device] [n_seqs + 1] int32, ascending from 0
+ *  out       [device] [tq][n_q_heads][head_dim] dtype
+ *  lse       [device] [tq][n_q_heads] float32 or NULL
+ *  workspace [device] spa_attention_prefill_workspace_bytes(...) bytes (may
+ *            be 0, then NULL), 16-byte aligned, no initial contents needed
+ * n_q_heads must be a multiple of n_kv_heads, scale > 0 and finite;
+ * head_dim a multiple of 8 up to 256.  Rows of out and lse outside every
+ * sequence are not written.
+ */
+size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                             int32_t head_dim);
+spa_status attention_prefill(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t tq,
+                             int32_t tk, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_q,
+                             const int32_t* cu_k, int32_t n_seqs, int32_t causal, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gated_residual_norm -- the norms after one block and before the next, with
+ * the block's gate and residual scale, one pass over each row:
+ *   u = N_post(x);  h = residual + scale * gate * u;  y = N_pre(h)
+ * N is one of
+ *   SPA_NORM_NONE   the identity (for pre: y = h)
+ *   SPA_NORM_RMS    x / sqrt(mean(x^2) + eps) * weight + bias
+ *   SPA_NORM_LAYER  (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias
+ * (weight and bias may be NULL: 1 and 0; a NULL descriptor is SPA_NORM_NONE).
+ * Everything is float32 between the inputs and the two outputs; N_pre sees h
+ * before it is rounded.
+ *  x, y      [device] [t][c] dtype; gate NULL (gate_rows 0), [c] (gate_rows
+ *            1) or [t][c] (gate_rows t); weights and biases [c]; all of dtype
+ *  residual  [device] [t][c] stream_dtype (dtype, or SPA_F32) or NULL for 0
+ *  h         [device] [t][c] stream_dtype, or NULL
+ *  y         may be NULL if h is not; h may be residual itself, and y may be
+ *            x itself
+ * t >= 0, c >= 1; c above 65536 is SPA_ERR_UNSUPPORTED.
+ */
+typedef struct spa_norm {
+  int32_t kind;             /* SPA_NORM_* */
+  const void* weight;       /* [device] [c] or NULL */
+  const void* bias;         /* [device] [c] or NULL */
+} spa_norm;
+spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t c, const void* residual,
+                               int32_t stream_dtype, const spa_norm* post, const void* gate, int32_t gate_rows,
+                               float scale, const spa_norm* pre, float eps, void* h, void* y, void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* spa_status_str(spa_status s);
 
