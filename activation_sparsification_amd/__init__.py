@@ -30,12 +30,19 @@ from ._binding import (  # noqa: F401
     workspace,
     workspace_bytes,
 )
-from ._layer import (  # noqa: F401
-    KvCache,
-    attention_decode,
-    attention_prefill,
-    gated_residual_norm,
-    kv_read,
-    kv_write,
-    new_kv_cache,
-)
+# The cache, attention and norm calls are bound natively (_layer): loaded at first use, so that this package can be
+# imported to build them.
+_LAYER = ("KvCache", "attention_decode", "attention_prefill", "gated_residual_norm", "kv_read", "kv_write", "new_kv_cache")
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import _layer
+    for n in _LAYER:
+        globals()[n] = getattr(_layer, n)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_LAYER))
