@@ -54,96 +54,181 @@ __device__ __forceinline__ int seq_tiles(const DecodeAttnArgs& a, int s) {
   return (min(max(a.lens[s], 0), cap) + kTile - 1) / kTile;
 }
 
-// The tiles of a piece: total tiles over the pieces wanted, the same on every wave.
+// The most tiles of a piece, the same on every wave: total tiles over the pieces wanted.  Cutting each sequence
+// into whole pieces makes about half a piece more per sequence, which is taken off the wanted number.
 __device__ __forceinline__ int piece_tiles(const DecodeAttnArgs& a) {
   const int lane = threadIdx.x & (kWave - 1);
   long long total = 0;
   for (int base = 0; base < a.n_seqs; base += kWave) total += base + lane < a.n_seqs ? seq_tiles(a, base + lane) : 0;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off, kWave);
-  const long long per = (total + a.target - 1) / a.target;
-  return (int)max(per, (long long)kMinTiles);
+  const int want = max(a.target - a.n_seqs / 2, (a.target + 3) / 4);
+  return (int)max((total + want - 1) / want, (long long)kMinTiles);
 }
 __device__ __forceinline__ int seq_pieces(const DecodeAttnArgs& a, int s, int per) {
   return max((seq_tiles(a, s) + per - 1) / per, 1);       // an empty sequence is one piece, of nothing
 }
 
+// One piece of a sequence, for one key-value head and up to 16 of its query heads.
+struct Piece {
+  int seq, head, h0, heads;    // key-value head; first query head and their number
+  int len;                     // positions of the sequence
+  int begin, end;              // tiles
+  bool whole;                  // the sequence is this piece alone
+};
+__device__ __forceinline__ bool find_piece(const DecodeAttnArgs& a, Piece& p) {
+  const int per = piece_tiles(a);
+  int piece;
+  locate(blockIdx.x, a.n_seqs, [&](int s) { return seq_pieces(a, s, per); }, p.seq, piece);
+  if (p.seq >= a.n_seqs) return false;
+  p.seq = __builtin_amdgcn_readfirstlane(p.seq);
+  piece = __builtin_amdgcn_readfirstlane(piece);
+  const int ht = blockIdx.y / a.hkv;
+  p.head = blockIdx.y % a.hkv;
+  p.heads = min(a.group - 16 * ht, 16);
+  p.h0 = p.head * a.group + 16 * ht;
+  p.len = min(max(a.lens[p.seq], 0), a.max_pages * (int)a.page.d);
+  const int tiles = (p.len + kTile - 1) / kTile, n = seq_pieces(a, p.seq, per);
+  const int even = (tiles + n - 1) / n;
+  p.begin = min(piece * even, tiles);
+  p.end = min(p.begin + even, tiles);
+  p.whole = n == 1;
+  return true;
+}
+
+// Four 8-bit codes as two words of 16-bit values (exact in both types: e4m3 has 4 significant bits, int8 7).
+template <int DT, int FMT>
+__device__ __forceinline__ uint2 widen4(uint32_t c) {
+  if constexpr (FMT == SPA_KV_FP8 && DT == SPA_BF16) {
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, true)));
+  } else if constexpr (FMT == SPA_KV_FP8) {
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.f, true)));
+  } else {
+    float x[4];
+    codes_to_f32<FMT>(c, x);
+    return make_uint2(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]));
+  }
+}
 // 8 consecutive elements of a cached row as a 16-bit matrix operand.
 template <int DT, int FMT>
 __device__ __forceinline__ uint4 widen8(uint2 c) {
-  float x[8];
-  codes_to_f32<FMT>(c.x, x);
-  codes_to_f32<FMT>(c.y, x + 4);
-  return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+  const uint2 lo = widen4<DT, FMT>(c.x), hi = widen4<DT, FMT>(c.y);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
-
-// NV consecutive elements of a cached row, as pairs of 16-bit values.
-template <int DT, int FMT, int NV>
-__device__ __forceinline__ void load_row(const void* base, size_t cell, int d, int at, bool live, uint32_t (&w)[NV / 2]) {
-  if (!live) {
+// NV elements as stored, to pairs of 16-bit values.
+template <int DT, int FMT, int NV, int VW>
+__device__ __forceinline__ void widen_row(const uint32_t (&raw)[VW], uint32_t (&w)[NV / 2]) {
 #pragma unroll
-    for (int i = 0; i < NV / 2; ++i) w[i] = 0;
-    return;
-  }
-  if constexpr (FMT == SPA_KV_NATIVE) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + cell * d + at);
-#pragma unroll
-    for (int i = 0; i < NV / 2; ++i) w[i] = p[i];
-  } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + cell * d + at);
-#pragma unroll
-    for (int i = 0; i < NV / 4; ++i) {
-      float x[4];
-      codes_to_f32<FMT>(p[i], x);
-      w[2 * i] = pack2<DT>(x[0], x[1]);
-      w[2 * i + 1] = pack2<DT>(x[2], x[3]);
+  for (int i = 0; i < VW; ++i) {
+    if constexpr (FMT == SPA_KV_NATIVE) {
+      w[i] = raw[i];
+    } else {
+      const uint2 x = widen4<DT, FMT>(raw[i]);
+      w[2 * i] = x.x;
+      w[2 * i + 1] = x.y;
     }
   }
 }
 
+// Largest of the four lanes that hold one column (lanes col, col + 16, + 32, + 48), on each of them.
+__device__ __forceinline__ float across_groups_max(float v) {
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// The query operand of k step c: columns are query heads, elements q_at(c, g).. + 7.
+template <int FMT>
+__device__ __forceinline__ int q_at(int c, int g) {
+  // 8-bit keys are read 16 bytes at a time, so two steps share 64 dimensions and a lane's 16 are consecutive
+  if constexpr (FMT == SPA_KV_NATIVE) return 32 * c + 8 * g;
+  else return 64 * (c / 2) + 16 * g + 8 * (c % 2);
+}
+template <int FMT, int KC>
+__device__ __forceinline__ void load_q(const DecodeAttnArgs& a, const Piece& p, int col, int g, uint4 (&qf)[KC]) {
+  const uint16_t* q = a.q + (size_t)p.seq * a.q_row + (size_t)(p.h0 + min(col, p.heads - 1)) * a.q_head;
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const int at = q_at<FMT>(c, g);
+    qf[c] = make_uint4(0, 0, 0, 0);
+    if (col < p.heads && at < a.d) qf[c] = *reinterpret_cast<const uint4*>(q + at);
+  }
+}
+
+// Joins the four waves and writes the piece's result: lane (col, g) holds dimensions NV * (4 g + r) + i of query
+// head col, its maximum and its own positions' sum.
 template <int DT, int FMT, int DP>
-__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnArgs a) {
-  constexpr int KC = DP / 32;      // k steps of S
-  constexpr int NV = DP / 16;      // dimensions of V a lane holds
+__device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, const f32x4 (&o)[DP / 16], float m, float l) {
+  constexpr int NV = DP / 16;
   __shared__ float s_o[kWaves][16][DP + 4];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int col = lane & 15, g = lane >> 4;
-  const int per = piece_tiles(a);
-  int seq, piece;
-  locate(blockIdx.x, a.n_seqs, [&](int s) { return seq_pieces(a, s, per); }, seq, piece);
-  if (seq >= a.n_seqs) return;
-  const int head = blockIdx.y % a.hkv, ht = blockIdx.y / a.hkv;     // key-value head, tile of 16 query heads
-  const int heads = min(a.group - 16 * ht, 16);                     // query heads of this tile
-  const int h0 = head * a.group + 16 * ht;
-  const int len = min(max(a.lens[seq], 0), a.max_pages * (int)a.page.d);
-  const int tile_end = min((len + kTile - 1) / kTile, (piece + 1) * per);
-
-  uint4 qf[KC];
-  {
-    const uint16_t* q = a.q + (size_t)seq * a.q_row + (size_t)(h0 + min(col, heads - 1)) * a.q_head;
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
 #pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      const int at = 32 * c + 8 * g;
-      qf[c] = make_uint4(0, 0, 0, 0);
-      if (col < heads && at < a.d) qf[c] = *reinterpret_cast<const uint4*>(q + at);
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = o[i][r];
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.heads * (DP / 2); e += kWaves * kWave) {
+    const int h = e / (DP / 2), dim = e % (DP / 2) * 2;
+    if (dim >= a.d) continue;
+    float mx = s_m[0][h];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = exp2_hw(s_m[w][h] - base);
+      sum += f * s_l[w][h];
+      x0 += f * s_o[w][h][dim];
+      x1 += f * s_o[w][h][dim + 1];
+    }
+    if (p.whole) {
+      const float inv = sum > 0.f ? 1.f / (sum * kPScale<FMT>) : 0.f;
+      const size_t to = (size_t)p.seq * a.hq + p.h0 + h;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
+      if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
+    } else {
+      const size_t to = (size_t)blockIdx.x * a.hq + p.h0 + h;
+      *reinterpret_cast<float2*>(a.part_o + to * a.d + dim) = make_float2(x0, x1);
+      if (dim == 0) a.part_ml[to] = make_float2(mx, sum);
     }
   }
+}
+
+// Any page size and head_dim: a lane finds one position's cell and the others get it by lane exchange.
+template <int DT, int FMT, int DP>
+__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnArgs a) {
+  constexpr int KC = DP / 32;      // k steps of S
+  constexpr int NV = DP / 16;      // dimensions of V a lane holds
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int col = lane & 15, g = lane >> 4;
+  Piece p;
+  if (!find_piece(a, p)) return;
+  uint4 qf[KC];
+  load_q<FMT, KC>(a, p, col, g, qf);
 
   f32x4 o[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
 
-  for (int tile = piece * per + wave; tile < tile_end; tile += kWaves) {
+  for (int tile = p.begin + wave; tile < p.end; tile += kWaves) {
     // lane i < 32 finds position i's cell; a position that does not count is bit i of `gone`
     const int pos = tile * kTile + (lane & 31);
-    const int p0 = min(pos, len - 1);
+    const int p0 = min(pos, p.len - 1);
     const int pc = (int)a.page.div((uint32_t)p0);
-    const int pg = a.table[(size_t)seq * a.max_pages + pc];
+    const int pg = a.table[(size_t)p.seq * a.max_pages + pc];
     const bool ok = pg >= 0 && pg < a.n_pages;
-    const int cell = ok ? (pg * a.hkv + head) * (int)a.page.d + (p0 - pc * (int)a.page.d) : 0;
-    const uint32_t gone = (uint32_t)__ballot(pos >= len || !ok);
+    const int cell = ok ? (pg * a.hkv + p.head) * (int)a.page.d + (p0 - pc * (int)a.page.d) : 0;
+    const uint32_t gone = (uint32_t)__ballot(pos >= p.len || !ok);
     const uint32_t bad = (uint32_t)__ballot(!ok);            // its cell is not the sequence's: the values are dropped
     float ksc = 1.f, vsc = 1.f;
     if constexpr (FMT != SPA_KV_NATIVE) {
@@ -157,7 +242,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
       f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        const int at = 32 * c + 8 * g;
+        const int at = q_at<FMT>(c, g);
         uint4 kf = make_uint4(0, 0, 0, 0);
         if (at < a.d) {
           if constexpr (FMT == SPA_KV_NATIVE)
@@ -186,7 +271,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
     const float alpha = exp2_hw(m - base);
     m = mx;
     l *= alpha;
-    float p[8];
+    float w[8];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -194,15 +279,21 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
         float e = exp2_hw(t[b][r] - base);
         l += e;
         if constexpr (FMT != SPA_KV_NATIVE) e *= __shfl(vsc, 16 * b + 4 * g + r, kWave) * kPScale<FMT>;
-        p[4 * b + r] = e;
+        w[4 * b + r] = e;
       }
-    const uint4 pf = make_uint4(pack2<DT>(p[0], p[1]), pack2<DT>(p[2], p[3]), pack2<DT>(p[4], p[5]), pack2<DT>(p[6], p[7]));
+    const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
     uint32_t vr[8][NV / 2];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = (j < 4 ? 4 * g + j : 16 + 4 * g + j - 4);
       const size_t vc = (size_t)(uint32_t)__shfl(cell, i, kWave);
-      load_row<DT, FMT, NV>(a.v, vc, a.d, NV * col, NV * col < a.d && !((bad >> i) & 1u), vr[j]);
+      constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1, VW = NV * ES / 4;
+      uint32_t raw[VW];
+      const bool live = NV * col < a.d && !((bad >> i) & 1u);
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.v) + (vc * a.d + NV * col) * ES);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) raw[e] = live && NV * col + 4 / ES * e < a.d ? at[e] : 0u;
+      widen_row<DT, FMT, NV>(raw, vr[j]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -217,48 +308,184 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
     }
   }
 
-  // join the four waves; lane (col, g) holds dimensions NV * (4 g + r) + i of query head col
-  l += __shfl_xor(l, 16, kWave);
-  l += __shfl_xor(l, 32, kWave);
-  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = o[i][r];
-  __syncthreads();
-  const bool whole = seq_pieces(a, seq, per) == 1;
-  for (int e = threadIdx.x; e < heads * (DP / 2); e += kWaves * kWave) {
-    const int h = e / (DP / 2), dim = e % (DP / 2) * 2;
-    if (dim >= a.d) continue;
-    float mx = s_m[0][h];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_hw(s_m[w][h] - base);
-      sum += f * s_l[w][h];
-      x0 += f * s_o[w][h][dim];
-      x1 += f * s_o[w][h][dim + 1];
-    }
-    if (whole) {
-      const float inv = sum > 0.f ? 1.f / (sum * kPScale<FMT>) : 0.f;
-      const size_t to = (size_t)seq * a.hq + h0 + h;
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
-      if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
-    } else {
-      const size_t to = (size_t)blockIdx.x * a.hq + h0 + h;
-      *reinterpret_cast<float2*>(a.part_o + to * a.d + dim) = make_float2(x0, x1);
-      if (dim == 0) a.part_ml[to] = make_float2(mx, sum);
-    }
-  }
+  finish<DT, FMT, DP>(a, p, o, m, l);
 }
 
-// One wave per (sequence, query head): the pieces' sums brought to their common maximum and added in order.
+// Pages of whole 16-position blocks and head_dim == DP: a block's rows are consecutive, so a tile has two bases that
+// the whole wave shares.  The page numbers of a wave's next 32 tiles are held one to a lane; keys of the next
+// tile are on their way while this tile's softmax and V product run, and values while its scores are formed.
+template <int DT, int FMT, int DP>
+__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(DecodeAttnArgs a) {
+  constexpr int KC = DP / 32, NV = DP / 16;
+  constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1;
+  constexpr int KL = FMT == SPA_KV_NATIVE ? KC : KC / 2;     // 16-byte key loads of a lane per block
+  constexpr int VW = NV * ES / 4;                            // 4-byte words of a lane's value load
+  constexpr int kBatch = kWave / 2;                          // tiles whose page numbers are held
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, g = lane >> 4;
+  Piece p;
+  if (!find_piece(a, p)) return;
+  uint4 qf[KC];
+  load_q<FMT, KC>(a, p, col, g, qf);
+
+  f32x4 o[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
+  int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
+  auto fetch_pages = [&](int it) {
+    const int block = (first + kWaves * (it + lane / 2)) * 2 + (lane & 1);
+    const int at = block * 16;
+    pages = -1;
+    if (at < p.len) {
+      pages = a.table[(size_t)p.seq * a.max_pages + a.page.div((uint32_t)at)];
+      if (pages >= a.n_pages) pages = -1;
+    }
+  };
+  // the first cell of block b of tile number `it`, and whether its page is there (else cell 0 of the cache)
+  auto base_of = [&](int it, int b, bool& there) {
+    const int pg = __builtin_amdgcn_readlane(pages, 2 * (it % kBatch) + b);
+    const uint32_t at = (uint32_t)((first + kWaves * it) * 2 + b) * 16;
+    there = pg >= 0;
+    const uint32_t cell = ((uint32_t)pg * a.hkv + p.head) * a.page.d + (at - a.page.div(at) * a.page.d);
+    return there ? cell : 0u;
+  };
+  uint4 kr[2][KL];
+  float4 ksc[2], vsc[2];
+  const uint32_t k_lane = (uint32_t)(col * DP * ES + 16 * g), v_lane = (uint32_t)((4 * g * DP + NV * col) * ES);
+  auto load_k = [&](const uint32_t (&cell)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (DP * ES);
+#pragma unroll
+      for (int c = 0; c < KL; ++c) kr[b][c] = *reinterpret_cast<const uint4*>(base + (k_lane + 64 * c));
+      if constexpr (FMT != SPA_KV_NATIVE) {
+        ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
+        vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
+      }
+    }
+  };
+
+  uint32_t cell[2];
+  bool there[2] = {true, true};
+  if (n > 0) {
+    fetch_pages(0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) cell[b] = base_of(0, b, there[b]);
+    load_k(cell);
+  }
+  for (int it = 0; it < n; ++it) {
+    const int tile = first + kWaves * it;
+    // values of this tile
+    uint32_t vraw[8][VW];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (DP * ES);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(base + (v_lane + (j % 4) * DP * ES));
+#pragma unroll
+      for (int i = 0; i < VW; ++i) vraw[j][i] = w[i];
+    }
+    // scores
+    f32x4 s[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        uint4 kf;
+        if constexpr (FMT == SPA_KV_NATIVE) kf = kr[b][c];
+        else kf = widen8<DT, FMT>(c % 2 ? make_uint2(kr[b][c / 2].z, kr[b][c / 2].w) : make_uint2(kr[b][c / 2].x, kr[b][c / 2].y));
+        s[b] = mfma16<DT>(kf, qf[c], s[b]);
+      }
+    }
+    float t[8], vs[8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float kq[4] = {ksc[b].x, ksc[b].y, ksc[b].z, ksc[b].w}, vq[4] = {vsc[b].x, vsc[b].y, vsc[b].z, vsc[b].w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        t[4 * b + r] = s[b][r] * a.c;
+        if constexpr (FMT != SPA_KV_NATIVE) t[4 * b + r] *= kq[r];
+        vs[4 * b + r] = FMT != SPA_KV_NATIVE ? vq[r] * kPScale<FMT> : 1.f;
+      }
+    }
+    // the last tile's end and absent pages: what does not count is removed from the scores, the values and their scales
+    const bool cut = (tile + 1) * kTile > p.len || !there[0] || !there[1];
+    uint32_t gone = 0;
+    if (cut) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int pos = tile * kTile + 16 * (j / 4) + 4 * g + j % 4;
+        if (pos >= p.len || !there[j / 4]) {
+          gone |= 1u << j;
+          t[j] = -INFINITY;
+          vs[j] = 0.f;
+        }
+      }
+    }
+    // keys of the next tile
+    if (it + 1 < n) {
+      if ((it + 1) % kBatch == 0) fetch_pages(it + 1);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) cell[b] = base_of(it + 1, b, there[b]);
+      load_k(cell);
+    }
+    // softmax
+    float mx = t[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) mx = fmaxf(mx, t[j]);
+    mx = across_groups_max(mx);
+    if (__any(mx > m)) {
+      const float now = fmaxf(m, mx), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+      m = now;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[i] *= alpha;
+    }
+    const float base = m == -INFINITY ? 0.f : m;           // nothing seen yet: every weight is 0
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = exp2_hw(t[j] - base);
+      l += w[j];
+      if constexpr (FMT != SPA_KV_NATIVE) w[j] *= vs[j];
+    }
+    const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
+    if (cut) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((gone >> j) & 1u)
+#pragma unroll
+          for (int i = 0; i < VW; ++i) vraw[j][i] = 0;
+    }
+    uint32_t vr[8][NV / 2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) widen_row<DT, FMT, NV>(vraw[j], vr[j]);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
+      uint4 vf;
+      vf.x = __builtin_amdgcn_perm(vr[1][i / 2], vr[0][i / 2], sel);
+      vf.y = __builtin_amdgcn_perm(vr[3][i / 2], vr[2][i / 2], sel);
+      vf.z = __builtin_amdgcn_perm(vr[5][i / 2], vr[4][i / 2], sel);
+      vf.w = __builtin_amdgcn_perm(vr[7][i / 2], vr[6][i / 2], sel);
+      o[i] = mfma16<DT>(vf, pf, o[i]);
+    }
+  }
+  finish<DT, FMT, DP>(a, p, o, m, l);
+}
+
+// One workgroup per (sequence, query head): the pieces' sums brought to their common maximum and added, eight
+// runs of pieces side by side and then the runs in order.
+constexpr int kJoinRuns = 8, kJoinCols = 32;
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kWave) k_attention_decode_join(DecodeAttnArgs a) {
-  const int lane = threadIdx.x;
+__global__ void __launch_bounds__(kJoinRuns * kJoinCols) k_attention_decode_join(DecodeAttnArgs a) {
+  __shared__ float4 s_x[kJoinRuns][kJoinCols][2];
+  __shared__ float s_sum[kJoinRuns];
+  const int lane = threadIdx.x & (kWave - 1);
   const int seq = blockIdx.x / a.hq, head = blockIdx.x % a.hq;
   const int per = piece_tiles(a);
   const int pieces = seq_pieces(a, seq, per);
@@ -272,31 +499,54 @@ __global__ void __launch_bounds__(kWave) k_attention_decode_join(DecodeAttnArgs 
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, kWave));
   const float base = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < pieces; ++i) {
+  const int run = threadIdx.x / kJoinCols, c = threadIdx.x % kJoinCols;
+  float sum = 0.f;
+  float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i = run; i < pieces; i += kJoinRuns) {
     const size_t row = (size_t)(first + i) * a.hq + head;
     const float2 ml = a.part_ml[row];
     const float f = exp2_hw(ml.x - base);
     sum += f * ml.y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + kWave * e < a.d) x[e] += f * a.part_o[row * a.d + lane + kWave * e];
+    for (int e = 0; e < 2; ++e) {
+      const int at = 4 * (c + kJoinCols * e);
+      if (at < a.d) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + row * a.d + at);
+        x[e].x += f * v.x; x[e].y += f * v.y; x[e].z += f * v.z; x[e].w += f * v.w;
+      }
+    }
+  }
+  s_x[run][c][0] = x[0];
+  s_x[run][c][1] = x[1];
+  if (c == 0) s_sum[run] = sum;
+  __syncthreads();
+  const int at = 4 * (int)threadIdx.x;
+  if (at >= a.d) return;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  sum = 0.f;
+#pragma unroll
+  for (int r = 0; r < kJoinRuns; ++r) {
+    const float4 v = s_x[r][threadIdx.x % kJoinCols][threadIdx.x / kJoinCols];
+    y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    sum += s_sum[r];
   }
   const float inv = sum > 0.f ? 1.f / (sum * kPScale<FMT>) : 0.f;
   const size_t to = (size_t)seq * a.hq + head;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + kWave * e < a.d)
-      static_cast<uint16_t*>(a.out)[to * a.d + lane + kWave * e] = (uint16_t)pack2<DT>(x[e] * inv, 0.f);
-  if (lane == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + at) =
+      make_uint2(pack2<DT>(y.x * inv, y.y * inv), pack2<DT>(y.z * inv, y.w * inv));
+  if (threadIdx.x == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
 }
 
 template <int DT, int FMT, int DP>
 hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
   const int units = spa_check::decode_units(a.n_seqs, a.hq, a.hkv);
-  hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), dim3(units, a.hkv * a.head_tiles), dim3(kWaves * kWave), 0, st, a);
+  const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
+  if (a.page.d % 16 == 0 && a.d == DP) hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), grid, block, 0, st, a);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_attention_decode_join<DT, FMT>), dim3(a.n_seqs * a.hq), dim3(kWave), 0, st, a);
+  // a table that holds no more than the shortest piece cannot be cut
+  if ((int64_t)a.max_pages * a.page.d <= kMinTiles * kTile) return hipSuccess;
+  hipLaunchKernelGGL((k_attention_decode_join<DT, FMT>), dim3(a.n_seqs * a.hq), dim3(kJoinRuns * kJoinCols), 0, st, a);
   return hipGetLastError();
 }
 template <int DT, int FMT>

@@ -17,7 +17,7 @@ constexpr int32_t kMaxHeadDim = 256;
 constexpr int32_t kMaxRows = 1 << 30;             // packed rows of a call
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 23;  // elements between rows: 64 rows of it stay below 2^31 bytes
-constexpr int64_t kMaxDecodeRows = int64_t(1) << 25;   // (sequence, query head) pairs: a wave of the join each
+constexpr int64_t kMaxDecodeRows = int64_t(1) << 23;   // (sequence, query head) pairs: a workgroup of the join each
 constexpr int32_t kMaxNormC = 1 << 16;            // channels a workgroup holds in registers
 
 inline bool valid_heads(const spa_heads* h) { return h && h->data; }
