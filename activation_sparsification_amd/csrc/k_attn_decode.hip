@@ -13,6 +13,8 @@
 // there are about 1024 workgroups whatever the lengths; the cut is computed by every workgroup from the lengths
 // on the device.  Pieces leave unnormalised float32 sums with their maximum, and a second kernel joins them in
 // a fixed order.
+#include <algorithm>
+
 #include "spa_attn.h"
 #include "spa_check_layer.h"
 #include "spa_layer.h"
@@ -38,6 +40,7 @@ struct DecodeAttnArgs {
   float* lse;
   float* part_o;             // [units][n_q_heads][d]
   float2* part_ml;           // [units][n_q_heads]
+  int2* part_of;             // [n_seqs]: a sequence's first unit and its number of pieces
   int n_seqs, hq, hkv, group, d, n_pages, max_pages, head_tiles;
   int target;                // pieces wanted over all sequences
   float c;                   // scale * log2 e
@@ -93,6 +96,7 @@ __device__ __forceinline__ bool find_piece(const DecodeAttnArgs& a, Piece& p) {
   p.begin = min(piece * even, tiles);
   p.end = min(p.begin + even, tiles);
   p.whole = n == 1;
+  if (piece == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.part_of[p.seq] = make_int2(blockIdx.x, n);
   return true;
 }
 
@@ -155,6 +159,29 @@ __device__ __forceinline__ void load_q(const DecodeAttnArgs& a, const Piece& p, 
     const int at = q_at<FMT>(c, g);
     qf[c] = make_uint4(0, 0, 0, 0);
     if (col < p.heads && at < a.d) qf[c] = *reinterpret_cast<const uint4*>(q + at);
+  }
+}
+
+// 16 bytes, or a lane's share of a value row, that are read once.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint4 stream_load16(const void* p) {
+  const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <int W>
+__device__ __forceinline__ void stream_load(const char* p, uint32_t (&w)[W]) {
+  if constexpr (W == 1) {
+    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (W == 2) {
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+    w[0] = v[0]; w[1] = v[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = stream_load16(p + 4 * i);
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
   }
 }
 
@@ -361,7 +388,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
     for (int b = 0; b < 2; ++b) {
       const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (DP * ES);
 #pragma unroll
-      for (int c = 0; c < KL; ++c) kr[b][c] = *reinterpret_cast<const uint4*>(base + (k_lane + 64 * c));
+      for (int c = 0; c < KL; ++c) kr[b][c] = stream_load16(base + (k_lane + 64 * c));
       if constexpr (FMT != SPA_KV_NATIVE) {
         ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
         vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
@@ -384,9 +411,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (DP * ES);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(base + (v_lane + (j % 4) * DP * ES));
-#pragma unroll
-      for (int i = 0; i < VW; ++i) vraw[j][i] = w[i];
+      stream_load<VW>(base + (v_lane + (j % 4) * DP * ES), vraw[j]);
     }
     // scores
     f32x4 s[2];
@@ -461,92 +486,93 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
 #pragma unroll
           for (int i = 0; i < VW; ++i) vraw[j][i] = 0;
     }
-    uint32_t vr[8][NV / 2];
+    // one stored word of the eight rows at a time: PW pairs of dimensions
+    constexpr int PW = 2 / ES;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) widen_row<DT, FMT, NV>(vraw[j], vr[j]);
+    for (int i = 0; i < VW; ++i) {
+      uint32_t vr[8][PW];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
-      uint4 vf;
-      vf.x = __builtin_amdgcn_perm(vr[1][i / 2], vr[0][i / 2], sel);
-      vf.y = __builtin_amdgcn_perm(vr[3][i / 2], vr[2][i / 2], sel);
-      vf.z = __builtin_amdgcn_perm(vr[5][i / 2], vr[4][i / 2], sel);
-      vf.w = __builtin_amdgcn_perm(vr[7][i / 2], vr[6][i / 2], sel);
-      o[i] = mfma16<DT>(vf, pf, o[i]);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t raw[1] = {vraw[j][i]};
+        widen_row<DT, FMT, 2 * PW, 1>(raw, vr[j]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2 * PW; ++e) {
+        const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
+        uint4 vf;
+        vf.x = __builtin_amdgcn_perm(vr[1][e / 2], vr[0][e / 2], sel);
+        vf.y = __builtin_amdgcn_perm(vr[3][e / 2], vr[2][e / 2], sel);
+        vf.z = __builtin_amdgcn_perm(vr[5][e / 2], vr[4][e / 2], sel);
+        vf.w = __builtin_amdgcn_perm(vr[7][e / 2], vr[6][e / 2], sel);
+        o[2 * PW * i + e] = mfma16<DT>(vf, pf, o[2 * PW * i + e]);
+      }
     }
   }
   finish<DT, FMT, DP>(a, p, o, m, l);
 }
 
-// One workgroup per (sequence, query head): the pieces' sums brought to their common maximum and added, eight
-// runs of pieces side by side and then the runs in order.
-constexpr int kJoinRuns = 8, kJoinCols = 32;
+// One workgroup per sequence and 1024 of its outputs: a thread takes four dimensions of one head and brings the
+// pieces' sums to their common maximum, in order.
+constexpr int kJoinThreads = 256;
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kJoinRuns * kJoinCols) k_attention_decode_join(DecodeAttnArgs a) {
-  __shared__ float4 s_x[kJoinRuns][kJoinCols][2];
-  __shared__ float s_sum[kJoinRuns];
-  const int lane = threadIdx.x & (kWave - 1);
-  const int seq = blockIdx.x / a.hq, head = blockIdx.x % a.hq;
-  const int per = piece_tiles(a);
-  const int pieces = seq_pieces(a, seq, per);
-  if (pieces == 1) return;
-  int first = 0;
-  for (int base = 0; base < seq; base += kWave) first += base + lane < seq ? seq_pieces(a, base + lane, per) : 0;
+__global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAttnArgs a) {
+  const int2 of = a.part_of[blockIdx.x];
+  if (of.y == 1) return;
+  const int quads = a.d / 4;
+  const int at = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int head = at / quads, dim = at % quads * 4;
+  if (head >= a.hq) return;
+  const float2* ml = a.part_ml + (size_t)of.x * a.hq + head;
+  const float* po = a.part_o + ((size_t)of.x * a.hq + head) * a.d + dim;
+  const size_t o_step = (size_t)a.hq * a.d;
+  float m = -INFINITY, sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 8;
+  for (int i = 0; i < of.y; i += U) {
+    float2 s[U];
+    float4 v[U];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) first += __shfl_xor(first, off, kWave);
-  float mx = -INFINITY;
-  for (int i = lane; i < pieces; i += kWave) mx = fmaxf(mx, a.part_ml[(size_t)(first + i) * a.hq + head].x);
+    for (int u = 0; u < U; ++u) {
+      const int k = min(i + u, of.y - 1);
+      s[u] = ml[(size_t)k * a.hq];
+      v[u] = *reinterpret_cast<const float4*>(po + k * o_step);
+      if (i + u >= of.y) s[u].x = -INFINITY;
+    }
+    float now = m;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, kWave));
-  const float base = mx == -INFINITY ? 0.f : mx;
-  const int run = threadIdx.x / kJoinCols, c = threadIdx.x % kJoinCols;
-  float sum = 0.f;
-  float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i = run; i < pieces; i += kJoinRuns) {
-    const size_t row = (size_t)(first + i) * a.hq + head;
-    const float2 ml = a.part_ml[row];
-    const float f = exp2_hw(ml.x - base);
-    sum += f * ml.y;
+    for (int u = 0; u < U; ++u) now = fmaxf(now, s[u].x);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float f0 = exp2_hw(m - base);
+    m = now;
+    sum *= f0;
+    x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int at = 4 * (c + kJoinCols * e);
-      if (at < a.d) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + row * a.d + at);
-        x[e].x += f * v.x; x[e].y += f * v.y; x[e].z += f * v.z; x[e].w += f * v.w;
-      }
+    for (int u = 0; u < U; ++u) {
+      const float f = exp2_hw(s[u].x - base);
+      sum += f * s[u].y;
+      x.x += f * v[u].x; x.y += f * v[u].y; x.z += f * v[u].z; x.w += f * v[u].w;
     }
   }
-  s_x[run][c][0] = x[0];
-  s_x[run][c][1] = x[1];
-  if (c == 0) s_sum[run] = sum;
-  __syncthreads();
-  const int at = 4 * (int)threadIdx.x;
-  if (at >= a.d) return;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  sum = 0.f;
-#pragma unroll
-  for (int r = 0; r < kJoinRuns; ++r) {
-    const float4 v = s_x[r][threadIdx.x % kJoinCols][threadIdx.x / kJoinCols];
-    y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-    sum += s_sum[r];
-  }
   const float inv = sum > 0.f ? 1.f / (sum * kPScale<FMT>) : 0.f;
-  const size_t to = (size_t)seq * a.hq + head;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + at) =
-      make_uint2(pack2<DT>(y.x * inv, y.y * inv), pack2<DT>(y.z * inv, y.w * inv));
-  if (threadIdx.x == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
+  const size_t to = (size_t)blockIdx.x * a.hq + head;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) =
+      make_uint2(pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv));
+  if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (m + log2_hw(sum)) : -INFINITY;
 }
 
 template <int DT, int FMT, int DP>
 hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
-  const int units = spa_check::decode_units(a.n_seqs, a.hq, a.hkv);
+  // the most pieces the lengths can give, and no more than the table has room for
+  const int64_t room = ((int64_t)a.max_pages * a.page.d + kMinTiles * kTile - 1) / (kMinTiles * kTile);
+  const int units = (int)std::min<int64_t>(spa_check::decode_units(a.n_seqs, a.hq, a.hkv), std::max<int64_t>(room, 1) * a.n_seqs);
   const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
   if (a.page.d % 16 == 0 && a.d == DP) hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), grid, block, 0, st, a);
   if (hipError_t e = hipGetLastError()) return e;
   // a table that holds no more than the shortest piece cannot be cut
-  if ((int64_t)a.max_pages * a.page.d <= kMinTiles * kTile) return hipSuccess;
-  hipLaunchKernelGGL((k_attention_decode_join<DT, FMT>), dim3(a.n_seqs * a.hq), dim3(kJoinRuns * kJoinCols), 0, st, a);
+  if (room <= 1) return hipSuccess;
+  const int groups = (a.hq * (a.d / 4) + kJoinThreads - 1) / kJoinThreads;
+  hipLaunchKernelGGL((k_attention_decode_join<DT, FMT>), dim3(a.n_seqs, groups), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
 }
 template <int DT, int FMT>
@@ -566,13 +592,14 @@ hipError_t by_format(int fmt, const DecodeAttnArgs& a, hipStream_t st) {
 
 hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads, const spa_kv_cache& c,
                                    const int32_t* table, int max_pages, const int32_t* lens, float scale, void* out,
-                                   float* lse, float* part_o, float* part_ml, hipStream_t st) {
+                                   float* lse, float* part_o, float* part_ml, int32_t* part_of, hipStream_t st) {
   DecodeAttnArgs a{};
   a.q = static_cast<const uint16_t*>(q.data);
   a.q_row = q.row_stride; a.q_head = q.head_stride;
   a.k = c.k; a.v = c.v; a.k_scale = c.k_scale; a.v_scale = c.v_scale;
   a.table = table; a.lens = lens; a.out = out; a.lse = lse;
   a.part_o = part_o; a.part_ml = reinterpret_cast<float2*>(part_ml);
+  a.part_of = reinterpret_cast<int2*>(part_of);
   a.n_seqs = n_seqs; a.hq = n_q_heads; a.hkv = c.n_heads; a.group = n_q_heads / c.n_heads;
   a.d = c.head_dim; a.n_pages = c.n_pages; a.max_pages = max_pages;
   a.head_tiles = spa_check::head_tiles(n_q_heads, c.n_heads);

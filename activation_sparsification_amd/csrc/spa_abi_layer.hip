@@ -51,7 +51,8 @@ spa_status attention_decode(const spa_heads* q, int32_t n_seqs, int32_t n_q_head
   char* base = static_cast<char*>(workspace);
   return hip_status(spa::launch_attention_decode(*q, n_seqs, n_q_heads, *cache, page_table, max_pages, seq_lens, scale,
                                                  out, lse, reinterpret_cast<float*>(base + p.o),
-                                                 reinterpret_cast<float*>(base + p.ml), stream_of(stream)));
+                                                 reinterpret_cast<float*>(base + p.ml), reinterpret_cast<int32_t*>(base + p.of),
+                                                 stream_of(stream)));
 }
 
 size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,

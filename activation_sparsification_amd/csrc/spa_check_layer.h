@@ -17,7 +17,7 @@ constexpr int32_t kMaxHeadDim = 256;
 constexpr int32_t kMaxRows = 1 << 30;             // packed rows of a call
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 23;  // elements between rows: 64 rows of it stay below 2^31 bytes
-constexpr int64_t kMaxDecodeRows = int64_t(1) << 23;   // (sequence, query head) pairs: a workgroup of the join each
+constexpr int64_t kMaxDecodeRows = int64_t(1) << 23;   // (sequence, query head) pairs of a call
 constexpr int32_t kMaxNormC = 1 << 16;            // channels a workgroup holds in registers
 
 inline bool valid_heads(const spa_heads* h) { return h && h->data; }
@@ -98,14 +98,17 @@ inline int decode_units(int n_seqs, int n_q_heads, int n_kv_heads) {
   return n_seqs + (kDecodeTarget + per_unit - 1) / per_unit;
 }
 struct DecodeAttnPlan {
-  size_t o, ml, bytes;    // [units][heads][head_dim] float32 partial outputs, [units][heads][2] maximum and sum
+  // [units][heads][head_dim] float32 partial outputs, [units][heads][2] maximum and sum, [n_seqs][2] first unit and
+  // number of pieces
+  size_t o, ml, of, bytes;
 };
 inline DecodeAttnPlan decode_attn_plan(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
   DecodeAttnPlan p{};
   const size_t rows = (size_t)decode_units(n_seqs, n_q_heads, n_kv_heads) * n_q_heads;
   p.o = 0;
   p.ml = round256(rows * head_dim * 4);
-  p.bytes = p.ml + round256(rows * 8);
+  p.of = p.ml + round256(rows * 8);
+  p.bytes = p.of + round256((size_t)n_seqs * 8);
   return p;
 }
 

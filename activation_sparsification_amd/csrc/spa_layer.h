@@ -15,7 +15,7 @@ hipError_t launch_kv_read(const spa_kv_cache& c, const int32_t* table, int n_seq
 
 hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads, const spa_kv_cache& c,
                                    const int32_t* table, int max_pages, const int32_t* lens, float scale, void* out,
-                                   float* lse, float* part_o, float* part_ml, hipStream_t st);
+                                   float* lse, float* part_o, float* part_ml, int32_t* part_of, hipStream_t st);
 
 hipError_t launch_attention_prefill(const spa_heads& q, const spa_heads& k, const spa_heads& v, int dtype, int tq,
                                     int tk, int n_q_heads, int n_kv_heads, int head_dim, const int32_t* cu_q,
