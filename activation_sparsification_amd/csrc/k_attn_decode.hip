@@ -9,10 +9,10 @@
 //         product is free, so it is taken as S^T leaves it: lane group g holds 4g..4g+3 and 16+4g..16+4g+3).
 //         A lane reads those 8 positions' rows, 16 lanes to a row, and turns its 8 x 8 block with byte
 //         permutes into one V^T operand per dimension.
-// The running maximum and sum are one column (query head) per lane.  A sequence is cut into pieces so that
-// there are about 1024 workgroups whatever the lengths; the cut is computed by every workgroup from the lengths
-// on the device.  Pieces leave unnormalised float32 sums with their maximum, and a second kernel joins them in
-// a fixed order.
+// The running maximum and sum are one column (query head) per lane.  The tiles of all sequences, end to end, are cut
+// into equal shares, one for each workgroup of a head, whatever the lengths; every workgroup finds its share from
+// the lengths on the device.  A sequence that is cut leaves unnormalised float32 sums with their maximum, and a
+// second kernel joins them in a fixed order.
 #include <algorithm>
 
 #include "spa_attn.h"
@@ -38,11 +38,11 @@ struct DecodeAttnArgs {
   const int32_t* lens;
   void* out;
   float* lse;
-  float* part_o;             // [units][n_q_heads][d]
-  float2* part_ml;           // [units][n_q_heads]
-  int2* part_of;             // [n_seqs]: a sequence's first unit and its number of pieces
+  float* part_o;             // [2 workgroups][n_q_heads][d]
+  float2* part_ml;           // [2 workgroups][n_q_heads]
+  int2* part_of;             // [n_seqs]: a sequence's first slot and its number of pieces
   int n_seqs, hq, hkv, group, d, n_pages, max_pages, head_tiles;
-  int target;                // pieces wanted over all sequences
+  int target;                // workgroups of a head at the most
   float c;                   // scale * log2 e
   FastDiv page;
 };
@@ -57,47 +57,80 @@ __device__ __forceinline__ int seq_tiles(const DecodeAttnArgs& a, int s) {
   return (min(max(a.lens[s], 0), cap) + kTile - 1) / kTile;
 }
 
-// The most tiles of a piece, the same on every wave: total tiles over the pieces wanted.  Cutting each sequence
-// into whole pieces makes about half a piece more per sequence, which is taken off the wanted number.
-__device__ __forceinline__ int piece_tiles(const DecodeAttnArgs& a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  long long total = 0;
-  for (int base = 0; base < a.n_seqs; base += kWave) total += base + lane < a.n_seqs ? seq_tiles(a, base + lane) : 0;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off, kWave);
-  const int want = max(a.target - a.n_seqs / 2, (a.target + 3) / 4);
-  return (int)max((total + want - 1) / want, (long long)kMinTiles);
-}
-__device__ __forceinline__ int seq_pieces(const DecodeAttnArgs& a, int s, int per) {
-  return max((seq_tiles(a, s) + per - 1) / per, 1);       // an empty sequence is one piece, of nothing
-}
-
+// What a workgroup works through: `per` consecutive tiles of all sequences' tiles laid end to end, so every
+// workgroup of a head has the same share whatever the lengths.  An empty sequence stands as one tile of nothing.
+struct Span {
+  int per;
+  int seq, local;              // where the next piece starts: sequence, tile within it
+  int left;                    // tiles still to do
+  bool fresh;                  // nothing done yet
+};
 // One piece of a sequence, for one key-value head and up to 16 of its query heads.
 struct Piece {
   int seq, head, h0, heads;    // key-value head; first query head and their number
   int len;                     // positions of the sequence
   int begin, end;              // tiles
   bool whole;                  // the sequence is this piece alone
+  int slot;                    // where the piece's sums go if not: two slots to a workgroup
 };
-__device__ __forceinline__ bool find_piece(const DecodeAttnArgs& a, Piece& p) {
-  const int per = piece_tiles(a);
-  int piece;
-  locate(blockIdx.x, a.n_seqs, [&](int s) { return seq_pieces(a, s, per); }, p.seq, piece);
-  if (p.seq >= a.n_seqs) return false;
-  p.seq = __builtin_amdgcn_readfirstlane(p.seq);
-  piece = __builtin_amdgcn_readfirstlane(piece);
+__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(seq_tiles(a, s), 1); }
+
+__device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int c0 = lane < a.n_seqs ? seq_share(a, lane) : 0;
+  const int incl0 = wave_scan(c0);
+  long long total = __builtin_amdgcn_readlane(incl0, kWave - 1);
+  for (int base = kWave; base < a.n_seqs; base += kWave) {
+    long long c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) c += __shfl_xor(c, off, kWave);
+    total += c;
+  }
+  const int per = (int)max((total + a.target - 1) / a.target, (long long)kMinTiles);
+  const long long start = (long long)blockIdx.x * per;
+  if (start >= total) return false;
+  long long before = 0;
+  int c = c0, incl = incl0, base = 0;
+  uint64_t past;
+  while (!(past = __ballot(before + incl > start))) {          // ends: start is below the total
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    base += kWave;
+    c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
+    incl = wave_scan(c);
+  }
+  const int at = __ffsll((unsigned long long)past) - 1;
+  s.per = per;
+  s.seq = base + at;
+  s.local = (int)(start - before) - __builtin_amdgcn_readlane(incl - c, at);
+  s.left = (int)min((long long)per, total - start);
+  s.fresh = true;
+  return true;
+}
+
+__device__ __forceinline__ Piece next_piece(const DecodeAttnArgs& a, Span& s) {
+  Piece p;
+  p.seq = s.seq;
   const int ht = blockIdx.y / a.hkv;
   p.head = blockIdx.y % a.hkv;
   p.heads = min(a.group - 16 * ht, 16);
   p.h0 = p.head * a.group + 16 * ht;
-  p.len = min(max(a.lens[p.seq], 0), a.max_pages * (int)a.page.d);
-  const int tiles = (p.len + kTile - 1) / kTile, n = seq_pieces(a, p.seq, per);
-  const int even = (tiles + n - 1) / n;
-  p.begin = min(piece * even, tiles);
-  p.end = min(p.begin + even, tiles);
-  p.whole = n == 1;
-  if (piece == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.part_of[p.seq] = make_int2(blockIdx.x, n);
-  return true;
+  p.len = min(max(a.lens[s.seq], 0), a.max_pages * (int)a.page.d);
+  const int tiles = (p.len + kTile - 1) / kTile, share = max(tiles, 1);
+  const int take = min(share - s.local, s.left);
+  p.begin = s.local;
+  p.end = min(s.local + take, tiles);
+  p.whole = take == share;
+  // a piece that starts inside its sequence is its workgroup's first, one that ends inside its last
+  p.slot = 2 * blockIdx.x + (s.local == 0 && !s.fresh);
+  if (s.local == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    const int more = share - take;                              // tiles in the workgroups after this one
+    a.part_of[p.seq] = make_int2(p.slot, 1 + (more + s.per - 1) / s.per);
+  }
+  s.left -= take;
+  ++s.seq;
+  s.local = 0;
+  s.fresh = false;
+  return p;
 }
 
 // Four 8-bit codes as two words of 16-bit values (exact in both types: e4m3 has 4 significant bits, int8 7).
@@ -223,11 +256,12 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
       if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
     } else {
-      const size_t to = (size_t)blockIdx.x * a.hq + p.h0 + h;
+      const size_t to = (size_t)p.slot * a.hq + p.h0 + h;
       *reinterpret_cast<float2*>(a.part_o + to * a.d + dim) = make_float2(x0, x1);
       if (dim == 0) a.part_ml[to] = make_float2(mx, sum);
     }
   }
+  __syncthreads();      // the next piece writes here again
 }
 
 // Any page size and head_dim: a lane finds one position's cell and the others get it by lane exchange.
@@ -237,105 +271,108 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
   constexpr int NV = DP / 16;      // dimensions of V a lane holds
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int col = lane & 15, g = lane >> 4;
-  Piece p;
-  if (!find_piece(a, p)) return;
-  uint4 qf[KC];
-  load_q<FMT, KC>(a, p, col, g, qf);
+  Span span;
+  if (!find_span(a, span)) return;
+  do {
+    const Piece p = next_piece(a, span);
+    uint4 qf[KC];
+    load_q<FMT, KC>(a, p, col, g, qf);
 
-  f32x4 o[NV];
+    f32x4 o[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
 
-  for (int tile = p.begin + wave; tile < p.end; tile += kWaves) {
-    // lane i < 32 finds position i's cell; a position that does not count is bit i of `gone`
-    const int pos = tile * kTile + (lane & 31);
-    const int p0 = min(pos, p.len - 1);
-    const int pc = (int)a.page.div((uint32_t)p0);
-    const int pg = a.table[(size_t)p.seq * a.max_pages + pc];
-    const bool ok = pg >= 0 && pg < a.n_pages;
-    const int cell = ok ? (pg * a.hkv + p.head) * (int)a.page.d + (p0 - pc * (int)a.page.d) : 0;
-    const uint32_t gone = (uint32_t)__ballot(pos >= p.len || !ok);
-    const uint32_t bad = (uint32_t)__ballot(!ok);            // its cell is not the sequence's: the values are dropped
-    float ksc = 1.f, vsc = 1.f;
-    if constexpr (FMT != SPA_KV_NATIVE) {
-      ksc = a.k_scale[cell];
-      vsc = ok ? a.v_scale[cell] : 0.f;
-    }
-    float t[2][4];
+    for (int tile = p.begin + wave; tile < p.end; tile += kWaves) {
+      // lane i < 32 finds position i's cell; a position that does not count is bit i of `gone`
+      const int pos = tile * kTile + (lane & 31);
+      const int p0 = min(pos, p.len - 1);
+      const int pc = (int)a.page.div((uint32_t)p0);
+      const int pg = a.table[(size_t)p.seq * a.max_pages + pc];
+      const bool ok = pg >= 0 && pg < a.n_pages;
+      const int cell = ok ? (pg * a.hkv + p.head) * (int)a.page.d + (p0 - pc * (int)a.page.d) : 0;
+      const uint32_t gone = (uint32_t)__ballot(pos >= p.len || !ok);
+      const uint32_t bad = (uint32_t)__ballot(!ok);            // its cell is not the sequence's: the values are dropped
+      float ksc = 1.f, vsc = 1.f;
+      if constexpr (FMT != SPA_KV_NATIVE) {
+        ksc = a.k_scale[cell];
+        vsc = ok ? a.v_scale[cell] : 0.f;
+      }
+      float t[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const size_t kc = (size_t)(uint32_t)__shfl(cell, 16 * b + col, kWave);
-      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < 2; ++b) {
+        const size_t kc = (size_t)(uint32_t)__shfl(cell, 16 * b + col, kWave);
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const int at = q_at<FMT>(c, g);
-        uint4 kf = make_uint4(0, 0, 0, 0);
-        if (at < a.d) {
-          if constexpr (FMT == SPA_KV_NATIVE)
-            kf = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + kc * a.d + at);
-          else
-            kf = widen8<DT, FMT>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k) + kc * a.d + at));
+        for (int c = 0; c < KC; ++c) {
+          const int at = q_at<FMT>(c, g);
+          uint4 kf = make_uint4(0, 0, 0, 0);
+          if (at < a.d) {
+            if constexpr (FMT == SPA_KV_NATIVE)
+              kf = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + kc * a.d + at);
+            else
+              kf = widen8<DT, FMT>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k) + kc * a.d + at));
+          }
+          s = mfma16<DT>(kf, qf[c], s);
         }
-        s = mfma16<DT>(kf, qf[c], s);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * b + 4 * g + r;
+          float x = s[r] * a.c;
+          if constexpr (FMT != SPA_KV_NATIVE) x *= __shfl(ksc, i, kWave);
+          t[b][r] = (gone >> i) & 1u ? -INFINITY : x;
+        }
+      }
+      float mx = m;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, t[b][r]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+      const float base = mx == -INFINITY ? 0.f : mx;           // nothing seen yet: every p is 0
+      const float alpha = exp2_hw(m - base);
+      m = mx;
+      l *= alpha;
+      float w[8];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float e = exp2_hw(t[b][r] - base);
+          l += e;
+          if constexpr (FMT != SPA_KV_NATIVE) e *= __shfl(vsc, 16 * b + 4 * g + r, kWave) * kPScale<FMT>;
+          w[4 * b + r] = e;
+        }
+      const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
+      uint32_t vr[8][NV / 2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = (j < 4 ? 4 * g + j : 16 + 4 * g + j - 4);
+        const size_t vc = (size_t)(uint32_t)__shfl(cell, i, kWave);
+        constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1, VW = NV * ES / 4;
+        uint32_t raw[VW];
+        const bool live = NV * col < a.d && !((bad >> i) & 1u);
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.v) + (vc * a.d + NV * col) * ES);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) raw[e] = live && NV * col + 4 / ES * e < a.d ? at[e] : 0u;
+        widen_row<DT, FMT, NV>(raw, vr[j]);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * b + 4 * g + r;
-        float x = s[r] * a.c;
-        if constexpr (FMT != SPA_KV_NATIVE) x *= __shfl(ksc, i, kWave);
-        t[b][r] = (gone >> i) & 1u ? -INFINITY : x;
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
+        uint4 vf;
+        vf.x = __builtin_amdgcn_perm(vr[1][i / 2], vr[0][i / 2], sel);
+        vf.y = __builtin_amdgcn_perm(vr[3][i / 2], vr[2][i / 2], sel);
+        vf.z = __builtin_amdgcn_perm(vr[5][i / 2], vr[4][i / 2], sel);
+        vf.w = __builtin_amdgcn_perm(vr[7][i / 2], vr[6][i / 2], sel);
+        o[i] *= alpha;
+        o[i] = mfma16<DT>(vf, pf, o[i]);
       }
     }
-    float mx = m;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, t[b][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-    const float base = mx == -INFINITY ? 0.f : mx;           // nothing seen yet: every p is 0
-    const float alpha = exp2_hw(m - base);
-    m = mx;
-    l *= alpha;
-    float w[8];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float e = exp2_hw(t[b][r] - base);
-        l += e;
-        if constexpr (FMT != SPA_KV_NATIVE) e *= __shfl(vsc, 16 * b + 4 * g + r, kWave) * kPScale<FMT>;
-        w[4 * b + r] = e;
-      }
-    const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
-    uint32_t vr[8][NV / 2];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = (j < 4 ? 4 * g + j : 16 + 4 * g + j - 4);
-      const size_t vc = (size_t)(uint32_t)__shfl(cell, i, kWave);
-      constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1, VW = NV * ES / 4;
-      uint32_t raw[VW];
-      const bool live = NV * col < a.d && !((bad >> i) & 1u);
-      const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.v) + (vc * a.d + NV * col) * ES);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) raw[e] = live && NV * col + 4 / ES * e < a.d ? at[e] : 0u;
-      widen_row<DT, FMT, NV>(raw, vr[j]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
-      uint4 vf;
-      vf.x = __builtin_amdgcn_perm(vr[1][i / 2], vr[0][i / 2], sel);
-      vf.y = __builtin_amdgcn_perm(vr[3][i / 2], vr[2][i / 2], sel);
-      vf.z = __builtin_amdgcn_perm(vr[5][i / 2], vr[4][i / 2], sel);
-      vf.w = __builtin_amdgcn_perm(vr[7][i / 2], vr[6][i / 2], sel);
-      o[i] *= alpha;
-      o[i] = mfma16<DT>(vf, pf, o[i]);
-    }
-  }
 
-  finish<DT, FMT, DP>(a, p, o, m, l);
+    finish<DT, FMT, DP>(a, p, o, m, l);
+  } while (span.left > 0);
 }
 
 // Pages of whole 16-position blocks and head_dim == DP: a block's rows are consecutive, so a tile has two bases that
@@ -351,164 +388,167 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, g = lane >> 4;
-  Piece p;
-  if (!find_piece(a, p)) return;
-  uint4 qf[KC];
-  load_q<FMT, KC>(a, p, col, g, qf);
+  Span span;
+  if (!find_span(a, span)) return;
+  do {
+    const Piece p = next_piece(a, span);
+    uint4 qf[KC];
+    load_q<FMT, KC>(a, p, col, g, qf);
 
-  f32x4 o[NV];
+    f32x4 o[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
 
-  const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
-  int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
-  auto fetch_pages = [&](int it) {
-    const int block = (first + kWaves * (it + lane / 2)) * 2 + (lane & 1);
-    const int at = block * 16;
-    pages = -1;
-    if (at < p.len) {
-      pages = a.table[(size_t)p.seq * a.max_pages + a.page.div((uint32_t)at)];
-      if (pages >= a.n_pages) pages = -1;
-    }
-  };
-  // the first cell of block b of tile number `it`, and whether its page is there (else cell 0 of the cache)
-  auto base_of = [&](int it, int b, bool& there) {
-    const int pg = __builtin_amdgcn_readlane(pages, 2 * (it % kBatch) + b);
-    const uint32_t at = (uint32_t)((first + kWaves * it) * 2 + b) * 16;
-    there = pg >= 0;
-    const uint32_t cell = ((uint32_t)pg * a.hkv + p.head) * a.page.d + (at - a.page.div(at) * a.page.d);
-    return there ? cell : 0u;
-  };
-  uint4 kr[2][KL];
-  float4 ksc[2], vsc[2];
-  const uint32_t k_lane = (uint32_t)(col * DP * ES + 16 * g), v_lane = (uint32_t)((4 * g * DP + NV * col) * ES);
-  auto load_k = [&](const uint32_t (&cell)[2]) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (DP * ES);
-#pragma unroll
-      for (int c = 0; c < KL; ++c) kr[b][c] = stream_load16(base + (k_lane + 64 * c));
-      if constexpr (FMT != SPA_KV_NATIVE) {
-        ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
-        vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
+    const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
+    int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
+    auto fetch_pages = [&](int it) {
+      const int block = (first + kWaves * (it + lane / 2)) * 2 + (lane & 1);
+      const int at = block * 16;
+      pages = -1;
+      if (at < p.len) {
+        pages = a.table[(size_t)p.seq * a.max_pages + a.page.div((uint32_t)at)];
+        if (pages >= a.n_pages) pages = -1;
       }
-    }
-  };
+    };
+    // the first cell of block b of tile number `it`, and whether its page is there (else cell 0 of the cache)
+    auto base_of = [&](int it, int b, bool& there) {
+      const int pg = __builtin_amdgcn_readlane(pages, 2 * (it % kBatch) + b);
+      const uint32_t at = (uint32_t)((first + kWaves * it) * 2 + b) * 16;
+      there = pg >= 0;
+      const uint32_t cell = ((uint32_t)pg * a.hkv + p.head) * a.page.d + (at - a.page.div(at) * a.page.d);
+      return there ? cell : 0u;
+    };
+    uint4 kr[2][KL];
+    float4 ksc[2], vsc[2];
+    const uint32_t k_lane = (uint32_t)(col * DP * ES + 16 * g), v_lane = (uint32_t)((4 * g * DP + NV * col) * ES);
+    auto load_k = [&](const uint32_t (&cell)[2]) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (DP * ES);
+#pragma unroll
+        for (int c = 0; c < KL; ++c) kr[b][c] = stream_load16(base + (k_lane + 64 * c));
+        if constexpr (FMT != SPA_KV_NATIVE) {
+          ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
+          vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
+        }
+      }
+    };
 
-  uint32_t cell[2];
-  bool there[2] = {true, true};
-  if (n > 0) {
-    fetch_pages(0);
+    uint32_t cell[2];
+    bool there[2] = {true, true};
+    if (n > 0) {
+      fetch_pages(0);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) cell[b] = base_of(0, b, there[b]);
-    load_k(cell);
-  }
-  for (int it = 0; it < n; ++it) {
-    const int tile = first + kWaves * it;
-    // values of this tile
-    uint32_t vraw[8][VW];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (DP * ES);
-      stream_load<VW>(base + (v_lane + (j % 4) * DP * ES), vraw[j]);
+      for (int b = 0; b < 2; ++b) cell[b] = base_of(0, b, there[b]);
+      load_k(cell);
     }
-    // scores
-    f32x4 s[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        uint4 kf;
-        if constexpr (FMT == SPA_KV_NATIVE) kf = kr[b][c];
-        else kf = widen8<DT, FMT>(c % 2 ? make_uint2(kr[b][c / 2].z, kr[b][c / 2].w) : make_uint2(kr[b][c / 2].x, kr[b][c / 2].y));
-        s[b] = mfma16<DT>(kf, qf[c], s[b]);
-      }
-    }
-    float t[8], vs[8];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const float kq[4] = {ksc[b].x, ksc[b].y, ksc[b].z, ksc[b].w}, vq[4] = {vsc[b].x, vsc[b].y, vsc[b].z, vsc[b].w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        t[4 * b + r] = s[b][r] * a.c;
-        if constexpr (FMT != SPA_KV_NATIVE) t[4 * b + r] *= kq[r];
-        vs[4 * b + r] = FMT != SPA_KV_NATIVE ? vq[r] * kPScale<FMT> : 1.f;
-      }
-    }
-    // the last tile's end and absent pages: what does not count is removed from the scores, the values and their scales
-    const bool cut = (tile + 1) * kTile > p.len || !there[0] || !there[1];
-    uint32_t gone = 0;
-    if (cut) {
+    for (int it = 0; it < n; ++it) {
+      const int tile = first + kWaves * it;
+      // values of this tile
+      uint32_t vraw[8][VW];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int pos = tile * kTile + 16 * (j / 4) + 4 * g + j % 4;
-        if (pos >= p.len || !there[j / 4]) {
-          gone |= 1u << j;
-          t[j] = -INFINITY;
-          vs[j] = 0.f;
+        const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (DP * ES);
+        stream_load<VW>(base + (v_lane + (j % 4) * DP * ES), vraw[j]);
+      }
+      // scores
+      f32x4 s[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          uint4 kf;
+          if constexpr (FMT == SPA_KV_NATIVE) kf = kr[b][c];
+          else kf = widen8<DT, FMT>(c % 2 ? make_uint2(kr[b][c / 2].z, kr[b][c / 2].w) : make_uint2(kr[b][c / 2].x, kr[b][c / 2].y));
+          s[b] = mfma16<DT>(kf, qf[c], s[b]);
+        }
+      }
+      float t[8], vs[8];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float kq[4] = {ksc[b].x, ksc[b].y, ksc[b].z, ksc[b].w}, vq[4] = {vsc[b].x, vsc[b].y, vsc[b].z, vsc[b].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          t[4 * b + r] = s[b][r] * a.c;
+          if constexpr (FMT != SPA_KV_NATIVE) t[4 * b + r] *= kq[r];
+          vs[4 * b + r] = FMT != SPA_KV_NATIVE ? vq[r] * kPScale<FMT> : 1.f;
+        }
+      }
+      // the last tile's end and absent pages: what does not count is removed from the scores, the values and their scales
+      const bool cut = (tile + 1) * kTile > p.len || !there[0] || !there[1];
+      uint32_t gone = 0;
+      if (cut) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int pos = tile * kTile + 16 * (j / 4) + 4 * g + j % 4;
+          if (pos >= p.len || !there[j / 4]) {
+            gone |= 1u << j;
+            t[j] = -INFINITY;
+            vs[j] = 0.f;
+          }
+        }
+      }
+      // keys of the next tile
+      if (it + 1 < n) {
+        if ((it + 1) % kBatch == 0) fetch_pages(it + 1);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) cell[b] = base_of(it + 1, b, there[b]);
+        load_k(cell);
+      }
+      // softmax
+      float mx = t[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mx = fmaxf(mx, t[j]);
+      mx = across_groups_max(mx);
+      if (__any(mx > m)) {
+        const float now = fmaxf(m, mx), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+        m = now;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[i] *= alpha;
+      }
+      const float base = m == -INFINITY ? 0.f : m;           // nothing seen yet: every weight is 0
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = exp2_hw(t[j] - base);
+        l += w[j];
+        if constexpr (FMT != SPA_KV_NATIVE) w[j] *= vs[j];
+      }
+      const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
+      if (cut) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((gone >> j) & 1u)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vraw[j][i] = 0;
+      }
+      // one stored word of the eight rows at a time: PW pairs of dimensions
+      constexpr int PW = 2 / ES;
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        uint32_t vr[8][PW];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t raw[1] = {vraw[j][i]};
+          widen_row<DT, FMT, 2 * PW, 1>(raw, vr[j]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2 * PW; ++e) {
+          const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
+          uint4 vf;
+          vf.x = __builtin_amdgcn_perm(vr[1][e / 2], vr[0][e / 2], sel);
+          vf.y = __builtin_amdgcn_perm(vr[3][e / 2], vr[2][e / 2], sel);
+          vf.z = __builtin_amdgcn_perm(vr[5][e / 2], vr[4][e / 2], sel);
+          vf.w = __builtin_amdgcn_perm(vr[7][e / 2], vr[6][e / 2], sel);
+          o[2 * PW * i + e] = mfma16<DT>(vf, pf, o[2 * PW * i + e]);
         }
       }
     }
-    // keys of the next tile
-    if (it + 1 < n) {
-      if ((it + 1) % kBatch == 0) fetch_pages(it + 1);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) cell[b] = base_of(it + 1, b, there[b]);
-      load_k(cell);
-    }
-    // softmax
-    float mx = t[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) mx = fmaxf(mx, t[j]);
-    mx = across_groups_max(mx);
-    if (__any(mx > m)) {
-      const float now = fmaxf(m, mx), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
-      m = now;
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) o[i] *= alpha;
-    }
-    const float base = m == -INFINITY ? 0.f : m;           // nothing seen yet: every weight is 0
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = exp2_hw(t[j] - base);
-      l += w[j];
-      if constexpr (FMT != SPA_KV_NATIVE) w[j] *= vs[j];
-    }
-    const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
-    if (cut) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((gone >> j) & 1u)
-#pragma unroll
-          for (int i = 0; i < VW; ++i) vraw[j][i] = 0;
-    }
-    // one stored word of the eight rows at a time: PW pairs of dimensions
-    constexpr int PW = 2 / ES;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) {
-      uint32_t vr[8][PW];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t raw[1] = {vraw[j][i]};
-        widen_row<DT, FMT, 2 * PW, 1>(raw, vr[j]);
-      }
-#pragma unroll
-      for (int e = 0; e < 2 * PW; ++e) {
-        const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
-        uint4 vf;
-        vf.x = __builtin_amdgcn_perm(vr[1][e / 2], vr[0][e / 2], sel);
-        vf.y = __builtin_amdgcn_perm(vr[3][e / 2], vr[2][e / 2], sel);
-        vf.z = __builtin_amdgcn_perm(vr[5][e / 2], vr[4][e / 2], sel);
-        vf.w = __builtin_amdgcn_perm(vr[7][e / 2], vr[6][e / 2], sel);
-        o[2 * PW * i + e] = mfma16<DT>(vf, pf, o[2 * PW * i + e]);
-      }
-    }
-  }
-  finish<DT, FMT, DP>(a, p, o, m, l);
+    finish<DT, FMT, DP>(a, p, o, m, l);
+  } while (span.left > 0);
 }
 
 // One workgroup per sequence and 1024 of its outputs: a thread takes four dimensions of one head and brings the
@@ -522,9 +562,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
   const int at = blockIdx.y * kJoinThreads + threadIdx.x;
   const int head = at / quads, dim = at % quads * 4;
   if (head >= a.hq) return;
-  const float2* ml = a.part_ml + (size_t)of.x * a.hq + head;
-  const float* po = a.part_o + ((size_t)of.x * a.hq + head) * a.d + dim;
-  const size_t o_step = (size_t)a.hq * a.d;
+  const int next = of.x & ~1;                  // piece k > 0 is in the first slot of the k-th workgroup after
   float m = -INFINITY, sum = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int U = 8;
@@ -534,8 +572,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = min(i + u, of.y - 1);
-      s[u] = ml[(size_t)k * a.hq];
-      v[u] = *reinterpret_cast<const float4*>(po + k * o_step);
+      const size_t row = (size_t)(k ? next + 2 * k : of.x) * a.hq + head;
+      s[u] = a.part_ml[row];
+      v[u] = *reinterpret_cast<const float4*>(a.part_o + row * a.d + dim);
       if (i + u >= of.y) s[u].x = -INFINITY;
     }
     float now = m;
@@ -562,15 +601,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
 
 template <int DT, int FMT, int DP>
 hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
-  // the most pieces the lengths can give, and no more than the table has room for
-  const int64_t room = ((int64_t)a.max_pages * a.page.d + kMinTiles * kTile - 1) / (kMinTiles * kTile);
-  const int units = (int)std::min<int64_t>(spa_check::decode_units(a.n_seqs, a.hq, a.hkv), std::max<int64_t>(room, 1) * a.n_seqs);
+  // no more workgroups than the table has room for
+  const int64_t room = ((int64_t)a.max_pages * a.page.d + kTile - 1) / kTile;
+  const int units = (int)std::min<int64_t>(a.target, (std::max<int64_t>(room, 1) * a.n_seqs + kMinTiles - 1) / kMinTiles);
   const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
   if (a.page.d % 16 == 0 && a.d == DP) hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), grid, block, 0, st, a);
   if (hipError_t e = hipGetLastError()) return e;
-  // a table that holds no more than the shortest piece cannot be cut
-  if (room <= 1) return hipSuccess;
+  // one workgroup to a head cuts nothing
+  if (units == 1) return hipSuccess;
   const int groups = (a.hq * (a.d / 4) + kJoinThreads - 1) / kJoinThreads;
   hipLaunchKernelGGL((k_attention_decode_join<DT, FMT>), dim3(a.n_seqs, groups), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
@@ -603,7 +642,7 @@ hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads
   a.n_seqs = n_seqs; a.hq = n_q_heads; a.hkv = c.n_heads; a.group = n_q_heads / c.n_heads;
   a.d = c.head_dim; a.n_pages = c.n_pages; a.max_pages = max_pages;
   a.head_tiles = spa_check::head_tiles(n_q_heads, c.n_heads);
-  a.target = spa_check::decode_units(n_seqs, n_q_heads, c.n_heads) - n_seqs;
+  a.target = spa_check::decode_groups(n_q_heads, c.n_heads);
   a.c = scale * kLog2e;
   a.page = FastDiv((uint32_t)c.page_size);
   return c.dtype == SPA_F16 ? by_format<SPA_F16>(c.format, a, st) : by_format<SPA_BF16>(c.format, a, st);

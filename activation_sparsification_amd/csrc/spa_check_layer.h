@@ -17,6 +17,7 @@ constexpr int32_t kMaxHeadDim = 256;
 constexpr int32_t kMaxRows = 1 << 30;             // packed rows of a call
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 23;  // elements between rows: 64 rows of it stay below 2^31 bytes
+constexpr int64_t kMaxPositions = int64_t(1) << 29;    // of one sequence's table: 64 sequences' tiles add up in 31 bits
 constexpr int64_t kMaxDecodeRows = int64_t(1) << 23;   // (sequence, query head) pairs of a call
 constexpr int32_t kMaxNormC = 1 << 16;            // channels a workgroup holds in registers
 
@@ -83,28 +84,28 @@ inline spa_status check_attention_decode(const spa_heads* q, int32_t n_seqs, int
   if (!valid_heads(q) || !valid_strides(q) || !lens || !out || !aligned16(out)) return SPA_ERR_INVALID;
   if (max_pages > 0 && !table) return SPA_ERR_INVALID;
   if (s != SPA_OK) return s;
-  if ((int64_t)max_pages * c->page_size > INT32_MAX - 64) return SPA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * c->page_size > kMaxPositions) return SPA_ERR_UNSUPPORTED;
   if ((int64_t)n_seqs * n_q_heads > kMaxDecodeRows) return SPA_ERR_UNSUPPORTED;
   return built_heads(q) ? SPA_OK : SPA_ERR_UNSUPPORTED;
 }
 
 // Query heads of one key-value head are worked on 16 at a time (the matrix instruction's columns).
 inline int head_tiles(int n_q_heads, int n_kv_heads) { return (n_q_heads / n_kv_heads + 15) / 16; }
-// Work units (pieces of a sequence's cache) a decode call can have: the device cuts the sequences into
-// pieces so that there are about kDecodeTarget workgroups, at least one piece for each sequence.
-constexpr int kDecodeTarget = 1024;
-inline int decode_units(int n_seqs, int n_q_heads, int n_kv_heads) {
+// Workgroups that share the cache of one key-value head and head tile: together about kDecodeTarget, so that all
+// of them are on the chip at once (two to each compute unit).
+constexpr int kDecodeTarget = 512;
+inline int decode_groups(int n_q_heads, int n_kv_heads) {
   const int per_unit = n_kv_heads * head_tiles(n_q_heads, n_kv_heads);
-  return n_seqs + (kDecodeTarget + per_unit - 1) / per_unit;
+  return (kDecodeTarget + per_unit - 1) / per_unit;
 }
 struct DecodeAttnPlan {
-  // [units][heads][head_dim] float32 partial outputs, [units][heads][2] maximum and sum, [n_seqs][2] first unit and
-  // number of pieces
+  // [2 groups][heads][head_dim] float32 partial outputs, [2 groups][heads][2] maximum and sum, [n_seqs][2] first slot
+  // and number of pieces
   size_t o, ml, of, bytes;
 };
 inline DecodeAttnPlan decode_attn_plan(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
   DecodeAttnPlan p{};
-  const size_t rows = (size_t)decode_units(n_seqs, n_q_heads, n_kv_heads) * n_q_heads;
+  const size_t rows = (size_t)2 * decode_groups(n_q_heads, n_kv_heads) * n_q_heads;
   p.o = 0;
   p.ml = round256(rows * head_dim * 4);
   p.of = p.ml + round256(rows * 8);
