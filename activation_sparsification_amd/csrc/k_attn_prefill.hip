@@ -20,6 +20,11 @@ constexpr int kThreads = 256;
 constexpr int kWaveRows = 32;
 constexpr int kBM = kThreads / kWave * kWaveRows;
 
+// The sums are kept relative to a reference that follows the running maximum only when that has risen by more than
+// a factor of 2^kSlack for some row of the wave: weights then reach 2^8 at most, which both 16-bit types hold with
+// their full precision, and the 64 multiplications per lane of a rescale are rare after the first tiles.
+constexpr float kSlack = 8.f;
+
 struct PrefillAttnArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -93,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   const int m_last = min(m0 + kBM, lq) - 1;
   const int k_end = a.causal ? clamp_to(m_last + shift + 1, 0, lk) : lk;                 // the workgroup's
   const int full = a.causal ? clamp_to(m0 + wave * kWaveRows + shift + 1, 0, lk) : lk;   // keys that all rows see
+  const int wave_end = a.causal ? clamp_to(m0 + wave * kWaveRows + kWaveRows + shift, 0, lk) : lk;   // keys that any sees
 
   uint4 qf[KS];
   {
@@ -138,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
     wait_vm<0>(0);
     bare_barrier();
     if (j0 + BN < k_end) stage(j0 + BN, buf ^ 1);
+    if (j0 >= wave_end) continue;        // every row of this wave ends before this tile
     const char* ks = s_kv + buf * 2 * kTileBytes;
     const char* vs = ks + kTileBytes;
 
@@ -166,11 +173,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-    mx = fmaxf(mx * a.c, m);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    const float alpha = exp2_hw(m - base);
-    m = mx;
+    mx = fmaxf(mx, __shfl_xor(mx, 32, kWave)) * a.c;
+    if (__any(mx > m + kSlack)) {
+      const float now = fmaxf(mx, m), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+      m = now;
+      l *= alpha;
+#pragma unroll
+      for (int b = 0; b < DB; ++b) o[b] *= alpha;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -179,9 +190,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
         s[b][r] = exp2_hw(fmaf(s[b][r], a.c, -base));
         sum += s[b][r];
       }
-    l = l * alpha + sum;
-#pragma unroll
-    for (int b = 0; b < DB; ++b) o[b] *= alpha;
+    l += sum;
 #pragma unroll
     for (int t = 0; t < BN / 16; ++t) {
       const f32x16& p = s[t / 2];
