@@ -34,7 +34,10 @@ struct PrefillAttnArgs {
   const int32_t* cu_k;
   uint16_t* out;
   float* lse;
+  float* part_o;             // splits > 1: [splits][tq][hq][d]
+  float2* part_ml;           // splits > 1: [splits][tq][hq]
   int tq, tk, hq, hkv, group, d, n_seqs, causal;
+  int splits;                // pieces of a tile's keys at the most
   float c;                   // scale * log2 e
 };
 
@@ -53,6 +56,78 @@ __device__ __forceinline__ int swz(int row) {
   else return ((row & 3) << 2) | ((row >> 2) & 3);
 }
 
+// One tile of queries: its sequence and rows, and the keys it can see.
+struct Tile {
+  int q_first, lq, k_first, lk;
+  int m0;                      // first row within the sequence
+  int k_end;                   // keys that any of its rows sees
+};
+__device__ __forceinline__ int visible_end(int row, int lq, int lk, int causal) {
+  return causal ? clamp_to(row + lk - lq + 1, 0, lk) : lk;
+}
+__device__ __forceinline__ Tile tile_of(const PrefillAttnArgs& a, int seq, int from_end) {
+  Tile t;
+  seq_rows(a.cu_q, seq, a.tq, t.q_first, t.lq);
+  seq_rows(a.cu_k, seq, a.tk, t.k_first, t.lk);
+  t.m0 = ((t.lq + kBM - 1) / kBM - 1 - from_end) * kBM;
+  t.k_end = visible_end(min(t.m0 + kBM, t.lq) - 1, t.lq, t.lk, a.causal);
+  return t;
+}
+// Keys of one piece when a tile's are divided: whole BN steps, evenly, at least kMinSteps of them.
+constexpr int kMinSteps = 4;
+template <int BN>
+__device__ __forceinline__ int piece_keys(int k_end, int splits) {
+  const int steps = (k_end + BN - 1) / BN;
+  return max((steps + splits - 1) / splits, kMinSteps) * BN;
+}
+
+// The tile with this number, the ones with the most keys first: within a sequence the last tile of queries sees
+// the most, and with up to 64 causal sequences all their tiles are ordered by their last tile's keys less their
+// distance from it (in steps of kBM), so that the longest work is not the last to start.
+__device__ __forceinline__ bool find_tile(const PrefillAttnArgs& a, int index, int& seq, int& from_end) {
+  auto tiles = [&](int s) {
+    int first, count;
+    seq_rows(a.cu_q, s, a.tq, first, count);
+    return (count + kBM - 1) / kBM;
+  };
+  if (a.n_seqs == 1 || a.n_seqs > kWave || !a.causal) {
+    locate(index, a.n_seqs, tiles, seq, from_end);
+  } else {
+    const int lane = threadIdx.x & (kWave - 1);
+    int n = 0, top = INT32_MIN, qf, lq, kf, lk;
+    if (lane < a.n_seqs) {
+      seq_rows(a.cu_q, lane, a.tq, qf, lq);
+      seq_rows(a.cu_k, lane, a.tk, kf, lk);
+      n = (lq + kBM - 1) / kBM;
+      if (n) top = (lk + kBM - 1) / kBM;
+    }
+    int level = top, low = n ? top - n : INT32_MAX;          // levels (low, top] hold this lane's tiles
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      level = max(level, __shfl_xor(level, off, kWave));
+      low = min(low, __shfl_xor(low, off, kWave));
+    }
+    seq = a.n_seqs;
+    from_end = 0;
+    for (; level > low; --level) {
+      const uint64_t at = __ballot(n > 0 && level <= top && level > top - n);
+      const int count = __popcll(at);
+      if (index < count) {
+        uint64_t rest = at;
+        for (int i = 0; i < index; ++i) rest &= rest - 1;
+        seq = __ffsll((unsigned long long)rest) - 1;
+        from_end = __shfl(top, seq, kWave) - level;
+        break;
+      }
+      index -= count;
+    }
+  }
+  if (seq >= a.n_seqs) return false;
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  from_end = __builtin_amdgcn_readfirstlane(from_end);
+  return true;
+}
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // 64 bits per lane, transposed in each group of 16 lanes: lane i gets element i % 4 of lanes i/4, 4 + i/4,
@@ -68,37 +143,33 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   constexpr int NB = BN / 32;            // 32-key blocks of a tile
   constexpr int DB = DP / 32;            // 32-dimension blocks of O
   constexpr int kTileBytes = BN * DP * 2;
+  constexpr bool kAhead = DP <= 128;     // the next tile's scores run beside this tile's softmax (registers allow it)
   constexpr int kLoads = BN * CH / kThreads;      // direct loads of a wave per tile and operand
-  extern __shared__ __align__(16) char s_kv[];    // [2 stages][K, V][BN][CH] pieces
+  extern __shared__ __align__(16) char s_kv[];    // [K, V][2 stages][BN][CH] pieces
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l32 = lane & 31, g = lane >> 5;
 
+  // key-value heads fastest (one XCD keeps to as few of them as there are), then the query heads that share one
   const int kvh = blockIdx.x % a.hkv;
   const int rest = blockIdx.x / a.hkv;
   const int head = kvh * a.group + rest % a.group;
-  int seq, local;
-  locate(rest / a.group, a.n_seqs, [&](int s) {
-    int first, count;
-    seq_rows(a.cu_q, s, a.tq, first, count);
-    return (count + kBM - 1) / kBM;
-  }, seq, local);
-  if (seq >= a.n_seqs) return;
-  seq = __builtin_amdgcn_readfirstlane(seq);
-  local = __builtin_amdgcn_readfirstlane(local);
-  int q_first, lq, k_first, lk;
-  seq_rows(a.cu_q, seq, a.tq, q_first, lq);
-  seq_rows(a.cu_k, seq, a.tk, k_first, lk);
-  // a sequence's last tile of queries sees the most keys: it comes first
-  const int m0 = ((lq + kBM - 1) / kBM - 1 - local) * kBM;
-  const int shift = lk - lq;                                    // query i sees keys 0..i + shift
-  const int row = m0 + wave * kWaveRows + l32;                  // this lane's query
-  const int sees = a.causal ? clamp_to(min(row, lq - 1) + shift + 1, 0, lk) : lk;        // its first hidden key
-  const int m_last = min(m0 + kBM, lq) - 1;
-  const int k_end = a.causal ? clamp_to(m_last + shift + 1, 0, lk) : lk;                 // the workgroup's
-  const int full = a.causal ? clamp_to(m0 + wave * kWaveRows + shift + 1, 0, lk) : lk;   // keys that all rows see
-  const int wave_end = a.causal ? clamp_to(m0 + wave * kWaveRows + kWaveRows + shift, 0, lk) : lk;   // keys that any sees
+  const int split = rest / a.group % a.splits;
+  int seq, from_end;
+  if (!find_tile(a, rest / a.group / a.splits, seq, from_end)) return;
+  const Tile t = tile_of(a, seq, from_end);
+  const int q_first = t.q_first, lq = t.lq, k_first = t.k_first, lk = t.lk, m0 = t.m0;
+  const int per = piece_keys<BN>(t.k_end, a.splits);
+  const int k_begin = split * per;                              // this piece's keys: [k_begin, k_end)
+  if (split && k_begin >= t.k_end) return;
+  const int k_end = min(k_begin + per, t.k_end);
+  const bool whole = t.k_end <= per;
+  const int w0 = m0 + wave * kWaveRows;
+  const int row = w0 + l32;                                     // this lane's query
+  const int sees = visible_end(min(row, lq - 1), lq, lk, a.causal);                       // its first hidden key
+  const int full = visible_end(w0, lq, lk, a.causal);                                     // keys that all its wave sees
+  const int wave_end = min(visible_end(w0 + kWaveRows - 1, lq, lk, a.causal), k_end);     // and that any does
 
   uint4 qf[KS];
   {
@@ -115,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   // head_dim repeat the first (they meet zeros of Q, or give columns of O that are not stored)
   const uint16_t* kbase = a.k + (size_t)k_first * a.k_row + (size_t)kvh * a.k_head;
   const uint16_t* vbase = a.v + (size_t)k_first * a.v_row + (size_t)kvh * a.v_head;
-  auto stage = [&](int j0, int buf) {
-    const uint32_t lds = lds_addr(s_kv) + buf * 2 * kTileBytes;
+  auto stage = [&](const uint16_t* base, int64_t stride, int j0, uint32_t lds) {
     const int left = lk - 1 - j0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -124,11 +194,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
       const int r = slot / CH;
       int piece = (slot % CH) ^ swz<CH>(r);
       if (piece * 8 >= a.d) piece = 0;
-      const int rr = min(r, left);
       const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (wave * kLoads + i) * kWave * 16);
-      lds_dma16(kbase + (size_t)j0 * a.k_row, (uint32_t)(rr * (int)a.k_row + piece * 8) * 2, to);
-      lds_dma16(vbase + (size_t)j0 * a.v_row, (uint32_t)(rr * (int)a.v_row + piece * 8) * 2, to + kTileBytes);
+      lds_dma16(base + (size_t)j0 * stride, (uint32_t)(min(r, left) * (int)stride + piece * 8) * 2, to);
     }
+  };
+  auto stage_k = [&](int j0, int buf) {
+    if (j0 < k_end) stage(kbase, a.k_row, j0, lds_addr(s_kv) + buf * kTileBytes);
+  };
+  auto stage_v = [&](int j0, int buf) {
+    if (j0 < k_end) stage(vbase, a.v_row, j0, lds_addr(s_kv) + (2 + buf) * kTileBytes);
   };
 
   f32x16 o[DB];
@@ -136,19 +210,11 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   for (int b = 0; b < DB; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, mx = -INFINITY;
 
-  if (k_end > 0) stage(0, 0);
-  int buf = 0;
-  for (int j0 = 0; j0 < k_end; j0 += BN, buf ^= 1) {
-    wait_vm<0>(0);
-    bare_barrier();
-    if (j0 + BN < k_end) stage(j0 + BN, buf ^ 1);
-    if (j0 >= wave_end) continue;        // every row of this wave ends before this tile
-    const char* ks = s_kv + buf * 2 * kTileBytes;
-    const char* vs = ks + kTileBytes;
-
-    f32x16 s[NB];
+  // the scores of the tile in K buffer `buf`: register r of block b is key 32 b + 8 (r / 4) + 4 g + r % 4
+  auto scores = [&](f32x16 (&s)[NB], int buf) {
+    const char* ks = s_kv + buf * kTileBytes;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -160,20 +226,26 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
         s[b] = mfma32<DT>(kf, qf[t], s[b]);
       }
     }
-    // register r of block b is key j0 + 32 b + 8 (r / 4) + 4 g + r % 4
-    if (j0 + BN > full) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (j0 + 32 * b + 8 * (r / 4) + 4 * g + r % 4 >= sees) s[b][r] = -INFINITY;
-    }
-    float mx = s[0][0];
+  };
+  auto mask = [&](f32x16 (&s)[NB], int j0) {
+    if (j0 + BN <= full) return;
+    const int hidden = sees - j0 - 4 * g;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32, kWave)) * a.c;
+      for (int r = 0; r < 16; ++r)
+        if (32 * b + 8 * (r / 4) + r % 4 >= hidden) s[b][r] = -INFINITY;
+  };
+  auto row_max = [&](const f32x16 (&s)[NB]) {
+    float v = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v = fmaxf(v, s[b][r]);
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1])) * a.c;
+  };
+  auto follow = [&]() {
     if (__any(mx > m + kSlack)) {
       const float now = fmaxf(mx, m), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
       m = now;
@@ -181,22 +253,29 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] *= alpha;
     }
+  };
+  auto weights = [&](f32x16 (&s)[NB], uint4 (&pf)[BN / 16]) {
     const float base = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int t = 0; t < BN / 16; ++t) {
+      f32x16& p = s[t / 2];
+      const int r0 = t % 2 * 8;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[b][r] = exp2_hw(fmaf(s[b][r], a.c, -base));
-        sum += s[b][r];
+      for (int r = r0; r < r0 + 8; ++r) {
+        p[r] = exp2_hw(fmaf(p[r], a.c, -base));
+        sum += p[r];
       }
+      pf[t] = make_uint4(pack2<DT>(p[r0], p[r0 + 1]), pack2<DT>(p[r0 + 2], p[r0 + 3]), pack2<DT>(p[r0 + 4], p[r0 + 5]),
+                         pack2<DT>(p[r0 + 6], p[r0 + 7]));
+    }
     l += sum;
+    asm volatile("" : "+v"(l));      // the sum is taken here, not after the product that follows
+  };
+  auto values = [&](const uint4 (&pf)[BN / 16], int buf) {
+    const char* vs = s_kv + (2 + buf) * kTileBytes;
 #pragma unroll
     for (int t = 0; t < BN / 16; ++t) {
-      const f32x16& p = s[t / 2];
-      const int r0 = t % 2 * 8;
-      const uint4 pf = make_uint4(pack2<DT>(p[r0], p[r0 + 1]), pack2<DT>(p[r0 + 2], p[r0 + 3]),
-                                  pack2<DT>(p[r0 + 4], p[r0 + 5]), pack2<DT>(p[r0 + 6], p[r0 + 7]));
       // lane (16-lane group q, i): row 16 t + 4 g + i / 4 (then + 8), dimensions 32 b + 16 (q % 2) + 4 (i % 4)
       const int vrow = 16 * t + 4 * g + ((lane & 15) >> 2);
       const int piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
@@ -204,15 +283,116 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
       for (int b = 0; b < DB; ++b) {
         const uint2 lo = lds_read_tr(vs + (vrow * CH + ((4 * b + piece) ^ swz<CH>(vrow))) * 16 + 8 * (lane & 1));
         const uint2 hi = lds_read_tr(vs + ((vrow + 8) * CH + ((4 * b + piece) ^ swz<CH>(vrow + 8))) * 16 + 8 * (lane & 1));
-        o[b] = mfma32<DT>(make_uint4(lo.x, lo.y, hi.x, hi.y), pf, o[b]);
+        o[b] = mfma32<DT>(make_uint4(lo.x, lo.y, hi.x, hi.y), pf[t], o[b]);
       }
     }
+  };
+  // Tile j0, whose scores are in `cur` (their maximum in mx), and the scores of the one after it: the next tile's
+  // K Q^T does not depend on this tile's exponentials, so matrix and vector instructions run side by side.
+  auto arrive = [&](int j0, int buf) {
+    wait_vm<0>(0);
+    bare_barrier();
+    if constexpr (kAhead) stage_k(j0 + 2 * BN, buf);
+    else stage_k(j0 + BN, buf ^ 1);
+    stage_v(j0 + BN, buf ^ 1);
+  };
+  // the order of a step's instructions: fragments a few reads ahead, vector work between the matrix instructions
+  auto interleave = [&]() {
+    constexpr int kRead = 0x100, kMfma = 0x8, kVector = 0x402;
+    __builtin_amdgcn_sched_group_barrier(kRead, 4, 0);
+#pragma unroll
+    for (int i = 0; i < NB * KS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kVector, 40 / KS, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < BN / 16 * DB; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(kVector, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    }
+  };
+  auto step = [&](f32x16 (&cur)[NB], f32x16 (&nxt)[NB], int j0, int buf) {
+    arrive(j0, buf);
+    follow();
+    uint4 pf[BN / 16];
+    scores(nxt, buf ^ 1);
+    weights(cur, pf);
+    values(pf, buf);
+    interleave();
+    mask(nxt, j0 + BN);
+    mx = row_max(nxt);
+  };
+  auto last = [&](f32x16 (&cur)[NB], int j0, int buf) {
+    arrive(j0, buf);
+    follow();
+    uint4 pf[BN / 16];
+    weights(cur, pf);
+    values(pf, buf);
+  };
+
+  if (k_begin < k_end) {
+    int j0 = k_begin, buf = 0;
+    stage_k(j0, 0);
+    if constexpr (kAhead) {
+      wait_vm<0>(0);
+      bare_barrier();
+      stage_k(j0 + BN, 1);
+    }
+    stage_v(j0, 0);
+    if constexpr (!kAhead) {
+      for (; j0 < wave_end; j0 += BN, buf ^= 1) {
+        arrive(j0, buf);
+        f32x16 s0[NB];
+        scores(s0, buf);
+        mask(s0, j0);
+        mx = row_max(s0);
+        follow();
+        uint4 pf[BN / 16];
+        weights(s0, pf);
+        values(pf, buf);
+      }
+    } else if (j0 < wave_end) {
+      f32x16 s0[NB], s1[NB];
+      scores(s0, 0);
+      mask(s0, j0);
+      mx = row_max(s0);
+      for (; j0 + 2 * BN < wave_end; j0 += 2 * BN) {
+        step(s0, s1, j0, 0);
+        step(s1, s0, j0 + BN, 1);
+      }
+      if (j0 + BN < wave_end) {
+        step(s0, s1, j0, 0);
+        last(s1, j0 + BN, 1);
+        j0 += 2 * BN;
+      } else {
+        last(s0, j0, 0);
+        j0 += BN;
+        buf = 1;
+      }
+    }
+    for (; j0 < k_end; j0 += BN, buf ^= 1) arrive(j0, buf);      // the other waves' tiles: this wave brings its part
   }
 
   l += __shfl_xor(l, 32, kWave);
   if (row >= lq) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
   const size_t to = (size_t)(q_first + row) * a.hq + head;
+  if (!whole) {
+    const size_t at = (size_t)split * a.tq * a.hq + to;
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int dim = 32 * b + 8 * r + 4 * g;
+        if (dim < a.d)
+          *reinterpret_cast<float4*>(a.part_o + at * a.d + dim) =
+              make_float4(o[b][4 * r], o[b][4 * r + 1], o[b][4 * r + 2], o[b][4 * r + 3]);
+      }
+    if (g == 0) a.part_ml[at] = make_float2(m, l);
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -226,10 +406,54 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   if (a.lse && g == 0) a.lse[to] = l > 0.f ? kLn2 * (m + log2_hw(l)) : -INFINITY;
 }
 
+// One workgroup per row and 1024 of its outputs: the pieces of the row's tile brought to their common maximum and
+// added in order.  A thread takes four dimensions of one head.
+template <int DT, int BN>
+__global__ void __launch_bounds__(kThreads) k_attention_prefill_join(PrefillAttnArgs a) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int row = blockIdx.x;
+  int seq = 0;                 // the number of sequences that end at or before the row
+  for (int base = 0; base < a.n_seqs; base += kWave) {
+    const int end = base + lane < a.n_seqs ? a.cu_q[base + lane + 1] : INT32_MAX;
+    seq += __popcll(__ballot(end <= row));
+  }
+  if (seq >= a.n_seqs) return;
+  Tile t = tile_of(a, seq, 0);
+  if (row < t.q_first || row >= t.q_first + t.lq) return;
+  t = tile_of(a, seq, (t.lq + kBM - 1) / kBM - 1 - (row - t.q_first) / kBM);
+  const int per = piece_keys<BN>(t.k_end, a.splits);
+  const int pieces = (t.k_end + per - 1) / per;
+  if (pieces <= 1) return;
+  const int quads = a.d / 4;
+  const int at = blockIdx.y * kThreads + threadIdx.x;
+  const int head = at / quads, dim = at % quads * 4;
+  if (head >= a.hq) return;
+  const size_t to = (size_t)row * a.hq + head, step = (size_t)a.tq * a.hq;
+  float m = -INFINITY, sum = 0.f;
+  for (int i = 0; i < pieces; ++i) m = fmaxf(m, a.part_ml[to + i * step].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < pieces; ++i) {
+    const float2 ml = a.part_ml[to + i * step];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (to + i * step) * a.d + dim);
+    const float f = exp2_hw(ml.x - base);
+    sum += f * ml.y;
+    x.x += f * v.x; x.y += f * v.y; x.z += f * v.z; x.w += f * v.w;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(a.out + to * a.d + dim) =
+      make_uint2(pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv));
+  if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (m + log2_hw(sum)) : -INFINITY;
+}
+
 template <int DT, int DP, int BN>
 hipError_t go(const PrefillAttnArgs& a, hipStream_t st) {
   const int tiles = a.tq / kBM + a.n_seqs;          // at least the sum over sequences of ceil(rows / kBM)
-  hipLaunchKernelGGL((k_attention_prefill<DT, DP, BN>), dim3(tiles * a.hq), dim3(kThreads), 4 * BN * DP * 2, st, a);
+  hipLaunchKernelGGL((k_attention_prefill<DT, DP, BN>), dim3(tiles * a.hq * a.splits), dim3(kThreads), 4 * BN * DP * 2, st, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (a.splits == 1) return hipSuccess;
+  const int groups = (a.hq * (a.d / 4) + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((k_attention_prefill_join<DT, BN>), dim3(a.tq, groups), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 template <int DT>
@@ -244,7 +468,7 @@ hipError_t by_dim(const PrefillAttnArgs& a, hipStream_t st) {
 hipError_t launch_attention_prefill(const spa_heads& q, const spa_heads& k, const spa_heads& v, int dtype, int tq,
                                     int tk, int n_q_heads, int n_kv_heads, int head_dim, const int32_t* cu_q,
                                     const int32_t* cu_k, int n_seqs, bool causal, float scale, void* out, float* lse,
-                                    hipStream_t st) {
+                                    int splits, float* part_o, float* part_ml, hipStream_t st) {
   PrefillAttnArgs a{};
   a.q = static_cast<const uint16_t*>(q.data);
   a.k = static_cast<const uint16_t*>(k.data);
@@ -257,6 +481,7 @@ hipError_t launch_attention_prefill(const spa_heads& q, const spa_heads& k, cons
   a.lse = lse;
   a.tq = tq; a.tk = tk; a.hq = n_q_heads; a.hkv = n_kv_heads; a.group = n_q_heads / n_kv_heads; a.d = head_dim;
   a.n_seqs = n_seqs; a.causal = causal;
+  a.splits = splits; a.part_o = part_o; a.part_ml = reinterpret_cast<float2*>(part_ml);
   a.c = scale * kLog2e;
   return dtype == SPA_F16 ? by_dim<SPA_F16>(a, st) : by_dim<SPA_BF16>(a, st);
 }

@@ -55,24 +55,30 @@ spa_status attention_decode(const spa_heads* q, int32_t n_seqs, int32_t n_q_head
                                                  stream_of(stream)));
 }
 
-size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t tk, int32_t n_seqs, int32_t n_q_heads,
                                              int32_t head_dim) {
-  (void)tq, (void)n_seqs, (void)n_q_heads, (void)n_kv_heads, (void)head_dim;
-  return 0;
+  if (tq < 1 || tq > kMaxRows || tk < 0 || tk > kMaxRows || n_seqs < 1 || n_seqs > kMaxSeqs || n_q_heads < 1 ||
+      n_q_heads > kMaxHeads || head_dim < 1 || !built_head_dim(head_dim))
+    return 0;
+  return prefill_attn_plan(tq, tk, n_seqs, n_q_heads, head_dim).bytes;
 }
 
 spa_status attention_prefill(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t tq,
                              int32_t tk, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_q,
                              const int32_t* cu_k, int32_t n_seqs, int32_t causal, float scale, void* out, float* lse,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace, (void)workspace_bytes;
   if (spa_status s = check_attention_prefill(q, k, v, dtype, tq, tk, n_q_heads, n_kv_heads, head_dim, cu_q, cu_k, n_seqs,
                                              scale, out))
     return s;
   if (tq == 0 || n_seqs == 0) return SPA_OK;
+  const PrefillAttnPlan p = prefill_attn_plan(tq, tk, n_seqs, n_q_heads, head_dim);
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes || !aligned16(workspace))) return SPA_ERR_INVALID;
+  char* base = static_cast<char*>(workspace);
   const spa_heads none{q->data, 0, 0};   // no keys at all: nothing is read through these
   return hip_status(spa::launch_attention_prefill(*q, tk ? *k : none, tk ? *v : none, dtype, tq, tk, n_q_heads,
                                                   n_kv_heads, head_dim, cu_q, cu_k, n_seqs, causal != 0, scale, out, lse,
+                                                  p.splits, p.bytes ? reinterpret_cast<float*>(base + p.o) : nullptr,
+                                                  p.bytes ? reinterpret_cast<float*>(base + p.ml) : nullptr,
                                                   stream_of(stream)));
 }
 

@@ -128,8 +128,34 @@ inline spa_status check_attention_prefill(const spa_heads* q, const spa_heads* k
   if (tk > 0 && (!valid_heads(k) || !valid_heads(v) || !valid_strides(k) || !valid_strides(v))) return SPA_ERR_INVALID;
   if (!built || !built_heads(q)) return SPA_ERR_UNSUPPORTED;
   if (tk > 0 && (!built_heads(k) || !built_heads(v))) return SPA_ERR_UNSUPPORTED;
-  if (((int64_t)tq / 64 + n_seqs) * n_q_heads > INT32_MAX / 2) return SPA_ERR_UNSUPPORTED;
+  if (((int64_t)tq / 128 + n_seqs) * n_q_heads > (int64_t(1) << 23)) return SPA_ERR_UNSUPPORTED;   // workgroups
   return SPA_OK;
+}
+
+// Pieces that the keys of a tile of 128 query rows are divided into when the call's tiles alone leave most of the
+// chip idle: as many as fill kPrefillTarget workgroups, up to 8.  The number of tiles is estimated (every sequence
+// ends with half a tile); sequences' keys stay on the device, where a piece is at least 4 key steps, so a call whose
+// keys altogether are no more than that is not divided.
+constexpr int kPrefillTarget = 512, kMaxSplits = 8;
+inline int prefill_splits(int tq, int tk, int n_seqs, int n_q_heads) {
+  const int64_t groups = ((int64_t)tq / 128 + (n_seqs + 1) / 2) * n_q_heads;
+  const int64_t most = tk / 256;
+  int64_t s = kPrefillTarget / (groups > 0 ? groups : 1);
+  s = s < most ? s : most;
+  return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+}
+struct PrefillAttnPlan {
+  int splits;
+  size_t o, ml, bytes;    // [splits][tq][heads][head_dim] float32 partial outputs, [splits][tq][heads][2] maximum and sum
+};
+inline PrefillAttnPlan prefill_attn_plan(int tq, int tk, int n_seqs, int n_q_heads, int head_dim) {
+  PrefillAttnPlan p{};
+  p.splits = prefill_splits(tq, tk, n_seqs, n_q_heads);
+  if (p.splits == 1) return p;
+  const size_t rows = (size_t)p.splits * tq * n_q_heads;
+  p.ml = round256(rows * head_dim * 4);
+  p.bytes = p.ml + round256(rows * 8);
+  return p;
 }
 
 // ---- norms ----

@@ -20,7 +20,7 @@ hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads
 hipError_t launch_attention_prefill(const spa_heads& q, const spa_heads& k, const spa_heads& v, int dtype, int tq,
                                     int tk, int n_q_heads, int n_kv_heads, int head_dim, const int32_t* cu_q,
                                     const int32_t* cu_k, int n_seqs, bool causal, float scale, void* out, float* lse,
-                                    hipStream_t st);
+                                    int splits, float* part_o, float* part_ml, hipStream_t st);
 
 struct NormArgs {
   const void* x;

@@ -423,7 +423,7 @@ PyObject* py_attention_prefill(PyObject*, PyObject* const* args, Py_ssize_t n_ar
     const at::Tensor out = output(a.v[8], {tq, hq, d}, type, dev, "out");
     at::Tensor lse;
     if (a.v[7] && truth(a.v[7])) lse = fresh({tq, hq}, at::kFloat, dev);
-    const at::Tensor ws = workspace(a.v[9], a.v[9] ? 0 : spa_attention_prefill_workspace_bytes(tq, n, hq, hkv, d), dev);
+    const at::Tensor ws = workspace(a.v[9], a.v[9] ? 0 : spa_attention_prefill_workspace_bytes(tq, tk, n, hq, d), dev);
     check(attention_prefill(&qh, &kh, &vh, dtype_code(type), tq, tk, hq, hkv, d, static_cast<const int32_t*>(cu_q.data_ptr()),
                             static_cast<const int32_t*>(cu_k.data_ptr()), n, a.v[5] ? truth(a.v[5]) : 1,
                             scale_of(a.v[6], d), out.data_ptr(),

@@ -511,12 +511,14 @@ spa_status attention_decode(const spa_heads* q, int32_t n_seqs, int32_t n_q_head
  *  out       [device] [tq][n_q_heads][head_dim] dtype
  *  lse       [device] [tq][n_q_heads] float32 or NULL
  *  workspace [device] spa_attention_prefill_workspace_bytes(...) bytes (may
- *            be 0, then NULL), 16-byte aligned, no initial contents needed
+ *            be 0, then NULL), 16-byte aligned, no initial contents needed:
+ *            partial sums where few query rows meet many keys and the keys
+ *            are divided over the chip
  * n_q_heads must be a multiple of n_kv_heads, scale > 0 and finite;
  * head_dim a multiple of 8 up to 256.  Rows of out and lse outside every
  * sequence are not written.
  */
-size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+size_t spa_attention_prefill_workspace_bytes(int32_t tq, int32_t tk, int32_t n_seqs, int32_t n_q_heads,
                                              int32_t head_dim);
 spa_status attention_prefill(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t tq,
                              int32_t tk, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_q,
