@@ -65,13 +65,10 @@ struct Tile {
 __device__ __forceinline__ int visible_end(int row, int lq, int lk, int causal) {
   return causal ? clamp_to(row + lk - lq + 1, 0, lk) : lk;
 }
-__device__ __forceinline__ Tile tile_of(const PrefillAttnArgs& a, int seq, int from_end) {
-  Tile t;
-  seq_rows(a.cu_q, seq, a.tq, t.q_first, t.lq);
-  seq_rows(a.cu_k, seq, a.tk, t.k_first, t.lk);
+// Fills in m0 and k_end of the tile that lies `from_end` tiles before its sequence's last.
+__device__ __forceinline__ void place_tile(const PrefillAttnArgs& a, Tile& t, int from_end) {
   t.m0 = ((t.lq + kBM - 1) / kBM - 1 - from_end) * kBM;
   t.k_end = visible_end(min(t.m0 + kBM, t.lq) - 1, t.lq, t.lk, a.causal);
-  return t;
 }
 // Keys of one piece when a tile's are divided: whole BN steps, evenly, at least kMinSteps of them.
 constexpr int kMinSteps = 4;
@@ -81,50 +78,70 @@ __device__ __forceinline__ int piece_keys(int k_end, int splits) {
   return max((steps + splits - 1) / splits, kMinSteps) * BN;
 }
 
-// The tile with this number, the ones with the most keys first: within a sequence the last tile of queries sees
-// the most, and with up to 64 causal sequences all their tiles are ordered by their last tile's keys less their
-// distance from it (in steps of kBM), so that the longest work is not the last to start.
-__device__ __forceinline__ bool find_tile(const PrefillAttnArgs& a, int index, int& seq, int& from_end) {
-  auto tiles = [&](int s) {
-    int first, count;
-    seq_rows(a.cu_q, s, a.tq, first, count);
-    return (count + kBM - 1) / kBM;
-  };
-  if (a.n_seqs == 1 || a.n_seqs > kWave || !a.causal) {
-    locate(index, a.n_seqs, tiles, seq, from_end);
-  } else {
+// The tile with this number; the last tile of a sequence's queries, which sees the most keys, comes first.  Up to
+// 64 sequences' offsets are read once, one to a lane.  Where the workgroups would fill the chip fewer than three
+// times, the tiles of all causal sequences are ordered by their last one's keys less their distance from it (in steps
+// of kBM), so that the longest work is not the last to start: 16 prompts of up to 1000 by 20 heads of 64 take 41 us so
+// and 45.5 us in the sequences' order.  With more, equal work that starts together also waits together: nine prompts
+// of up to 1531 by 32 heads of 128 take 97 us so and 92 us in order.
+template <int DP>
+__device__ __forceinline__ bool find_tile(const PrefillAttnArgs& a, int index, Tile& t) {
+  constexpr uint32_t kPlaces = DP <= 64 ? 768 : DP <= 128 ? 512 : 256;      // workgroups on the chip at a time
+  int seq, from_end = 0;
+  if (a.n_seqs <= kWave) {
     const int lane = threadIdx.x & (kWave - 1);
-    int n = 0, top = INT32_MIN, qf, lq, kf, lk;
+    int qf = 0, lq = 0, kf = 0, lk = 0;
     if (lane < a.n_seqs) {
       seq_rows(a.cu_q, lane, a.tq, qf, lq);
       seq_rows(a.cu_k, lane, a.tk, kf, lk);
-      n = (lq + kBM - 1) / kBM;
-      if (n) top = (lk + kBM - 1) / kBM;
     }
-    int level = top, low = n ? top - n : INT32_MAX;          // levels (low, top] hold this lane's tiles
+    const int n = (lq + kBM - 1) / kBM;
+    seq = kWave;
+    if (a.causal && a.n_seqs > 1 && gridDim.x < 3 * kPlaces) {
+      const int top = (lk + kBM - 1) / kBM;
+      int level = n ? top : INT32_MIN, low = n ? top - n : INT32_MAX;        // levels (top - n, top] hold a lane's tiles
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      level = max(level, __shfl_xor(level, off, kWave));
-      low = min(low, __shfl_xor(low, off, kWave));
-    }
-    seq = a.n_seqs;
-    from_end = 0;
-    for (; level > low; --level) {
-      const uint64_t at = __ballot(n > 0 && level <= top && level > top - n);
-      const int count = __popcll(at);
-      if (index < count) {
-        uint64_t rest = at;
-        for (int i = 0; i < index; ++i) rest &= rest - 1;
-        seq = __ffsll((unsigned long long)rest) - 1;
-        from_end = __shfl(top, seq, kWave) - level;
-        break;
+      for (int off = 32; off >= 1; off >>= 1) {
+        level = max(level, __shfl_xor(level, off, kWave));
+        low = min(low, __shfl_xor(low, off, kWave));
       }
-      index -= count;
+      for (; level > low; --level) {
+        uint64_t at = __ballot(level <= top && level > top - n);
+        const int count = __popcll(at);
+        if (index < count) {
+          for (int i = 0; i < index; ++i) at &= at - 1;
+          seq = __ffsll((unsigned long long)at) - 1;
+          from_end = __shfl(top, seq, kWave) - level;
+          break;
+        }
+        index -= count;
+      }
+    } else {
+      const int incl = wave_scan(n);
+      const uint64_t past = __ballot(incl > index);
+      if (past) {
+        seq = __ffsll((unsigned long long)past) - 1;
+        from_end = index - __shfl(incl - n, seq, kWave);
+      }
     }
+    if (seq == kWave) return false;
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    t.q_first = __builtin_amdgcn_readlane(qf, seq);
+    t.lq = __builtin_amdgcn_readlane(lq, seq);
+    t.k_first = __builtin_amdgcn_readlane(kf, seq);
+    t.lk = __builtin_amdgcn_readlane(lk, seq);
+  } else {
+    locate(index, a.n_seqs, [&](int s) {
+      int first, count;
+      seq_rows(a.cu_q, s, a.tq, first, count);
+      return (count + kBM - 1) / kBM;
+    }, seq, from_end);
+    if (seq >= a.n_seqs) return false;
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    seq_rows(a.cu_q, seq, a.tq, t.q_first, t.lq);
+    seq_rows(a.cu_k, seq, a.tk, t.k_first, t.lk);
   }
-  if (seq >= a.n_seqs) return false;
-  seq = __builtin_amdgcn_readfirstlane(seq);
-  from_end = __builtin_amdgcn_readfirstlane(from_end);
+  place_tile(a, t, from_end);
   return true;
 }
 
@@ -156,15 +173,17 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   const int rest = blockIdx.x / a.hkv;
   const int head = kvh * a.group + rest % a.group;
   const int split = rest / a.group % a.splits;
-  int seq, from_end;
-  if (!find_tile(a, rest / a.group / a.splits, seq, from_end)) return;
-  const Tile t = tile_of(a, seq, from_end);
-  const int q_first = t.q_first, lq = t.lq, k_first = t.k_first, lk = t.lk, m0 = t.m0;
-  const int per = piece_keys<BN>(t.k_end, a.splits);
+  Tile t;
+  if (!find_tile<DP>(a, rest / a.group / a.splits, t)) return;
+  // one value for the wave, whichever way it was found: tile bases stay in scalar registers
+  const int q_first = __builtin_amdgcn_readfirstlane(t.q_first), lq = __builtin_amdgcn_readfirstlane(t.lq);
+  const int k_first = __builtin_amdgcn_readfirstlane(t.k_first), lk = __builtin_amdgcn_readfirstlane(t.lk);
+  const int m0 = __builtin_amdgcn_readfirstlane(t.m0), tile_end = __builtin_amdgcn_readfirstlane(t.k_end);
+  const int per = piece_keys<BN>(tile_end, a.splits);
   const int k_begin = split * per;                              // this piece's keys: [k_begin, k_end)
-  if (split && k_begin >= t.k_end) return;
-  const int k_end = min(k_begin + per, t.k_end);
-  const bool whole = t.k_end <= per;
+  if (split && k_begin >= tile_end) return;
+  const int k_end = min(k_begin + per, tile_end);
+  const bool whole = tile_end <= per;
   const int w0 = m0 + wave * kWaveRows;
   const int row = w0 + l32;                                     // this lane's query
   const int sees = visible_end(min(row, lq - 1), lq, lk, a.causal);                       // its first hidden key
@@ -418,9 +437,11 @@ __global__ void __launch_bounds__(kThreads) k_attention_prefill_join(PrefillAttn
     seq += __popcll(__ballot(end <= row));
   }
   if (seq >= a.n_seqs) return;
-  Tile t = tile_of(a, seq, 0);
+  Tile t;
+  seq_rows(a.cu_q, seq, a.tq, t.q_first, t.lq);
+  seq_rows(a.cu_k, seq, a.tk, t.k_first, t.lk);
   if (row < t.q_first || row >= t.q_first + t.lq) return;
-  t = tile_of(a, seq, (t.lq + kBM - 1) / kBM - 1 - (row - t.q_first) / kBM);
+  place_tile(a, t, (t.lq + kBM - 1) / kBM - 1 - (row - t.q_first) / kBM);
   const int per = piece_keys<BN>(t.k_end, a.splits);
   const int pieces = (t.k_end + per - 1) / per;
   if (pieces <= 1) return;
