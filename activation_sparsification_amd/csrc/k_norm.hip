@@ -1,10 +1,12 @@
 // Norms after one block and before the next, with the block's gate and residual scale:
 //   u = N_post(x),  h = residual + scale * gate * u,  y = N_pre(h).
 //
-// One workgroup per row.  The row stays in registers as float32 from its one read to its one write, so the
-// HBM traffic is the inputs once and the outputs once; the reductions go wave butterfly -> LDS -> every thread.
-// The layer norm's variance is taken about the mean in a second pass over the registers (no cancellation).
-// Every load of the row, its residual, gate and weights is issued before the first reduction.
+// Bound by HBM for many rows, by latency for one.  A workgroup holds a row in registers from its one read to its
+// one write, so the traffic is the inputs once and the outputs once; it walks over rows with the next row's loads
+// in flight while this one is reduced, and keeps the weights.  Sums go DPP adds -> LDS -> every thread.  The layer
+// norm's variance is taken about the mean in a second pass over the registers (no cancellation).
+#include <algorithm>
+
 #include "spa_common.h"
 #include "spa_layer.h"
 
@@ -12,23 +14,33 @@ namespace spa {
 
 namespace {
 
-// VEC consecutive elements of DT at index i (VEC == 8: 16-byte loads; VEC == 1: any alignment).
+// VEC consecutive elements as stored (VEC == 8: 16-byte loads; VEC == 1: any alignment).
 template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void* p, size_t i, float (&out)[VEC]) {
-  using T = typename Dt<DT>::T;
-  const T* s = static_cast<const T*>(p) + i;
-  if constexpr (VEC == 1) {
-    out[0] = to_f32<DT>(s[0]);
-  } else if constexpr (DT == SPA_F32) {
-    const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
-    out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
-    out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(s);
+struct Stored {
+  static constexpr int kBytes = VEC * Dt<DT>::bytes, kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    using T = typename Dt<DT>::T;
+    const T* s = static_cast<const T*>(p) + i;
+    if constexpr (VEC == 1) {
+      if constexpr (DT == SPA_F32) w[0] = __float_as_uint(s[0]);
+      else w[0] = s[0];
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = elem16<DT>(v, e);
+      for (int k = 0; k < kWords; k += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(s) + 4 * k);
+        w[k] = v.x; w[k + 1] = v.y; w[k + 2] = v.z; w[k + 3] = v.w;
+      }
+    }
   }
-}
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (DT == SPA_F32) return __uint_as_float(w[e]);
+    else {
+      const uint32_t h = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
+      return DT == SPA_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+    }
+  }
+};
 template <int DT, int VEC>
 __device__ __forceinline__ void store_vec(void* p, size_t i, const float (&v)[VEC]) {
   using T = typename Dt<DT>::T;
@@ -45,28 +57,47 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const float (&v)[VE
   }
 }
 
-// Sum over the workgroup, the same bits on every thread.  s_tmp: 16 floats; `flip` alternates the halves of a
-// 32-float buffer so that one barrier per reduction is enough.
-__device__ __forceinline__ float group_sum(float v, float* s_buf, int& flip) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROW_MASK, 0xF, false));
+}
+// Sum over the wave in a fixed order, the same on every lane (pairs, quads, 8, 16, then the four rows).
+__device__ __forceinline__ float wave_sum_f(float v) {
+  v += dpp_f<0xB1, 0xF>(v);
+  v += dpp_f<0x4E, 0xF>(v);
+  v += dpp_f<0x141, 0xF>(v);
+  v += dpp_f<0x140, 0xF>(v);
+  v += dpp_f<0x142, 0xA>(v);
+  v += dpp_f<0x143, 0xC>(v);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// Sum over the workgroup, the same on every thread.  Two buffers of 16 floats in turn, so that one barrier per
+// sum is enough (a buffer is written again only after the barrier of the sum between).
+__device__ __forceinline__ float group_sum(float v, float (&s_buf)[2][16], int& flip) {
+  v = wave_sum_f(v);
   const int waves = blockDim.x / kWave;
   if (waves == 1) return v;
-  float* s = s_buf + 16 * flip;
+  float* s = s_buf[flip];
   flip ^= 1;
   if ((threadIdx.x & (kWave - 1)) == 0) s[threadIdx.x / kWave] = v;
   __syncthreads();
-  float total = 0.f;
-  for (int w = 0; w < waves; ++w) total += s[w];
-  return total;
+  // every row of 16 lanes adds the waves' sums the same way
+  const int w = threadIdx.x & 15;
+  v = w < waves ? s[w] : 0.f;
+  v += dpp_f<0xB1, 0xF>(v);
+  v += dpp_f<0x4E, 0xF>(v);
+  v += dpp_f<0x141, 0xF>(v);
+  return v + dpp_f<0x140, 0xF>(v);
 }
 
-// v[U][VEC] <- N(v); elements past the row (live[u] false) hold anything and are not counted.
-template <int DT, int VEC, int U>
-__device__ __forceinline__ void norm_row(float (&v)[U][VEC], const bool (&live)[U], const spa_norm& n, int c, float eps,
-                                         const float (&w)[U][VEC], const float (&b)[U][VEC], float* s_buf, int& flip) {
+// v <- N(v); elements past the row (live false) hold anything and are not counted.  The weights are in w and b, or,
+// with kLate, read here.
+template <int DT, int VEC, int U, bool kLate>
+__device__ __forceinline__ void norm_row(float (&v)[U][VEC], const bool (&live)[U], const int (&at)[U], const spa_norm& n,
+                                         float inv_c, float eps, const Stored<DT, VEC> (&w)[U],
+                                         const Stored<DT, VEC> (&b)[U], float (&s_buf)[2][16], int& flip) {
   if (n.kind == SPA_NORM_NONE) return;
-  const float inv_c = 1.f / (float)c;
   if (n.kind == SPA_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
@@ -88,52 +119,106 @@ __device__ __forceinline__ void norm_row(float (&v)[U][VEC], const bool (&live)[
       for (int e = 0; e < VEC; ++e) q += v[u][e] * v[u][e];
   const float r = 1.f / sqrtf(group_sum(q, s_buf, flip) * inv_c + eps);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    Stored<DT, VEC> lw = w[u], lb = b[u];
+    if constexpr (kLate) {
+      if (live[u] && n.weight) lw.load(n.weight, at[u]);
+      if (live[u] && n.bias) lb.load(n.bias, at[u]);
+    }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[u][e] = v[u][e] * r * w[u][e] + b[u][e];
+    for (int e = 0; e < VEC; ++e) {
+      float x = v[u][e] * r;
+      if (n.weight) x *= lw.at(e);
+      if (n.bias) x += lb.at(e);
+      v[u][e] = x;
+    }
+  }
 }
 
+// kAhead: the weights stay in registers and the next row is read while this one is worked on.  Rows that need more
+// than 8 elements of a thread have no registers for that; there one workgroup takes one row and reads the gate and
+// the weights (from L2) where they are used.
 template <int DT, int ST, int VEC, int U>
 __global__ void __launch_bounds__(1024) k_gated_norm(NormArgs a) {
-  __shared__ float s_buf[32];
-  const size_t row = (size_t)blockIdx.x * a.c;
+  constexpr bool kAhead = U * VEC <= 8;
+  __shared__ float s_buf[2][16];
   int flip = 0;
-  float v[U][VEC], res[U][VEC], gate[U][VEC], pw[U][VEC], pb[U][VEC], nw[U][VEC], nb[U][VEC];
+  int at[U];
   bool live[U];
+  Stored<DT, VEC> pw[U], pb[U], nw[U], nb[U], x[U], gate[U];
+  Stored<ST, VEC> res[U];
+  auto fetch = [&](int row) {
+    const size_t base = (size_t)row * a.c;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!live[u]) continue;
+      x[u].load(a.x, base + at[u]);
+      if (a.residual) res[u].load(a.residual, base + at[u]);
+      if (kAhead && a.gate_per_token) gate[u].load(a.gate, base + at[u]);
+    }
+  };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int i = (u * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    live[u] = i < a.c;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[u][e] = res[u][e] = pb[u][e] = nb[u][e] = 0.f, gate[u][e] = pw[u][e] = nw[u][e] = 1.f;
-    if (!live[u]) continue;
-    load_vec<DT, VEC>(a.x, row + i, v[u]);
-    if (a.residual) load_vec<ST, VEC>(a.residual, row + i, res[u]);
-    if (a.gate) load_vec<DT, VEC>(a.gate, (a.gate_per_token ? row : 0) + i, gate[u]);
-    if (a.post.weight) load_vec<DT, VEC>(a.post.weight, i, pw[u]);
-    if (a.post.bias) load_vec<DT, VEC>(a.post.bias, i, pb[u]);
-    if (a.pre.weight) load_vec<DT, VEC>(a.pre.weight, i, nw[u]);
-    if (a.pre.bias) load_vec<DT, VEC>(a.pre.bias, i, nb[u]);
+    at[u] = (u * (int)blockDim.x + (int)threadIdx.x) * VEC;
+    live[u] = at[u] < a.c;
   }
-  norm_row<DT, VEC, U>(v, live, a.post, a.c, a.eps, pw, pb, s_buf, flip);
+  int row = blockIdx.x;
+  fetch(row);
+  if constexpr (kAhead) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[u][e] = res[u][e] + a.scale * (gate[u][e] * v[u][e]);
-    if (a.h && live[u]) store_vec<ST, VEC>(a.h, row + (u * (int)blockDim.x + (int)threadIdx.x) * VEC, v[u]);
+    for (int u = 0; u < U; ++u) {
+      if (!live[u]) continue;
+      if (a.gate && !a.gate_per_token) gate[u].load(a.gate, at[u]);
+      if (a.post.weight) pw[u].load(a.post.weight, at[u]);
+      if (a.post.bias) pb[u].load(a.post.bias, at[u]);
+      if (a.pre.weight) nw[u].load(a.pre.weight, at[u]);
+      if (a.pre.bias) nb[u].load(a.pre.bias, at[u]);
+    }
   }
-  if (!a.y) return;
-  norm_row<DT, VEC, U>(v, live, a.pre, a.c, a.eps, nw, nb, s_buf, flip);
+  const float inv_c = 1.f / (float)a.c;
+  for (; row < a.t; row += gridDim.x) {
+    const size_t base = (size_t)row * a.c;
+    float v[U][VEC];
+    Stored<DT, VEC> g[U];
+    Stored<ST, VEC> r[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (live[u]) store_vec<DT, VEC>(a.y, row + (u * (int)blockDim.x + (int)threadIdx.x) * VEC, v[u]);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[u][e] = x[u].at(e);
+      r[u] = res[u];
+      g[u] = gate[u];
+      if (!kAhead && a.gate && live[u]) g[u].load(a.gate, (a.gate_per_token ? base : 0) + at[u]);
+    }
+    // the rows of this workgroup are its own: the next one is read before this one's outputs are written
+    if (kAhead && row + (int)gridDim.x < a.t) fetch(row + gridDim.x);
+    norm_row<DT, VEC, U, !kAhead>(v, live, at, a.post, inv_c, a.eps, pw, pb, s_buf, flip);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float k = a.gate ? a.scale * g[u].at(e) : a.scale;
+        v[u][e] = (a.residual ? r[u].at(e) : 0.f) + k * v[u][e];
+      }
+      if (a.h && live[u]) store_vec<ST, VEC>(a.h, base + at[u], v[u]);
+    }
+    if (!a.y) continue;
+    norm_row<DT, VEC, U, !kAhead>(v, live, at, a.pre, inv_c, a.eps, nw, nb, s_buf, flip);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (live[u]) store_vec<DT, VEC>(a.y, base + at[u], v[u]);
+  }
 }
+
+constexpr int kUnits = 256;              // compute units
+constexpr int kResident = 1024;          // threads of a unit that walk over rows
 
 template <int DT, int ST, int VEC, int U>
 hipError_t go(const NormArgs& a, hipStream_t st) {
   const int per = VEC * U;
   const int threads = ((a.c + per - 1) / per + kWave - 1) / kWave * kWave;
-  hipLaunchKernelGGL((k_gated_norm<DT, ST, VEC, U>), dim3(a.t), dim3(threads), 0, st, a);
+  // one workgroup to a row, or as many as the chip holds where they walk over rows
+  const int places = U * VEC <= 8 ? kUnits * std::max(1, kResident / threads) : a.t;
+  hipLaunchKernelGGL((k_gated_norm<DT, ST, VEC, U>), dim3(std::min(a.t, places)), dim3(threads), 0, st, a);
   return hipGetLastError();
 }
 
