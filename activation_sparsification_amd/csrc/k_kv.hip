@@ -3,8 +3,8 @@
 //
 // Both move every byte once: a vector of head_dim elements is held by a group of LG lanes, 8 elements each, so
 // its largest magnitude is a butterfly over the group and nothing passes through memory twice.  A workgroup
-// handles 16 (or more, for short vectors) consecutive tokens of one head, keys and values together: consecutive
-// tokens are consecutive positions of a page, so the codes and the 4-byte scales of a workgroup leave as runs.
+// handles consecutive tokens of one head, keys and values together: consecutive tokens are consecutive positions of
+// a page, so the codes and the 4-byte scales of a workgroup are runs.
 #include "spa_common.h"
 #include "spa_attn.h"
 #include "spa_layer.h"
@@ -70,20 +70,21 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
   const int lane = threadIdx.x % LG;
   const int head = blockIdx.x % a.heads;
   const int tok = (blockIdx.x / a.heads) * ROWS + threadIdx.x / LG;
+  // the vectors' loads do not wait for the slot: a skipped token's are read for nothing
+  uint4 raw[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    raw[s] = make_uint4(0, 0, 0, 0);
+    if (tok < a.t && lane * 8 < a.d)
+      raw[s] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[s]) + (size_t)tok * a.row_stride[s] +
+                                               (size_t)head * a.head_stride[s] + lane * 8);
+  }
   const int slot = tok < a.t ? a.slots[tok] : -1;
   const int page_size = a.page.d;
   const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
   const bool ok = slot >= 0 && pg < a.n_pages;                  // the whole group agrees
   const bool live = ok && lane * 8 < a.d;
   const size_t cell = ((size_t)pg * a.heads + head) * page_size + (slot - pg * page_size);
-  uint4 raw[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    raw[s] = make_uint4(0, 0, 0, 0);
-    if (live)
-      raw[s] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[s]) + (size_t)tok * a.row_stride[s] +
-                                               (size_t)head * a.head_stride[s] + lane * 8);
-  }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if constexpr (FMT == SPA_KV_NATIVE) {
@@ -99,56 +100,90 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
   }
 }
 
+// A wave takes kReadRows consecutive rows of one head.  Lane i finds row i's sequence, page and scales, all rows at
+// once, and the groups get them by lane exchange; then every load of the wave's rows is in flight together.
+constexpr int kReadRows = 16;
 template <int DT, int FMT, int LG>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
-  constexpr int ROWS = kThreads / LG, PER_WAVE = kWave / LG;
-  const int lane = threadIdx.x % LG;
+  constexpr int PER = kWave / LG, STEPS = (kReadRows + PER - 1) / PER;      // rows side by side, and one after the other
+  const int wl = threadIdx.x % kWave, lane = wl % LG;
   const int head = blockIdx.x % a.heads;
-  const int row = (blockIdx.x / a.heads) * ROWS + threadIdx.x / LG;
-  // this row's sequence: the number of offsets after the first that are at or below the row
-  const int wl = threadIdx.x % kWave;
-  const int first = row - wl / LG;                              // the wave's first row
+  const int first = (blockIdx.x / a.heads * (kThreads / kWave) + threadIdx.x / kWave) * kReadRows;
+  if (first >= a.t) return;                                     // the whole wave
+  const int row = first + wl % kReadRows;
+  // a row's sequence: the number of offsets after the first that are at or below it
   int seq = 0;
   for (int base = 0; base < a.n_seqs; base += kWave) {
     const int end = base + wl < a.n_seqs ? a.cu[base + wl + 1] : INT32_MAX;
-#pragma unroll
-    for (int r = 0; r < PER_WAVE; ++r) {
-      const int n = __popcll(__ballot(end <= first + r));
-      if (wl / LG == r) seq += n;
-    }
+    const int low = __popcll(__ballot(end <= first)), high = __popcll(__ballot(end <= first + kReadRows - 1));
+    seq += low;
+    for (int i = low; i < high; ++i) seq += __shfl(end, i, kWave) <= row;      // sequences that end within the rows
   }
-  const bool mine = row < a.t && seq < a.n_seqs && lane * 8 < a.d;
-  if (!mine) return;
-  const int pos = row - a.cu[seq];
   const int page_size = a.page.d;
-  const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
-  const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
-  const bool ok = pg >= 0 && pg < a.n_pages;
-  const size_t cell = ok ? ((size_t)pg * a.heads + head) * page_size + (pos - col * page_size) : 0;
-  const size_t to = ((size_t)row * a.heads + head) * a.d + lane * 8;
+  bool ok = row < a.t && seq < a.n_seqs;
+  const bool mine = ok;
+  int cell = 0;
+  if (ok) {
+    const int pos = row - a.cu[seq];
+    const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
+    const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
+    ok = pg >= 0 && pg < a.n_pages;
+    if (ok) cell = (pg * a.heads + head) * page_size + (pos - col * page_size);
+  }
+  float sc[2] = {0.f, 0.f};
+  if constexpr (FMT != SPA_KV_NATIVE) {
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok) {
-      if constexpr (FMT == SPA_KV_NATIVE) {
-        v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.pages[s]) + cell * a.d + lane * 8);
-      } else {
-        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.pages[s]) + cell * a.d + lane * 8);
-        const float sc = a.scale[s][cell];
-        float x[8];
-        codes_to_f32<FMT>(c.x, x);
-        codes_to_f32<FMT>(c.y, x + 4);
-        v = make_uint4(pack2<DT>(x[0] * sc, x[1] * sc), pack2<DT>(x[2] * sc, x[3] * sc),
-                       pack2<DT>(x[4] * sc, x[5] * sc), pack2<DT>(x[6] * sc, x[7] * sc));
+    for (int s = 0; s < 2; ++s)
+      if (ok) sc[s] = a.scale[s][cell];
+  }
+  const uint32_t there = (uint32_t)__ballot(ok), write = (uint32_t)__ballot(mine);
+  constexpr int W = FMT == SPA_KV_NATIVE ? 4 : 2;
+  uint32_t raw[STEPS][2][W];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = i * PER + wl / LG;
+    const size_t c = (uint32_t)__shfl(cell, r & (kReadRows - 1), kWave);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) raw[i][s][w] = 0;
+      if (r < kReadRows && (there >> r) & 1u && lane * 8 < a.d) {
+        if constexpr (FMT == SPA_KV_NATIVE) {
+          const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.pages[s]) + c * a.d + lane * 8);
+          raw[i][s][0] = v.x; raw[i][s][1] = v.y; raw[i][s][2] = v.z; raw[i][s][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.pages[s]) + c * a.d + lane * 8);
+          raw[i][s][0] = v.x; raw[i][s][1] = v.y;
+        }
       }
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[s]) + to) = v;
+  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = i * PER + wl / LG;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint4 v;
+      if constexpr (FMT == SPA_KV_NATIVE) {
+        v = make_uint4(raw[i][s][0], raw[i][s][1], raw[i][s][2], raw[i][s][3]);
+      } else {
+        const float k = __shfl(sc[s], r & (kReadRows - 1), kWave);
+        float x[8];
+        codes_to_f32<FMT>(raw[i][s][0], x);
+        codes_to_f32<FMT>(raw[i][s][1], x + 4);
+        v = make_uint4(pack2<DT>(x[0] * k, x[1] * k), pack2<DT>(x[2] * k, x[3] * k), pack2<DT>(x[4] * k, x[5] * k),
+                       pack2<DT>(x[6] * k, x[7] * k));
+      }
+      if (r < kReadRows && (write >> r) & 1u && lane * 8 < a.d)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[s]) + ((size_t)(first + r) * a.heads + head) * a.d + lane * 8) = v;
+    }
   }
 }
 
 template <int DT, int FMT, int LG>
 hipError_t go(bool write, const KvArgs& a, hipStream_t st) {
-  const int64_t blocks = ((int64_t)a.t * LG + kThreads - 1) / kThreads * a.heads;
+  const int rows = write ? kThreads / LG : kThreads / kWave * kReadRows;      // of a workgroup
+  const int64_t blocks = ((int64_t)a.t + rows - 1) / rows * a.heads;
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   if (write) hipLaunchKernelGGL((k_kv_write<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
   else hipLaunchKernelGGL((k_kv_read<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
