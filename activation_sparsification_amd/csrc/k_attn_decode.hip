@@ -52,10 +52,11 @@ struct DecodeAttnArgs {
 // max / 127: with a largest value of 1, 2^8 / 448 and 2^6 / 127 are about a half.
 template <int FMT> constexpr float kPScale = FMT == SPA_KV_FP8 ? 256.f : FMT == SPA_KV_INT8 ? 64.f : 1.f;
 
-__device__ __forceinline__ int seq_tiles(const DecodeAttnArgs& a, int s) {
-  const int cap = a.max_pages * (int)a.page.d;
-  return (min(max(a.lens[s], 0), cap) + kTile - 1) / kTile;
+// Positions of sequence s that can count, and their tiles.
+__device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int s) {
+  return min(max(a.lens[s], 0), a.max_pages * (int)a.page.d);
 }
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 // What a workgroup works through: `per` consecutive tiles of all sequences' tiles laid end to end, so every
 // workgroup of a head has the same share whatever the lengths.  An empty sequence stands as one tile of nothing.
@@ -64,6 +65,7 @@ struct Span {
   int seq, local;              // where the next piece starts: sequence, tile within it
   int left;                    // tiles still to do
   bool fresh;                  // nothing done yet
+  int lens;                    // lane i: the positions of sequence i < 64
 };
 // One piece of a sequence, for one key-value head and up to 16 of its query heads.
 struct Piece {
@@ -73,11 +75,12 @@ struct Piece {
   bool whole;                  // the sequence is this piece alone
   int slot;                    // where the piece's sums go if not: two slots to a workgroup
 };
-__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(seq_tiles(a, s), 1); }
+__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(tiles_of(seq_len(a, s)), 1); }
 
 __device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int c0 = lane < a.n_seqs ? seq_share(a, lane) : 0;
+  s.lens = lane < a.n_seqs ? seq_len(a, lane) : 0;
+  const int c0 = lane < a.n_seqs ? max(tiles_of(s.lens), 1) : 0;
   const int incl0 = wave_scan(c0);
   long long total = __builtin_amdgcn_readlane(incl0, kWave - 1);
   for (int base = kWave; base < a.n_seqs; base += kWave) {
@@ -114,8 +117,8 @@ __device__ __forceinline__ Piece next_piece(const DecodeAttnArgs& a, Span& s) {
   p.head = blockIdx.y % a.hkv;
   p.heads = min(a.group - 16 * ht, 16);
   p.h0 = p.head * a.group + 16 * ht;
-  p.len = min(max(a.lens[s.seq], 0), a.max_pages * (int)a.page.d);
-  const int tiles = (p.len + kTile - 1) / kTile, share = max(tiles, 1);
+  p.len = s.seq < kWave ? __builtin_amdgcn_readlane(s.lens, s.seq) : seq_len(a, s.seq);
+  const int tiles = tiles_of(p.len), share = max(tiles, 1);
   const int take = min(share - s.local, s.left);
   p.begin = s.local;
   p.end = min(s.local + take, tiles);
@@ -642,7 +645,7 @@ hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads
   a.n_seqs = n_seqs; a.hq = n_q_heads; a.hkv = c.n_heads; a.group = n_q_heads / c.n_heads;
   a.d = c.head_dim; a.n_pages = c.n_pages; a.max_pages = max_pages;
   a.head_tiles = spa_check::head_tiles(n_q_heads, c.n_heads);
-  a.target = spa_check::decode_groups(n_q_heads, c.n_heads);
+  a.target = spa_check::decode_groups(n_q_heads, c.n_heads, c.head_dim);
   a.c = scale * kLog2e;
   a.page = FastDiv((uint32_t)c.page_size);
   return c.dtype == SPA_F16 ? by_format<SPA_F16>(c.format, a, st) : by_format<SPA_BF16>(c.format, a, st);

@@ -91,12 +91,12 @@ inline spa_status check_attention_decode(const spa_heads* q, int32_t n_seqs, int
 
 // Query heads of one key-value head are worked on 16 at a time (the matrix instruction's columns).
 inline int head_tiles(int n_q_heads, int n_kv_heads) { return (n_q_heads / n_kv_heads + 15) / 16; }
-// Workgroups that share the cache of one key-value head and head tile: together about kDecodeTarget, so that all
-// of them are on the chip at once (two to each compute unit).
-constexpr int kDecodeTarget = 512;
-inline int decode_groups(int n_q_heads, int n_kv_heads) {
+// Workgroups that share the cache of one key-value head and head tile: as many as the chip holds at a time over all
+// heads, 3, 2 or 1 to a compute unit as the registers for the head's dimensions allow.
+inline int decode_groups(int n_q_heads, int n_kv_heads, int head_dim) {
+  const int places = head_dim <= 64 ? 768 : head_dim <= 128 ? 512 : 256;
   const int per_unit = n_kv_heads * head_tiles(n_q_heads, n_kv_heads);
-  return (kDecodeTarget + per_unit - 1) / per_unit;
+  return (places + per_unit - 1) / per_unit;
 }
 struct DecodeAttnPlan {
   // [2 groups][heads][head_dim] float32 partial outputs, [2 groups][heads][2] maximum and sum, [n_seqs][2] first slot
@@ -105,7 +105,7 @@ struct DecodeAttnPlan {
 };
 inline DecodeAttnPlan decode_attn_plan(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
   DecodeAttnPlan p{};
-  const size_t rows = (size_t)2 * decode_groups(n_q_heads, n_kv_heads) * n_q_heads;
+  const size_t rows = (size_t)2 * decode_groups(n_q_heads, n_kv_heads, head_dim) * n_q_heads;
   p.o = 0;
   p.ml = round256(rows * head_dim * 4);
   p.of = p.ml + round256(rows * 8);
