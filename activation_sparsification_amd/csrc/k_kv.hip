@@ -184,7 +184,6 @@ template <int DT, int FMT, int LG>
 hipError_t go(bool write, const KvArgs& a, hipStream_t st) {
   const int rows = write ? kThreads / LG : kThreads / kWave * kReadRows;      // of a workgroup
   const int64_t blocks = ((int64_t)a.t + rows - 1) / rows * a.heads;
-  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   if (write) hipLaunchKernelGGL((k_kv_write<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
   else hipLaunchKernelGGL((k_kv_read<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();

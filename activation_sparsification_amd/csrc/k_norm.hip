@@ -136,8 +136,8 @@ __device__ __forceinline__ void norm_row(float (&v)[U][VEC], const bool (&live)[
 }
 
 // kAhead: the weights stay in registers and the next row is read while this one is worked on.  Rows that need more
-// than 8 elements of a thread have no registers for that; there one workgroup takes one row and reads the gate and
-// the weights (from L2) where they are used.
+// than 8 elements of a thread have no registers for that; there a workgroup takes one row (up to 2^20 of them) and
+// reads the gate and the weights (from L2) where they are used.
 template <int DT, int ST, int VEC, int U>
 __global__ void __launch_bounds__(1024) k_gated_norm(NormArgs a) {
   constexpr bool kAhead = U * VEC <= 8;
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(1024) k_gated_norm(NormArgs a) {
     live[u] = at[u] < a.c;
   }
   int row = blockIdx.x;
-  fetch(row);
   if constexpr (kAhead) {
+    fetch(row);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!live[u]) continue;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(1024) k_gated_norm(NormArgs a) {
   }
   const float inv_c = 1.f / (float)a.c;
   for (; row < a.t; row += gridDim.x) {
+    if constexpr (!kAhead) fetch(row);
     const size_t base = (size_t)row * a.c;
     float v[U][VEC];
     Stored<DT, VEC> g[U];
@@ -217,7 +218,7 @@ hipError_t go(const NormArgs& a, hipStream_t st) {
   const int per = VEC * U;
   const int threads = ((a.c + per - 1) / per + kWave - 1) / kWave * kWave;
   // one workgroup to a row, or as many as the chip holds where they walk over rows
-  const int places = U * VEC <= 8 ? kUnits * std::max(1, kResident / threads) : a.t;
+  const int places = U * VEC <= 8 ? kUnits * std::max(1, kResident / threads) : 1 << 20;
   hipLaunchKernelGGL((k_gated_norm<DT, ST, VEC, U>), dim3(std::min(a.t, places)), dim3(threads), 0, st, a);
   return hipGetLastError();
 }

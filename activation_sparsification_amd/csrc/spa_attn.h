@@ -2,6 +2,7 @@
 #pragma once
 
 #include "spa_common.h"
+#include "spa_div.h"
 
 namespace spa {
 
@@ -10,22 +11,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// Division of an unsigned number below 2^31 by a divisor of 1..2^31 - 1 fixed for the launch: with s =
-// ceil(log2 d) and m = ceil(2^(31 + s) / d), floor(x * m / 2^(31 + s)) = floor(x / d) for every x < 2^31 (the
-// excess of m over 2^(31+s)/d is below 1, so the product is high by less than x / 2^(31+s) <= 1 / d).
-struct FastDiv {
-  uint32_t d, m, s;
-  FastDiv() = default;
-  explicit __host__ __device__ FastDiv(uint32_t div) : d(div) {
-    s = 0;
-    while ((1ull << s) < div) ++s;
-    m = (uint32_t)(((1ull << (31 + s)) + div - 1) / div);       // below 2^32: 2^s < 2 d
-  }
-  __host__ __device__ __forceinline__ uint32_t div(uint32_t x) const {
-    return (uint32_t)(((uint64_t)x * m) >> (31 + s));
-  }
-};
 
 // Four 8-bit codes as float32.
 template <int FMT>

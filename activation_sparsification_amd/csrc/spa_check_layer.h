@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "spa.h"
 #include "spa_check.h"
 
@@ -15,6 +17,7 @@ namespace spa_check {
 constexpr int32_t kMaxHeads = 1 << 12;
 constexpr int32_t kMaxHeadDim = 256;
 constexpr int32_t kMaxRows = 1 << 30;             // packed rows of a call
+constexpr int64_t kMaxVectors = int64_t(1) << 26;  // (token, head) pairs of a cache call: the launch counts threads in 32 bits
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 23;  // elements between rows: 64 rows of it stay below 2^31 bytes
 constexpr int64_t kMaxPositions = int64_t(1) << 29;    // of one sequence's table: 64 sequences' tiles add up in 31 bits
@@ -56,6 +59,7 @@ inline spa_status check_kv_write(const spa_heads* k, const spa_heads* v, int32_t
   if (t == 0) return s;
   if (!valid_heads(k) || !valid_heads(v) || !slots || !valid_strides(k) || !valid_strides(v)) return SPA_ERR_INVALID;
   if (s != SPA_OK) return s;
+  if ((int64_t)t * c->n_heads > kMaxVectors) return SPA_ERR_UNSUPPORTED;
   return built_heads(k) && built_heads(v) ? SPA_OK : SPA_ERR_UNSUPPORTED;
 }
 
@@ -66,6 +70,7 @@ inline spa_status check_kv_read(const spa_kv_cache* c, const int32_t* table, int
   if (s == SPA_ERR_INVALID) return s;
   if (n_seqs == 0 || total == 0) return s;
   if (max_pages < 1 || !table || !cu || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SPA_ERR_INVALID;
+  if (s == SPA_OK && (int64_t)total * c->n_heads > kMaxVectors) return SPA_ERR_UNSUPPORTED;
   return s;
 }
 
