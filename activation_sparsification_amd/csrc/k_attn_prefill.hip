@@ -190,17 +190,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   const int full = visible_end(w0, lq, lk, a.causal);                                     // keys that all its wave sees
   const int wave_end = min(visible_end(w0 + kWaveRows - 1, lq, lk, a.causal), k_end);     // and that any does
 
-  uint4 qf[KS];
-  {
-    const uint16_t* q = a.q + (size_t)(q_first + min(row, lq - 1)) * a.q_row + (size_t)head * a.q_head;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int at = 16 * s + 8 * g;
-      qf[s] = make_uint4(0, 0, 0, 0);
-      if (at < a.d) qf[s] = *reinterpret_cast<const uint4*>(q + at);
-    }
-  }
-
   // a tile's direct loads: lane -> (row, stored piece); rows past the end repeat the last one, pieces past
   // head_dim repeat the first (they meet zeros of Q, or give columns of O that are not stored)
   const uint16_t* kbase = a.k + (size_t)k_first * a.k_row + (size_t)kvh * a.k_head;
@@ -223,6 +212,21 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   auto stage_v = [&](int j0, int buf) {
     if (j0 < k_end) stage(vbase, a.v_row, j0, lds_addr(s_kv) + (2 + buf) * kTileBytes);
   };
+
+  // the first keys, the queries, the keys after and the first values: all on their way at once
+  stage_k(k_begin, 0);
+  uint4 qf[KS];
+  {
+    const uint16_t* q = a.q + (size_t)(q_first + min(row, lq - 1)) * a.q_row + (size_t)head * a.q_head;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int at = 16 * s + 8 * g;
+      qf[s] = make_uint4(0, 0, 0, 0);
+      if (at < a.d) qf[s] = *reinterpret_cast<const uint4*>(q + at);
+    }
+  }
+  if constexpr (kAhead) stage_k(k_begin + BN, 1);
+  stage_v(k_begin, 0);
 
   f32x16 o[DB];
 #pragma unroll
@@ -353,13 +357,10 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
 
   if (k_begin < k_end) {
     int j0 = k_begin, buf = 0;
-    stage_k(j0, 0);
     if constexpr (kAhead) {
       wait_vm<0>(0);
       bare_barrier();
-      stage_k(j0 + BN, 1);
     }
-    stage_v(j0, 0);
     if constexpr (!kAhead) {
       for (; j0 < wave_end; j0 += BN, buf ^= 1) {
         arrive(j0, buf);

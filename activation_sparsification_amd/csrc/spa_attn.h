@@ -51,14 +51,18 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Inclusive sum over the lanes of a wave.
+// Inclusive sum over the lanes of a wave, by DPP: shifts within rows of 16, then the rows before.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
+}
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int o = __shfl_up(v, off, kWave);
-    if (lane >= off) v += o;
-  }
+  v += dpp_i<0x111, 0xF>(v);   // row_shr 1
+  v += dpp_i<0x112, 0xF>(v);   // row_shr 2
+  v += dpp_i<0x114, 0xF>(v);   // row_shr 4
+  v += dpp_i<0x118, 0xF>(v);   // row_shr 8
+  v += dpp_i<0x142, 0xA>(v);   // row_bcast15 -> rows 1, 3
+  v += dpp_i<0x143, 0xC>(v);   // row_bcast31 -> rows 2, 3
   return v;
 }
 
