@@ -95,9 +95,10 @@ __device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
   long long before = 0;
   int c = c0, incl = incl0, base = 0;
   uint64_t past;
-  while (!(past = __ballot(before + incl > start))) {          // ends: start is below the total
+  while (!(past = __ballot(before + incl > start))) {
     before += __builtin_amdgcn_readlane(incl, kWave - 1);
     base += kWave;
+    if (base >= a.n_seqs) return false;
     c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
     incl = wave_scan(c);
   }
