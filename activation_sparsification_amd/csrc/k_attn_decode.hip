@@ -206,6 +206,29 @@ __device__ __forceinline__ uint4 stream_load16(const void* p) {
   const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// The first `live` of W words, the others 0 (live is W, W / 2 or 0: whole 8-element pieces).
+template <int W>
+__device__ __forceinline__ void stream_load(const char* p, int live, uint32_t (&w)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = 0;
+  if constexpr (W == 1) {
+    if (live) w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+  } else {
+    constexpr int kStep = W >= 8 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < W; i += kStep) {
+      if (i < live) {
+        if constexpr (kStep == 4) {
+          const uint4 v = stream_load16(p + 4 * i);
+          w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        } else {
+          const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + 4 * i));
+          w[i] = v[0]; w[i + 1] = v[1];
+        }
+      }
+    }
+  }
+}
 template <int W>
 __device__ __forceinline__ void stream_load(const char* p, uint32_t (&w)[W]) {
   if constexpr (W == 1) {
@@ -268,7 +291,7 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
   __syncthreads();      // the next piece writes here again
 }
 
-// Any page size and head_dim: a lane finds one position's cell and the others get it by lane exchange.
+// Any page size: a lane finds one position's cell and the others get it by lane exchange.
 template <int DT, int FMT, int DP>
 __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnArgs a) {
   constexpr int KC = DP / 32;      // k steps of S
@@ -379,10 +402,10 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
   } while (span.left > 0);
 }
 
-// Pages of whole 16-position blocks and head_dim == DP: a block's rows are consecutive, so a tile has two bases that
-// the whole wave shares.  The page numbers of a wave's next 32 tiles are held one to a lane; keys of the next
+// Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave
+// shares.  EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  The page numbers of a wave's next 32 tiles are held one to a lane; keys of the next
 // tile are on their way while this tile's softmax and V product run, and values while its scores are formed.
-template <int DT, int FMT, int DP>
+template <int DT, int FMT, int DP, bool EXACT>
 __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(DecodeAttnArgs a) {
   constexpr int KC = DP / 32, NV = DP / 16;
   constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1;
@@ -425,13 +448,31 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
     };
     uint4 kr[2][KL];
     float4 ksc[2], vsc[2];
-    const uint32_t k_lane = (uint32_t)(col * DP * ES + 16 * g), v_lane = (uint32_t)((4 * g * DP + NV * col) * ES);
+    const int d = EXACT ? DP : a.d;
+    const uint32_t k_lane = (uint32_t)(col * d * ES + 16 * g), v_lane = (uint32_t)((4 * g * d + NV * col) * ES);
+    const int v_live = EXACT ? VW : min(max((d - NV * col) / 4 * ES, 0), VW);      // words of a value row: ES for 4 elements
     auto load_k = [&](const uint32_t (&cell)[2]) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (DP * ES);
+        const char* base = static_cast<const char*>(a.k) + (size_t)cell[b] * (uint32_t)(d * ES);
 #pragma unroll
-        for (int c = 0; c < KL; ++c) kr[b][c] = stream_load16(base + (k_lane + 64 * c));
+        for (int c = 0; c < KL; ++c) {
+          if constexpr (EXACT) {
+            kr[b][c] = stream_load16(base + (k_lane + 64 * c));
+          } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+            const int bytes = d * ES - (16 * g + 64 * c);              // left in the row; whole 8-element pieces
+            const char* from = base + (k_lane + 64 * c);
+            if (bytes >= 16) {
+              const uint4 v = stream_load16(from);
+              w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else if (bytes > 0) {
+              w[0] = reinterpret_cast<const uint32_t*>(from)[0];
+              w[1] = reinterpret_cast<const uint32_t*>(from)[1];
+            }
+            kr[b][c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
         if constexpr (FMT != SPA_KV_NATIVE) {
           ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
           vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
@@ -453,8 +494,9 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
       uint32_t vraw[8][VW];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (DP * ES);
-        stream_load<VW>(base + (v_lane + (j % 4) * DP * ES), vraw[j]);
+        const char* base = static_cast<const char*>(a.v) + (size_t)cell[j / 4] * (uint32_t)(d * ES);
+        if constexpr (EXACT) stream_load<VW>(base + (v_lane + (j % 4) * DP * ES), vraw[j]);
+        else stream_load<VW>(base + (v_lane + (j % 4) * d * ES), v_live, vraw[j]);
       }
       // scores
       f32x4 s[2];
@@ -636,7 +678,10 @@ hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
   const int64_t room = ((int64_t)a.max_pages * a.page.d + kTile - 1) / kTile;
   const int units = (int)std::min<int64_t>(a.target, (std::max<int64_t>(room, 1) * a.n_seqs + kMinTiles - 1) / kMinTiles);
   const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
-  if (a.page.d % 16 == 0 && a.d == DP) hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP>), grid, block, 0, st, a);
+  if (a.page.d % 16 == 0 && a.d == DP)
+    hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP, true>), grid, block, 0, st, a);
+  else if (a.page.d % 16 == 0)
+    hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP, false>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), grid, block, 0, st, a);
   if (hipError_t e = hipGetLastError()) return e;
   // one workgroup to a head cuts nothing
