@@ -177,7 +177,7 @@ inline spa_status check_norm(const void* x, int32_t dtype, int32_t t, int32_t c,
   if (gate_rows != 0 && gate_rows != 1 && gate_rows != t) return SPA_ERR_INVALID;
   if (t == 0) return SPA_OK;
   if ((gate_rows != 0) != (gate != nullptr)) return SPA_ERR_INVALID;
-  if (!x || (!h && !y)) return SPA_ERR_INVALID;
+  if (!x || (!h && !y) || h == y) return SPA_ERR_INVALID;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gate) || !aligned16(h) || !aligned16(y)) return SPA_ERR_INVALID;
   for (const spa_norm* n : {post, pre})
     if (n && (!aligned16(n->weight) || !aligned16(n->bias))) return SPA_ERR_INVALID;

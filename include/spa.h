@@ -540,8 +540,8 @@ spa_status attention_prefill(const spa_heads* q, const spa_heads* k, const spa_h
  *            1) or [t][c] (gate_rows t); weights and biases [c]; all of dtype
  *  residual  [device] [t][c] stream_dtype (dtype, or SPA_F32) or NULL for 0
  *  h         [device] [t][c] stream_dtype, or NULL
- *  y         may be NULL if h is not; h may be residual itself, and y may be
- *            x itself
+ *  y         may be NULL if h is not (and must not be h); h may be residual
+ *            itself, and y may be x itself
  * t >= 0, c >= 1; c above 65536 is SPA_ERR_UNSUPPORTED.
  */
 typedef struct spa_norm {

@@ -77,6 +77,16 @@ def test_prompt_lengths(dev, lens_q, lens_k, causal):
     prompt_check(dev, F16, 2, 1, 128, lens_q, lens_k, causal, seed=1 + len(lens_q))
 
 
+@pytest.mark.parametrize("d", [40, 64, 128, 256])
+def test_prompt_divided_keys(dev, d):
+    # few rows over many keys: a tile's keys are divided and joined; rows that see nothing, pieces that some rows see
+    # nothing of, sequences too short to divide
+    for dtype, causal in ((BF16, True), (F16, True), (BF16, False)):
+        assert spa.lib().spa_attention_prefill_workspace_bytes(305, 3290, 3, 4, d) > 0
+        prompt_check(dev, dtype, 4, 2, d, [300, 5, 0], [290, 2900, 100], causal, seed=d)
+    prompt_check(dev, BF16, 4, 1, d, [1], [5000], True)
+
+
 def test_prompt_many_sequences(dev):
     lens = [(7 * i) % 41 for i in range(150)]
     prompt_check(dev, BF16, 2, 2, 64, lens, [x + i % 3 for i, x in enumerate(lens)], True)
@@ -305,6 +315,12 @@ def test_decode_many_sequences(dev):
     decode_check(dev, BF16, "native", 4, 2, 64, 8, [(13 * i) % 97 for i in range(200)], seed=3)
 
 
+def test_decode_long_among_short(dev):
+    # more sequences than a wave has lanes, and one that is cut many times in the middle of them
+    decode_check(dev, BF16, "fp8", 4, 2, 128, 16, [5] * 70 + [20000] + [0, 33] * 3, seed=5)
+    decode_check(dev, F16, "native", 4, 2, 64, 7, [5] * 70 + [3000] + [0, 33] * 3, seed=6)
+
+
 def test_decode_more_sequences_than_pieces(dev):
     decode_check(dev, F16, "fp8", 8, 8, 64, 16, [(31 * i) % 300 for i in range(400)], seed=4)
 
@@ -468,6 +484,13 @@ def norm_check(dev, dtype, stream, t, c, post, pre, gate, weights=True, offset=0
 def test_norm_sizes(dev, dtype, stream, t, c):
     norm_check(dev, dtype, stream, t, c, "rms", "rms", "channel")
     norm_check(dev, dtype, stream, t, c, "layer", "layer", "token", seed=1)
+
+
+@pytest.mark.parametrize("t,c", [(1500, 4096), (9000, 8), (3000, 512), (2100, 1000), (700, 9), (300, 16384)])
+def test_norm_many_rows(dev, t, c):
+    # more rows than workgroups on the chip: each walks over several
+    norm_check(dev, BF16, F32, t, c, "rms", "layer", "token")
+    norm_check(dev, F16, F16, t, c, "layer", "rms", "channel")
 
 
 @pytest.mark.parametrize("post", ["none", "rms", "layer"])

@@ -121,7 +121,7 @@ def test_norm_rejections(B):
     assert norm(t=0) == OK
     for kw in (dict(dtype=3), dict(st=-1), dict(t=-1), dict(c=0), dict(post=bad), dict(pre=bad), dict(eps=-1.0), dict(eps=math.nan),
                dict(scale=math.nan), dict(scale=math.inf), dict(gate=4096, rows=3), dict(gate=4096, rows=0), dict(rows=1),
-               dict(x=None), dict(h=None, y=None), dict(x=4104), dict(h=12290), dict(post=B._Norm(1, 4100, None))):
+               dict(x=None), dict(h=None, y=None), dict(h=4096, y=4096), dict(x=4104), dict(h=12290), dict(post=B._Norm(1, 4100, None))):
         assert norm(**kw) == INVALID, kw
     for kw in (dict(dtype=0, st=2), dict(dtype=1, st=2), dict(c=65537, pre=rms)):
         assert norm(**kw) == UNSUPPORTED, kw
