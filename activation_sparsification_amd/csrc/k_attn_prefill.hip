@@ -13,7 +13,7 @@
 //
 // Bound by the matrix cores and the vector unit together (32 exponentials of 16 cycles beside 32 matrix instructions
 // of 32 per lane and 64 keys).  One causal prompt of 8192 by 32 heads of 128 on 8: 523 us, 1051 TFLOP/s (a large
-// library product reaches 1112 on the same card), matrix cores busy 50 % at a sustained 1.98 GHz, no bank conflicts.
+// library product reaches 1112 on the same card), matrix cores busy 54 % at a sustained 1.98 GHz, no bank conflicts.
 // Nine prompts of up to 1531: 93 us; three pieces over 4093 cached keys by 16 heads of 64: 30 us.
 #include "spa_attn.h"
 #include "spa_layer.h"
