@@ -138,16 +138,33 @@ inline spa_status check_attention_prefill(const spa_heads* q, const spa_heads* k
 }
 
 // Pieces that the keys of a tile of 128 query rows are divided into when the call's tiles alone leave most of the
-// chip idle: as many as fill kPrefillTarget workgroups, up to 8.  The number of tiles is estimated (every sequence
-// ends with half a tile); sequences' keys stay on the device, where a piece is at least 4 key steps, so a call whose
-// keys altogether are no more than that is not divided.
+// chip idle: up to 8, and no more than fill two workgroups on each of 256 compute units.  The number of tiles is
+// estimated (every sequence ends with half a tile); sequences' keys stay on the device, where a piece is at least 4
+// key steps, so a call whose keys altogether are no more than that is not divided.  Of those the number is taken that
+// ends soonest by what was measured: a tile walks its keys at 400 + 6 head_dim ns per 64, whether one workgroup or
+// two stand on its unit (the longest of n sequences is taken as 2n / (n + 1) times their mean); a join costs 5 us, and
+// each piece 4 bytes per output element written and read at 4 TB/s.  Against pieces up to two workgroups on each unit
+// (us): a prompt of 700 by 32 heads of 128 26.4 -> 18.7, six of up to 300 by 16 19.2 -> 12.3, four of 300 18.3 ->
+// 12.4; worst 2000 by 8 heads 29.6 -> 31.5.  One workgroup to a unit takes 75 us for 4000 by 8 heads, this 59.
 constexpr int kPrefillTarget = 512, kMaxSplits = 8;
-inline int prefill_splits(int tq, int tk, int n_seqs, int n_q_heads) {
+inline int prefill_splits(int tq, int tk, int n_seqs, int n_q_heads, int head_dim) {
   const int64_t groups = ((int64_t)tq / 128 + (n_seqs + 1) / 2) * n_q_heads;
-  const int64_t most = tk / 256;
-  int64_t s = kPrefillTarget / (groups > 0 ? groups : 1);
-  s = s < most ? s : most;
-  return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+  int64_t most = kPrefillTarget / (groups > 0 ? groups : 1);
+  most = most < tk / 256 ? most : tk / 256;
+  most = most < kMaxSplits ? most : kMaxSplits;
+  const double longest = 2.0 * tk / (n_seqs + 1);
+  const double walk = longest / 64 * (400 + 6 * head_dim);      // ns
+  const double piece = double(tq) * n_q_heads * head_dim * 8 / 4000;
+  int best = 1;
+  double least = walk;
+  for (int s = 2; s <= most; ++s) {
+    const double t = walk / s + 5000 + piece * s;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
 struct PrefillAttnPlan {
   int splits;
@@ -155,7 +172,7 @@ struct PrefillAttnPlan {
 };
 inline PrefillAttnPlan prefill_attn_plan(int tq, int tk, int n_seqs, int n_q_heads, int head_dim) {
   PrefillAttnPlan p{};
-  p.splits = prefill_splits(tq, tk, n_seqs, n_q_heads);
+  p.splits = prefill_splits(tq, tk, n_seqs, n_q_heads, head_dim);
   if (p.splits == 1) return p;
   const size_t rows = (size_t)p.splits * tq * n_q_heads;
   p.ml = round256(rows * head_dim * 4);

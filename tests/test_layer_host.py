@@ -110,6 +110,15 @@ def test_attention_rejections(B):
     assert L.spa_attention_decode_workspace_bytes(4, 8, 2, 64) > 0
 
 
+def test_prompt_keys_are_divided_where_it_pays(B):
+    # the join costs more than it brings for short prompts that leave a unit one workgroup, less for long ones
+    need = B.lib().spa_attention_prefill_workspace_bytes
+    assert need(700, 700, 1, 32, 128) == 0
+    assert need(1200, 1200, 4, 16, 128) == 0
+    assert need(4000, 4000, 1, 8, 128) == 2 * 4000 * 8 * (128 * 4 + 8)
+    assert need(0, 0, 0, 8, 64) == 0
+
+
 def test_norm_rejections(B):
     L = B.lib()
 
