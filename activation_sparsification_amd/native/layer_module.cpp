@@ -116,12 +116,26 @@ int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? SPA_F32 : t == at::kHalf ? SPA_F16 : t == at::kBFloat16 ? SPA_BF16 : -1;
 }
 
+// Refuses a tensor whose storage no longer holds it (resized, or given back): elements up to the last one named by
+// sizes and strides.
+void held(const at::Tensor& x, const char* name) {
+  int64_t end = x.storage_offset() + 1;
+  for (int64_t i = 0; i < x.dim(); ++i) {
+    if (x.size(i) == 0) return;
+    end += (x.size(i) - 1) * x.stride(i);
+  }
+  if ((int64_t)x.storage().nbytes() < end * (int64_t)x.element_size())
+    refuse(std::string(name) + ": its storage is smaller than the tensor");
+}
+
 using Shape = std::initializer_list<int64_t>;
 // A contiguous tensor of exactly this shape, type and device.
 void given(const at::Tensor& x, Shape shape, at::ScalarType type, at::Device dev, const char* name) {
   if (x.scalar_type() == type && x.device() == dev && x.sizes() == c10::IntArrayRef(shape.begin(), shape.size()) &&
-      x.is_contiguous())
+      x.is_contiguous()) {
+    held(x, name);
     return;
+  }
   std::string s = std::string(name) + ": expected a contiguous " + c10::toString(type) + " tensor of shape [";
   for (auto it = shape.begin(); it != shape.end(); ++it) s += (it == shape.begin() ? "" : ", ") + std::to_string(*it);
   refuse(s + "] on " + dev.str());
@@ -133,6 +147,7 @@ spa_heads heads(const at::Tensor& x, const char* name) {
   if (!x.is_cuda()) refuse(std::string(name) + ": expected a device tensor");
   if (x.dim() != 3) refuse(std::string(name) + ": expected [rows, heads, head_dim]");
   if (x.size(2) > 1 && x.stride(2) != 1) refuse(std::string(name) + ": expected a dense last axis");
+  held(x, name);
   return spa_heads{x.data_ptr(), x.size(0) > 1 ? x.stride(0) : 0, x.size(1) > 1 ? x.stride(1) : 0};
 }
 
@@ -183,45 +198,51 @@ PyObject* guarded(F body) {
 // ---------------------------------------------------------------------------
 struct KvCache {
   PyObject_HEAD
-  PyObject* part[4];      // k, v, k_scale, v_scale
-  spa_kv_cache c;         // dtype is filled in for each call
+  PyObject* part[4];      // k, v, k_scale, v_scale; None or NULL where there are none
+};
+
+// What a cache's tensors are now.  They are looked at for each call: a program may give them other memory.
+struct Pages {
+  spa_kv_cache c;         // dtype is filled in by cache_for
   at::ScalarType type;
   at::Device dev;
 };
+Pages pages_of(PyObject* const (&p)[4]) {
+  need(p[0] && p[1], "KvCache: not initialised");
+  const at::Tensor &k = tensor(p[0], "KvCache.k"), &v = tensor(p[1], "KvCache.v");
+  need(k.is_cuda(), "KvCache: expected device tensors");
+  need(k.dim() == 4 && k.is_contiguous(), "KvCache: k is [n_pages, n_heads, page_size, head_dim], contiguous");
+  const at::ScalarType type = k.scalar_type();
+  const int64_t n = k.size(0), h = k.size(1), s = k.size(2), d = k.size(3);
+  given(k, {n, h, s, d}, type, k.device(), "KvCache.k");
+  given(v, {n, h, s, d}, type, k.device(), "KvCache.v");
+  spa_kv_cache c{};
+  c.format = type == at::kFloat8_e4m3fn ? SPA_KV_FP8 : type == at::kChar ? SPA_KV_INT8 : SPA_KV_NATIVE;
+  const bool scales[2] = {p[2] && p[2] != Py_None, p[3] && p[3] != Py_None};
+  if (c.format != SPA_KV_NATIVE) {
+    need(scales[0] && scales[1], "KvCache: 8-bit pages need k_scale and v_scale");
+    const at::Tensor &ks = tensor(p[2], "KvCache.k_scale"), &vs = tensor(p[3], "KvCache.v_scale");
+    given(ks, {n, h, s}, at::kFloat, k.device(), "KvCache.k_scale");
+    given(vs, {n, h, s}, at::kFloat, k.device(), "KvCache.v_scale");
+    c.k_scale = static_cast<float*>(ks.data_ptr());
+    c.v_scale = static_cast<float*>(vs.data_ptr());
+  } else {
+    need(dtype_code(type) >= 0, "KvCache: pages are float16, bfloat16, float8_e4m3fn or int8");
+    need(!scales[0] && !scales[1], "KvCache: scales belong to 8-bit pages");
+  }
+  c.n_pages = size32(n, "n_pages"); c.n_heads = size32(h, "n_heads");
+  c.page_size = size32(s, "page_size"); c.head_dim = size32(d, "head_dim");
+  c.k = k.data_ptr();
+  c.v = v.data_ptr();
+  return Pages{c, type, k.device()};
+}
 
 int cache_init(KvCache* self, PyObject* args, PyObject* kw) {
   static const char* names[] = {"k", "v", "k_scale", "v_scale", nullptr};
   PyObject* p[4] = {nullptr, nullptr, nullptr, nullptr};
   if (!PyArg_ParseTupleAndKeywords(args, kw, "OO|OO", const_cast<char**>(names), &p[0], &p[1], &p[2], &p[3])) return -1;
   PyObject* ok = guarded([&]() -> PyObject* {
-    for (int i = 2; i < 4; ++i)
-      if (p[i] == Py_None) p[i] = nullptr;
-    const at::Tensor &k = tensor(p[0], "KvCache.k"), &v = tensor(p[1], "KvCache.v");
-    need(k.is_cuda(), "KvCache: expected device tensors");
-    need(k.dim() == 4 && k.is_contiguous(), "KvCache: k is [n_pages, n_heads, page_size, head_dim], contiguous");
-    const at::ScalarType type = k.scalar_type();
-    const int64_t n = k.size(0), h = k.size(1), s = k.size(2), d = k.size(3);
-    given(v, {n, h, s, d}, type, k.device(), "KvCache.v");
-    spa_kv_cache c{};
-    c.format = type == at::kFloat8_e4m3fn ? SPA_KV_FP8 : type == at::kChar ? SPA_KV_INT8 : SPA_KV_NATIVE;
-    if (c.format != SPA_KV_NATIVE) {
-      need(p[2] && p[3], "KvCache: 8-bit pages need k_scale and v_scale");
-      const at::Tensor &ks = tensor(p[2], "KvCache.k_scale"), &vs = tensor(p[3], "KvCache.v_scale");
-      given(ks, {n, h, s}, at::kFloat, k.device(), "KvCache.k_scale");
-      given(vs, {n, h, s}, at::kFloat, k.device(), "KvCache.v_scale");
-      c.k_scale = static_cast<float*>(ks.data_ptr());
-      c.v_scale = static_cast<float*>(vs.data_ptr());
-    } else {
-      need(dtype_code(type) >= 0, "KvCache: pages are float16, bfloat16, float8_e4m3fn or int8");
-      need(!p[2] && !p[3], "KvCache: scales belong to 8-bit pages");
-    }
-    c.n_pages = size32(n, "n_pages"); c.n_heads = size32(h, "n_heads");
-    c.page_size = size32(s, "page_size"); c.head_dim = size32(d, "head_dim");
-    c.k = k.data_ptr();
-    c.v = v.data_ptr();
-    self->c = c;
-    self->type = type;
-    self->dev = k.device();
+    pages_of(p);
     for (int i = 0; i < 4; ++i) {
       PyObject* now = p[i] ? p[i] : Py_None;
       Py_INCREF(now);
@@ -237,7 +258,6 @@ int cache_traverse(KvCache* self, visitproc visit, void* arg) {
   return 0;
 }
 int cache_clear(KvCache* self) {
-  self->c = spa_kv_cache{};
   for (PyObject*& p : self->part) Py_CLEAR(p);
   return 0;
 }
@@ -252,29 +272,35 @@ PyMemberDef cache_members[] = {
     {"v", T_OBJECT, offsetof(KvCache, part) + sizeof(PyObject*), READONLY, "values, or their codes"},
     {"k_scale", T_OBJECT, offsetof(KvCache, part) + 2 * sizeof(PyObject*), READONLY, "float32 scales of 8-bit keys, or None"},
     {"v_scale", T_OBJECT, offsetof(KvCache, part) + 3 * sizeof(PyObject*), READONLY, "float32 scales of 8-bit values, or None"},
-    {"n_pages", T_INT, offsetof(KvCache, c) + offsetof(spa_kv_cache, n_pages), READONLY, ""},
-    {"page_size", T_INT, offsetof(KvCache, c) + offsetof(spa_kv_cache, page_size), READONLY, ""},
-    {"n_heads", T_INT, offsetof(KvCache, c) + offsetof(spa_kv_cache, n_heads), READONLY, ""},
-    {"head_dim", T_INT, offsetof(KvCache, c) + offsetof(spa_kv_cache, head_dim), READONLY, ""},
     {nullptr, 0, 0, 0, nullptr}};
+
+template <int32_t spa_kv_cache::*SIZE>
+PyObject* cache_size(PyObject* self, void*) {
+  return guarded([&]() -> PyObject* { return PyLong_FromLong(pages_of(reinterpret_cast<KvCache*>(self)->part).c.*SIZE); });
+}
+PyGetSetDef cache_sizes[] = {
+    {"n_pages", cache_size<&spa_kv_cache::n_pages>, nullptr, nullptr, nullptr},
+    {"page_size", cache_size<&spa_kv_cache::page_size>, nullptr, nullptr, nullptr},
+    {"n_heads", cache_size<&spa_kv_cache::n_heads>, nullptr, nullptr, nullptr},
+    {"head_dim", cache_size<&spa_kv_cache::head_dim>, nullptr, nullptr, nullptr},
+    {nullptr, nullptr, nullptr, nullptr, nullptr}};
 
 PyTypeObject g_cache_type = {PyVarObject_HEAD_INIT(nullptr, 0)};
 
 // The C descriptor for vectors of `type` going in or out.
-spa_kv_cache cache_for(const KvCache* kv, at::ScalarType type) {
-  need(kv->c.k, "KvCache: not initialised");
-  need(dtype_code(type) >= 0 && (kv->c.format != SPA_KV_NATIVE || kv->type == type),
+spa_kv_cache cache_for(const Pages& kv, at::ScalarType type) {
+  need(dtype_code(type) >= 0 && (kv.c.format != SPA_KV_NATIVE || kv.type == type),
        "KvCache: the vectors' type is not the pages'");
-  spa_kv_cache c = kv->c;
+  spa_kv_cache c = kv.c;
   c.dtype = dtype_code(type);
   return c;
 }
-const KvCache* cache(PyObject* o) {
+Pages cache(PyObject* o) {
   if (!PyObject_TypeCheck(o, &g_cache_type)) {
     PyErr_Format(PyExc_TypeError, "cache: expected a KvCache, not %s", Py_TYPE(o)->tp_name);
     throw Raised();
   }
-  return reinterpret_cast<const KvCache*>(o);
+  return pages_of(reinterpret_cast<const KvCache*>(o)->part);
 }
 
 // ---------------------------------------------------------------------------
@@ -289,15 +315,15 @@ PyObject* py_kv_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     static const char* const names[] = {"k", "v", "slots", "cache"};
     Args<4> a("kv_write", names, 4, 4, args, n, kw);
     const at::Tensor &k = tensor(a.v[0], "k"), &v = tensor(a.v[1], "v"), &slots = tensor(a.v[2], "slots");
-    const KvCache* kv = cache(a.v[3]);
+    const Pages kv = cache(a.v[3]);
     const spa_heads kh = heads(k, "k"), vh = heads(v, "v");
-    need(k.device() == kv->dev && v.device() == kv->dev, "kv_write: tensors on several devices");
+    need(k.device() == kv.dev && v.device() == kv.dev, "kv_write: tensors on several devices");
     need(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(), "kv_write: k and v differ in shape or type");
-    need(k.size(1) == kv->c.n_heads && k.size(2) == kv->c.head_dim, "kv_write: the cache has other heads");
-    given(slots, {k.size(0)}, at::kInt, kv->dev, "slots");
+    need(k.size(1) == kv.c.n_heads && k.size(2) == kv.c.head_dim, "kv_write: the cache has other heads");
+    given(slots, {k.size(0)}, at::kInt, kv.dev, "slots");
     const spa_kv_cache c = cache_for(kv, k.scalar_type());
     check(spa_kv_write(&kh, &vh, size32(k.size(0), "k"), static_cast<const int32_t*>(slots.data_ptr()), &c,
-                       stream_of(kv->dev)), "spa_kv_write");
+                       stream_of(kv.dev)), "spa_kv_write");
     Py_RETURN_NONE;
   });
 }
@@ -319,14 +345,14 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObje
   return guarded([&]() -> PyObject* {
     static const char* const names[] = {"cache", "page_table", "cu_seqlens", "total", "k_out", "v_out", "dtype"};
     Args<7> a("kv_read", names, 4, 7, args, n_args, kw);
-    const KvCache* kv = cache(a.v[0]);
+    const Pages kv = cache(a.v[0]);
     const at::Tensor &table = tensor(a.v[1], "page_table"), &cu = tensor(a.v[2], "cu_seqlens");
     const int32_t total = integer(a.v[3], "total");
     need(total >= 0, "total: expected 0 or more");
-    const int32_t max_pages = table_width(table, -1, kv->dev);
+    const int32_t max_pages = table_width(table, -1, kv.dev);
     const int32_t n = size32(table.size(0), "page_table");
-    given(cu, {(int64_t)n + 1}, at::kInt, kv->dev, "cu_seqlens");
-    at::ScalarType type = kv->type;
+    given(cu, {(int64_t)n + 1}, at::kInt, kv.dev, "cu_seqlens");
+    at::ScalarType type = kv.type;
     if (a.v[6]) {
       if (!THPDtype_Check(a.v[6])) {
         PyErr_SetString(PyExc_TypeError, "dtype: expected a torch.dtype");
@@ -336,13 +362,13 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObje
     } else if (a.v[4] || a.v[5]) {
       type = tensor(a.v[4] ? a.v[4] : a.v[5], "k_out").scalar_type();
     } else {
-      need(kv->c.format == SPA_KV_NATIVE, "kv_read: 8-bit pages need dtype or outputs");
+      need(kv.c.format == SPA_KV_NATIVE, "kv_read: 8-bit pages need dtype or outputs");
     }
     const spa_kv_cache c = cache_for(kv, type);
-    const at::Tensor k = output(a.v[4], {total, c.n_heads, c.head_dim}, type, kv->dev, "k_out");
-    const at::Tensor v = output(a.v[5], {total, c.n_heads, c.head_dim}, type, kv->dev, "v_out");
+    const at::Tensor k = output(a.v[4], {total, c.n_heads, c.head_dim}, type, kv.dev, "k_out");
+    const at::Tensor v = output(a.v[5], {total, c.n_heads, c.head_dim}, type, kv.dev, "v_out");
     check(spa_kv_read(&c, static_cast<const int32_t*>(table.data_ptr()), n, max_pages,
-                      static_cast<const int32_t*>(cu.data_ptr()), total, k.data_ptr(), v.data_ptr(), stream_of(kv->dev)),
+                      static_cast<const int32_t*>(cu.data_ptr()), total, k.data_ptr(), v.data_ptr(), stream_of(kv.dev)),
           "spa_kv_read");
     return pair(back(a.v[4], k), back(a.v[5], v));
   });
@@ -355,6 +381,7 @@ at::Tensor workspace(PyObject* o, size_t bytes, at::Device dev) {
   if (o) {
     const at::Tensor& t = tensor(o, "ws");
     need(t.device() == dev && t.is_contiguous() && t.scalar_type() == at::kByte, "ws: expected a contiguous uint8 tensor");
+    held(t, "ws");
     return t;
   }
   return bytes ? fresh({(int64_t)bytes}, at::kByte, dev) : at::Tensor();
@@ -371,14 +398,14 @@ PyObject* py_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n_arg
     static const char* const names[] = {"q", "cache", "page_table", "seq_lens", "scale", "want_lse", "out", "ws"};
     Args<8> a("attention_decode", names, 4, 8, args, n_args, kw);
     const at::Tensor& q = tensor(a.v[0], "q");
-    const KvCache* kv = cache(a.v[1]);
+    const Pages kv = cache(a.v[1]);
     const at::Tensor &table = tensor(a.v[2], "page_table"), &lens = tensor(a.v[3], "seq_lens");
     const spa_heads qh = heads(q, "q");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
-    need(kv->dev == dev, "attention_decode: tensors on several devices");
-    need(q.size(2) == kv->c.head_dim, "attention_decode: the cache has another head_dim");
-    const int32_t n = size32(q.size(0), "q"), hq = size32(q.size(1), "q"), d = kv->c.head_dim;
+    need(kv.dev == dev, "attention_decode: tensors on several devices");
+    need(q.size(2) == kv.c.head_dim, "attention_decode: the cache has another head_dim");
+    const int32_t n = size32(q.size(0), "q"), hq = size32(q.size(1), "q"), d = kv.c.head_dim;
     const int32_t max_pages = table_width(table, n, dev);
     given(lens, {n}, at::kInt, dev, "seq_lens");
     const spa_kv_cache c = cache_for(kv, type);
@@ -474,6 +501,7 @@ PyObject* py_gated_residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n_
     const at::Device dev = x.device();
     const at::ScalarType type = x.scalar_type();
     need(dtype_code(type) >= 0, "x: expected float32, float16 or bfloat16");
+    held(x, "x");
     at::ScalarType stream_type = type;
     const void* residual = nullptr;
     if (a.v[1]) {
@@ -530,13 +558,15 @@ PyMODINIT_FUNC PyInit__layer_native() {
       "KvCache(k, v, k_scale=None, v_scale=None)\n--\n\n"
       "A paged cache of one layer: k and v are [n_pages, n_heads, page_size, head_dim].\n\n"
       "float16 or bfloat16 pages hold the vectors as they are; float8_e4m3fn and int8 pages hold codes, with float32\n"
-      "k_scale and v_scale [n_pages, n_heads, page_size].  The cache keeps its tensors and passes their memory on.";
+      "k_scale and v_scale [n_pages, n_heads, page_size].  The cache keeps its tensors; each call works on\n"
+      "the memory and sizes that they have then.";
   g_cache_type.tp_new = PyType_GenericNew;
   g_cache_type.tp_init = reinterpret_cast<initproc>(cache_init);
   g_cache_type.tp_dealloc = reinterpret_cast<destructor>(cache_dealloc);
   g_cache_type.tp_traverse = reinterpret_cast<traverseproc>(cache_traverse);
   g_cache_type.tp_clear = reinterpret_cast<inquiry>(cache_clear);
   g_cache_type.tp_members = cache_members;
+  g_cache_type.tp_getset = cache_sizes;
   if (PyType_Ready(&g_cache_type) < 0) return nullptr;
   PyObject* m = PyModule_Create(&g_module);
   if (!m) return nullptr;
