@@ -50,10 +50,25 @@ struct DecodeAttnArgs {
   FastDiv page;
 };
 
-// P is multiplied by the value vector's scale before it is rounded to 16 bits; a constant power of two keeps
-// that product of ordinary values near 1 (it leaves with the final division).  Scales are max / 448 and
-// max / 127: with a largest value of 1, 2^8 / 448 and 2^6 / 127 are about a half.
-template <int FMT> constexpr float kPScale = FMT == SPA_KV_FP8 ? 256.f : FMT == SPA_KV_INT8 ? 64.f : 1.f;
+// With an 8-bit cache a softmax weight carries its value vector's scale when it is rounded to 16 bits for the matrix
+// product.  bfloat16 has the exponents for it.  For float16 the scales are taken relative to the largest that the wave
+// has met, brought to 2^14: a weight then keeps its 11 bits down to 2^-28 of the largest, whatever the size of the values
+// (with a constant factor instead, values of 1e-4 beside a heavy key were lost whole).  The reference is a power of two,
+// so nothing is rounded twice, and the sums follow it as they follow the running maximum, when it rises.
+template <int DT, int FMT> constexpr bool kFollowScale = FMT != SPA_KV_NATIVE && DT == SPA_F16;
+struct ValueScale {
+  static constexpr int kLow = 14;      // scales below 2^-112 are not brought up; a written vector's are above 2^-109
+  int top = kLow;                      // the largest scale's exponent field, one value for the wave
+  // Takes in a tile's largest scale; what sums so far are to be multiplied by, or 1.
+  __device__ __forceinline__ float follow(float largest) {
+    const int e = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(largest) >> 23 & 0xFFu));
+    const int before = top;
+    top = max(top, e);
+    return __uint_as_float((uint32_t)max(127 + before - top, 0) << 23);
+  }
+  __device__ __forceinline__ float up() const { return __uint_as_float((uint32_t)(267 - top) << 23); }       // 2^(140 - top)
+  __device__ __forceinline__ float down() const { return __uint_as_float((uint32_t)(top - 13) << 23); }      // 2^(top - 140)
+};
 
 // Positions of sequence s that can count, and their tiles.
 __device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int s) {
@@ -184,6 +199,14 @@ __device__ __forceinline__ float across_groups_max(float v) {
   return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
+// Largest magnitude of a tile's scales, eight on each lane of a group, on every lane.
+__device__ __forceinline__ float largest(const float (&vs)[8]) {
+  float v = fabsf(vs[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) v = fmaxf(v, fabsf(vs[j]));
+  return across_groups_max(v);
+}
+
 // The query operand of k step c: columns are query heads, elements q_at(c, g).. + 7.
 template <int FMT>
 __device__ __forceinline__ int q_at(int c, int g) {
@@ -249,9 +272,10 @@ __device__ __forceinline__ void stream_load(const char* p, uint32_t (&w)[W]) {
 }
 
 // Joins the four waves and writes the piece's result: lane (col, g) holds dimensions NV * (4 g + r) + i of query
-// head col, its maximum and its own positions' sum.
+// head col, its maximum and its own positions' sum; `unit` is what one of o stands for.
 template <int DT, int FMT, int DP>
-__device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, const f32x4 (&o)[DP / 16], float m, float l) {
+__device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, const f32x4 (&o)[DP / 16], float unit, float m,
+                                       float l) {
   constexpr int NV = DP / 16;
   __shared__ float s_o[kWaves][16][DP + 4];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -263,7 +287,7 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = o[i][r];
+    for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = kFollowScale<DT, FMT> ? o[i][r] * unit : o[i][r];
   __syncthreads();
   for (int e = threadIdx.x; e < p.heads * (DP / 2); e += kWaves * kWave) {
     const int h = e / (DP / 2), dim = e % (DP / 2) * 2;
@@ -281,7 +305,7 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
       x1 += f * s_o[w][h][dim + 1];
     }
     if (p.whole) {
-      const float inv = sum > 0.f ? 1.f / (sum * kPScale<FMT>) : 0.f;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const size_t to = (size_t)p.seq * a.hq + p.h0 + h;
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
       if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
@@ -312,6 +336,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
 #pragma unroll
     for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
+    ValueScale vmax;
 
     for (int tile = p.begin + wave; tile < p.end; tile += kWaves) {
       // lane i < 32 finds position i's cell; a position that does not count is bit i of `gone`
@@ -364,16 +389,19 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
       const float alpha = exp2_hw(m - base);
       m = mx;
       l *= alpha;
-      float w[8];
+      float w[8], vs[8], grow = alpha;
+      if constexpr (FMT != SPA_KV_NATIVE) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int j = 0; j < 8; ++j) vs[j] = __shfl(vsc, 16 * (j / 4) + 4 * g + j % 4, kWave);
+      }
+      if constexpr (kFollowScale<DT, FMT>) grow *= vmax.follow(largest(vs));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float e = exp2_hw(t[b][r] - base);
-          l += e;
-          if constexpr (FMT != SPA_KV_NATIVE) e *= __shfl(vsc, 16 * b + 4 * g + r, kWave) * kPScale<FMT>;
-          w[4 * b + r] = e;
-        }
+      for (int j = 0; j < 8; ++j) {
+        w[j] = exp2_hw(t[j / 4][j % 4] - base);
+        l += w[j];
+        if constexpr (kFollowScale<DT, FMT>) vs[j] *= vmax.up();
+        if constexpr (FMT != SPA_KV_NATIVE) w[j] *= vs[j];
+      }
       const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
       uint32_t vr[8][NV / 2];
 #pragma unroll
@@ -396,12 +424,12 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
         vf.y = __builtin_amdgcn_perm(vr[3][i / 2], vr[2][i / 2], sel);
         vf.z = __builtin_amdgcn_perm(vr[5][i / 2], vr[4][i / 2], sel);
         vf.w = __builtin_amdgcn_perm(vr[7][i / 2], vr[6][i / 2], sel);
-        o[i] *= alpha;
+        o[i] *= grow;
         o[i] = mfma16<DT>(vf, pf, o[i]);
       }
     }
 
-    finish<DT, FMT, DP>(a, p, o, m, l);
+    finish<DT, FMT, DP>(a, p, o, vmax.down(), m, l);
   } while (span.left > 0);
 }
 
@@ -429,6 +457,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
 #pragma unroll
     for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
+    ValueScale vmax;
 
     const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
     int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
@@ -522,7 +551,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
         for (int r = 0; r < 4; ++r) {
           t[4 * b + r] = s[b][r] * a.c;
           if constexpr (FMT != SPA_KV_NATIVE) t[4 * b + r] *= kq[r];
-          vs[4 * b + r] = FMT != SPA_KV_NATIVE ? vq[r] * kPScale<FMT> : 1.f;
+          vs[4 * b + r] = FMT != SPA_KV_NATIVE ? vq[r] : 1.f;
         }
       }
       // the last tile's end and absent pages: what does not count is removed from the scores, the values and their scales
@@ -559,11 +588,19 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
         for (int i = 0; i < NV; ++i) o[i] *= alpha;
       }
       const float base = m == -INFINITY ? 0.f : m;           // nothing seen yet: every weight is 0
+      if constexpr (kFollowScale<DT, FMT>) {
+        const float grow = vmax.follow(largest(vs));
+        if (grow != 1.f) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) o[i] *= grow;
+        }
+      }
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         w[j] = exp2_hw(t[j] - base);
         l += w[j];
+        if constexpr (kFollowScale<DT, FMT>) vs[j] *= vmax.up();
         if constexpr (FMT != SPA_KV_NATIVE) w[j] *= vs[j];
       }
       const uint4 pf = make_uint4(pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7]));
@@ -596,7 +633,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
         }
       }
     }
-    finish<DT, FMT, DP>(a, p, o, m, l);
+    finish<DT, FMT, DP>(a, p, o, vmax.down(), m, l);
   } while (span.left > 0);
 }
 
@@ -668,7 +705,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
     }
   }
   if (!live) return;
-  const float inv = j.sum > 0.f ? 1.f / (j.sum * kPScale<FMT>) : 0.f;
+  const float inv = j.sum > 0.f ? 1.f / j.sum : 0.f;
   const size_t to = (size_t)blockIdx.x * a.hq + head;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) =
       make_uint2(pack2<DT>(j.x.x * inv, j.x.y * inv), pack2<DT>(j.x.z * inv, j.x.w * inv));
