@@ -673,7 +673,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
         const size_t row = (size_t)(k ? next + 2 * k : of.x) * a.hq + head;
         s[u] = a.part_ml[row];
         v[u] = *reinterpret_cast<const float4*>(a.part_o + row * a.d + dim);
-        if (i + u * RUNS >= of.y) s[u].x = -INFINITY;
+        if (i + u * RUNS >= of.y) {               // none: not a piece of weight 0, whose infinities would give NaN
+          s[u].x = -INFINITY;
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
       float now = j.m;
 #pragma unroll

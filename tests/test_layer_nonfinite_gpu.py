@@ -1,0 +1,79 @@
+"""Infinities and NaN in keys, values and queries: a row that does not see them is not touched, one that sees them says so."""
+import math
+
+import pytest
+import torch
+
+import attention_bounds as A
+
+pytestmark = pytest.mark.gpu
+
+spa = pytest.importorskip("activation_sparsification_amd")
+
+BF16, F16 = torch.bfloat16, torch.float16
+INF, NAN = math.inf, math.nan
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
+
+
+def check_rows(got, got_lse, q, k, v, visible, scale, dtype, codes=False):
+    """Rows against the reference on finite values; a visible NaN or infinity of v must appear in its dimension, and only
+    there.  k and q are finite, or such that the reference's scores are finite or -inf."""
+    hq, hkv = q.shape[1], k.shape[1]
+    bad = ~torch.isfinite(v)
+    r = A.reference(q, k, v.masked_fill(bad, 0.0), scale, visible)
+    seen = visible.double()
+    per = hq // hkv
+
+    def marks(which):           # [lq, hq, d]: a row sees such a value in this dimension
+        m = torch.stack([seen @ which[:, h].double() for h in range(hkv)], 1) > 0
+        return m.repeat_interleave(per, 1)
+
+    plus, minus, nan = marks(v == INF), marks(v == -INF), marks(v.isnan())
+    nan = nan | (plus & minus)
+    plus, minus = plus & ~nan, minus & ~nan
+    assert got[nan].isnan().all(), "a visible NaN was lost"
+    assert (got[plus] == INF).all() and (got[minus] == -INF).all(), "a visible infinity was lost or became NaN"
+    rest = ~(nan | plus | minus)
+    A.check(torch.where(rest, got.double(), r["out"]), got_lse, r, dtype, codes)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# single tokens
+# ---------------------------------------------------------------------------------------------------------------
+def decode(page, lens, q, k, v, hkv=2, d=64):
+    """k, v: lists of [len, hkv, d]; a native cache with the sequences on consecutive pages."""
+    need = [-(-x // page) for x in lens]
+    cache = spa.new_kv_cache(sum(need) + 1, page, hkv, d, q.dtype)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for s, x in enumerate(lens):
+        table[s, :need[s]] = torch.arange(at, at + need[s])
+        slots = torch.arange(x, dtype=torch.int32, device="cuda") + at * page
+        spa.kv_write(k[s], v[s], slots, cache)
+        at += need[s]
+    return spa.attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), want_lse=True)
+
+
+@pytest.mark.parametrize("page", [16])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_decode_nonfinite_values(page, dtype, value):
+    # the last position, whose row stands in for the tile's end, and one in the middle
+    lens = [37, 70, 3, 2000]
+    g = gen(page)
+    q = torch.randn((4, 8, 64), generator=g, device="cuda").to(dtype)
+    k, v = ([torch.randn((x, 2, 64), generator=g, device="cuda").to(dtype) for x in lens] for _ in range(2))
+    for s, at in ((0, 36), (1, 40), (2, 2), (3, 1999)):
+        v[s][at, :, 3:6] = value
+    out, lse = decode(page, lens, q, k, v)
+    for s, x in enumerate(lens):
+        check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1].double(), k[s].double(), v[s].double(),
+                   torch.ones((1, x), dtype=torch.bool, device="cuda"), 0.125, dtype)
+
