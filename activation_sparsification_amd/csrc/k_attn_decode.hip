@@ -346,12 +346,12 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
       const int pg = a.table[(size_t)p.seq * a.max_pages + pc];
       const bool ok = pg >= 0 && pg < a.n_pages;
       const int cell = ok ? (pg * a.hkv + p.head) * (int)a.page.d + (p0 - pc * (int)a.page.d) : 0;
-      const uint32_t gone = (uint32_t)__ballot(pos >= p.len || !ok);
-      const uint32_t bad = (uint32_t)__ballot(!ok);            // its cell is not the sequence's: the values are dropped
+      const bool counts = pos < p.len && ok;
+      const uint32_t gone = (uint32_t)__ballot(!counts);       // the scores are hidden and the values dropped
       float ksc = 1.f, vsc = 1.f;
       if constexpr (FMT != SPA_KV_NATIVE) {
         ksc = a.k_scale[cell];
-        vsc = ok ? a.v_scale[cell] : 0.f;
+        vsc = counts ? a.v_scale[cell] : 0.f;
       }
       float t[2][4];
 #pragma unroll
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
         const size_t vc = (size_t)(uint32_t)__shfl(cell, i, kWave);
         constexpr int ES = FMT == SPA_KV_NATIVE ? 2 : 1, VW = NV * ES / 4;
         uint32_t raw[VW];
-        const bool live = NV * col < a.d && !((bad >> i) & 1u);
+        const bool live = NV * col < a.d && !((gone >> i) & 1u);
         const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.v) + (vc * a.d + NV * col) * ES);
 #pragma unroll
         for (int e = 0; e < VW; ++e) raw[e] = live && NV * col + 4 / ES * e < a.d ? at[e] : 0u;

@@ -61,7 +61,7 @@ def decode(page, lens, q, k, v, hkv=2, d=64):
     return spa.attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), want_lse=True)
 
 
-@pytest.mark.parametrize("page", [16])
+@pytest.mark.parametrize("page", [16, 7, 1, 24])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("value", [NAN, INF, -INF])
 def test_decode_nonfinite_values(page, dtype, value):
