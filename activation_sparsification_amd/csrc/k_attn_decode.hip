@@ -305,10 +305,10 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
       x1 += f * s_o[w][h][dim + 1];
     }
     if (p.whole) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const size_t to = (size_t)p.seq * a.hq + p.h0 + h;
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
-      if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (base + log2_hw(sum)) : -INFINITY;
+      if (dim == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : kLn2 * (base + log2_hw(sum));
     } else {
       const size_t to = (size_t)p.slot * a.hq + p.h0 + h;
       *reinterpret_cast<float2*>(a.part_o + to * a.d + dim) = make_float2(x0, x1);
@@ -708,11 +708,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
     }
   }
   if (!live) return;
-  const float inv = j.sum > 0.f ? 1.f / j.sum : 0.f;
+  const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
   const size_t to = (size_t)blockIdx.x * a.hq + head;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) =
       make_uint2(pack2<DT>(j.x.x * inv, j.x.y * inv), pack2<DT>(j.x.z * inv, j.x.w * inv));
-  if (dim == 0 && a.lse) a.lse[to] = j.sum > 0.f ? kLn2 * (j.m + log2_hw(j.sum)) : -INFINITY;
+  if (dim == 0 && a.lse) a.lse[to] = j.sum == 0.f ? -INFINITY : kLn2 * (j.m + log2_hw(j.sum));
 }
 
 template <int DT, int FMT, int DP>

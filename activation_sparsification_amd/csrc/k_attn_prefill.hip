@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
     if (g == 0) a.part_ml[at] = make_float2(m, l);
     return;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
             make_uint2(pack2<DT>(o[b][4 * r] * inv, o[b][4 * r + 1] * inv),
                        pack2<DT>(o[b][4 * r + 2] * inv, o[b][4 * r + 3] * inv));
     }
-  if (a.lse && g == 0) a.lse[to] = l > 0.f ? kLn2 * (m + log2_hw(l)) : -INFINITY;
+  if (a.lse && g == 0) a.lse[to] = l == 0.f ? -INFINITY : kLn2 * (m + log2_hw(l));
 }
 
 // One workgroup per row and 1024 of its outputs: the pieces of the row's tile brought to their common maximum and
@@ -468,10 +468,10 @@ __global__ void __launch_bounds__(kThreads) k_attention_prefill_join(PrefillAttn
     sum += f * ml.y;
     x.x += f * v.x; x.y += f * v.y; x.z += f * v.z; x.w += f * v.w;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint2*>(a.out + to * a.d + dim) =
       make_uint2(pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv));
-  if (dim == 0 && a.lse) a.lse[to] = sum > 0.f ? kLn2 * (m + log2_hw(sum)) : -INFINITY;
+  if (dim == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : kLn2 * (m + log2_hw(sum));
 }
 
 template <int DT, int DP, int BN>

@@ -45,6 +45,24 @@ def check_rows(got, got_lse, q, k, v, visible, scale, dtype, codes=False):
 
 
 # ---------------------------------------------------------------------------------------------------------------
+# prompts
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("lk", [40, 3000])
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompt_rows_of_nan(d, lk):
+    # a NaN query has NaN outputs and a NaN log-sum-exp; its neighbours have their own
+    g = gen(9)
+    q, k, v = (torch.randn((n, 2, d), generator=g, device="cuda").to(BF16) for n in (30, lk, lk))
+    q[7, 0, 5] = NAN
+    out, lse = spa.attention_prefill(q, k, v, offsets([30]), offsets([lk]), causal=False, want_lse=True)
+    assert out[7, 0].isnan().all() and lse[7, 0].isnan()
+    q[7, 0], out[7, 0], lse[7, 0] = 0.0, 0.0, 0.0
+    r = A.reference(q, k, v, d ** -0.5, torch.ones((30, lk), dtype=torch.bool, device="cuda"))
+    r["out"][7, 0] = r["lse"][7, 0] = 0.0
+    A.check(out, lse, r, BF16)
+
+
+# ---------------------------------------------------------------------------------------------------------------
 # single tokens
 # ---------------------------------------------------------------------------------------------------------------
 def decode(page, lens, q, k, v, hkv=2, d=64):
@@ -77,3 +95,22 @@ def test_decode_nonfinite_values(page, dtype, value):
         check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1].double(), k[s].double(), v[s].double(),
                    torch.ones((1, x), dtype=torch.bool, device="cuda"), 0.125, dtype)
 
+
+@pytest.mark.parametrize("page", [16, 7])
+def test_decode_rows_of_nan(page):
+    # one sequence that is cut, one that is not, one that is empty
+    lens = [3000, 20, 0]
+    g = gen(3)
+    q = torch.randn((3, 4, 64), generator=g, device="cuda").to(BF16)
+    k, v = ([torch.randn((x, 2, 64), generator=g, device="cuda").to(BF16) for x in lens] for _ in range(2))
+    q[:, 1, 9] = NAN
+    out, lse = decode(page, lens, q, k, v)
+    assert out[:2, 1].isnan().all() and lse[:2, 1].isnan().all()
+    assert (out[2] == 0).all() and (lse[2] == -INF).all()
+    rest = [0, 2, 3]
+    for s in range(2):
+        r = A.reference(q[s:s + 1].nan_to_num(0.0), k[s], v[s], 0.125, torch.ones((1, lens[s]), dtype=torch.bool, device="cuda"))
+        r["out"][:, 1] = r["lse"][:, 1] = 0.0
+        a, b = out[s:s + 1].clone(), lse[s:s + 1].clone()
+        a[:, 1] = b[:, 1] = 0.0
+        A.check(a, b, r, BF16)
