@@ -30,30 +30,32 @@ struct KvArgs {
 };
 
 template <int LG>
-__device__ __forceinline__ float group_max(float v) {
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
 #pragma unroll
-  for (int off = LG / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  for (int off = LG / 2; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, kWave));
   return v;
 }
 
-// Codes of 8 values and their vector's scale: the definition's float32 operations in its order.
+// Codes of 8 values and their vector's scale: the definition's float32 operations in its order.  The largest magnitude
+// is found on the bit patterns, which order like the numbers with infinity and NaN at the top: no such value is passed
+// over.
 template <int FMT, int LG>
 __device__ __forceinline__ uint2 quantise(const float (&x)[8], float& scale) {
 #pragma clang fp contract(off)
   constexpr float top = FMT == SPA_KV_FP8 ? 448.f : 127.f;
-  float a = 0.f;
+  uint32_t bits = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
-  a = group_max<LG>(a);
-  const bool live = a >= 0x1p-100f;
-  scale = live ? __fdiv_rn(a, top) : 0.f;
+  for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+  const float a = __uint_as_float(group_max<LG>(bits));
+  const bool finite = a < INFINITY, live = finite && a >= 0x1p-100f;
+  scale = live ? __fdiv_rn(a, top) : finite ? 0.f : NAN;
   const float inv = live ? __fdiv_rn(top, a) : 0.f;
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float q[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = x[4 * h + e] * inv;
+    for (int e = 0; e < 4; ++e) q[e] = finite ? x[4 * h + e] * inv : 0.f;
     if constexpr (FMT == SPA_KV_FP8) {
       w[h] = fp8_pair(q[0], q[1]) | (fp8_pair(q[2], q[3]) << 16);
     } else {

@@ -427,8 +427,9 @@ typedef struct spa_heads {
  *                 vector and Q = 448 (e4m3) or 127 (int8): scale = a / Q,
  *                 code = x * (Q / a) rounded to nearest even, each division
  *                 and product one float32 operation; a vector with a < 2^-100
- *                 is stored as zeros with scale 0.  The value of a code is
- *                 code * scale.
+ *                 is stored as zeros with scale 0, one that holds a NaN or an
+ *                 infinity as zeros with scale NaN: all of it reads back as
+ *                 NaN.  The value of a code is code * scale.
  * dtype (SPA_F16 or SPA_BF16) is the type of the vectors that go in and out.
  * head_dim must be a multiple of 8 up to 256 and n_pages * page_size *
  * n_heads below 2^31, else SPA_ERR_UNSUPPORTED; any page_size >= 1. */

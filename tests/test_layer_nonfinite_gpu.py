@@ -63,6 +63,35 @@ def test_prompt_rows_of_nan(d, lk):
 
 
 # ---------------------------------------------------------------------------------------------------------------
+# the cache
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [8, 40, 128, 256])
+def test_write_of_nan_and_infinity(fmt, dtype, d):
+    # no value stands for them in 8 bits beside finite ones: the whole vector reads back as NaN, and no other does
+    g = gen(d)
+    h = 3
+    k, v = (torch.randn((9, h, d), generator=g, device="cuda").to(dtype) for _ in range(2))
+    good = spa.new_kv_cache(1, 16, h, d, dtype, fmt)
+    slots = torch.arange(9, dtype=torch.int32, device="cuda")
+    spa.kv_write(k, v, slots, good)
+    k[1, 0, d // 2], k[2, 1, 0], k[3, 2, d - 1], v[4, 0], v[5, 1] = NAN, INF, -INF, NAN, INF
+    v[6, 2, 1], v[6, 2, 2] = NAN, INF
+    cache = spa.new_kv_cache(1, 16, h, d, dtype, fmt)
+    spa.kv_write(k, v, slots, cache)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    got = spa.kv_read(cache, table, offsets([9]), 9, dtype=dtype)
+    want = spa.kv_read(good, table, offsets([9]), 9, dtype=dtype)
+    for x, y, cells in ((got[0], want[0], ((1, 0), (2, 1), (3, 2))), (got[1], want[1], ((4, 0), (5, 1), (6, 2)))):
+        sick = torch.zeros((9, h), dtype=torch.bool, device="cuda")
+        for t, head in cells:
+            sick[t, head] = True
+        assert x[sick].isnan().all(), "a NaN or an infinity was stored as numbers"
+        assert torch.equal(x[~sick], y[~sick])
+
+
+# ---------------------------------------------------------------------------------------------------------------
 # single tokens
 # ---------------------------------------------------------------------------------------------------------------
 def decode(page, lens, q, k, v, hkv=2, d=64):
