@@ -159,6 +159,212 @@ __device__ __forceinline__ uint2 lds_read_tr(const char* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
 }
 
+// What a wave of workgroup `block` works on: 32 query rows of one head and the keys of its workgroup's piece.
+struct Place {
+  int head, kvh, split;
+  int q_first, lq, k_first, lk;
+  int k_begin, k_end;          // the piece's keys
+  bool whole;                  // the piece is all of the tile's keys
+  int w0;                      // the wave's first row within the sequence
+  int full, wave_end;          // keys that all its rows see, and the end of the piece's that any does
+};
+// The number of block's tile, for find_tile.
+__device__ __forceinline__ int tile_number(const PrefillAttnArgs& a, int block) {
+  return block / a.hkv / a.group / a.splits;
+}
+// False if the tile has no keys for the workgroup's piece.
+template <int BN>
+__device__ __forceinline__ bool place_wave(const PrefillAttnArgs& a, int block, int wave, const Tile& t, Place& p) {
+  // key-value heads fastest (one XCD keeps to as few of them as there are), then the query heads that share one
+  p.kvh = block % a.hkv;
+  const int rest = block / a.hkv;
+  p.head = p.kvh * a.group + rest % a.group;
+  p.split = rest / a.group % a.splits;
+  // one value for the wave, whichever way it was found: tile bases stay in scalar registers
+  p.q_first = __builtin_amdgcn_readfirstlane(t.q_first), p.lq = __builtin_amdgcn_readfirstlane(t.lq);
+  p.k_first = __builtin_amdgcn_readfirstlane(t.k_first), p.lk = __builtin_amdgcn_readfirstlane(t.lk);
+  const int m0 = __builtin_amdgcn_readfirstlane(t.m0), tile_end = __builtin_amdgcn_readfirstlane(t.k_end);
+  const int per = piece_keys<BN>(tile_end, a.splits);
+  p.k_begin = p.split * per;                                    // this piece's keys: [k_begin, k_end)
+  p.k_end = min(p.k_begin + per, tile_end);
+  p.whole = tile_end <= per;
+  p.w0 = m0 + wave * kWaveRows;
+  p.full = visible_end(p.w0, p.lq, p.lk, a.causal);
+  p.wave_end = min(visible_end(p.w0 + kWaveRows - 1, p.lq, p.lk, a.causal), p.k_end);
+  return !p.split || p.k_begin < tile_end;
+}
+
+// A 16-bit value into its half of a word: itself if it is finite; else 1 into `plus` for +inf, `minus` for -inf, both for NaN.
+template <int DT> constexpr uint32_t kOne16 = DT == SPA_BF16 ? 0x3F80u : 0x3C00u;
+template <int DT>
+__device__ __forceinline__ void take_out(uint32_t h, int sh, uint32_t& v, uint32_t& plus, uint32_t& minus) {
+  constexpr uint32_t kInf = DT == SPA_BF16 ? 0x7F80u : 0x7C00u;
+  const uint32_t size = h & 0x7FFFu;
+  if (size < kInf) v |= h << sh;
+  if (size > kInf || h == kInf) plus |= kOne16<DT> << sh;
+  if (size > kInf || h == (kInf | 0x8000u)) minus |= kOne16<DT> << sh;
+}
+
+// Hides what a lane's row does not see of the scores of tile j0: register r of block b is key 32 b + 8 (r / 4) + 4 g + r % 4.
+template <int BN>
+__device__ __forceinline__ void hide(f32x16 (&s)[BN / 32], int j0, int full, int sees, int g) {
+  if (j0 + BN <= full) return;
+  const int hidden = sees - j0 - 4 * g;
+#pragma unroll
+  for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (32 * b + 8 * (r / 4) + r % 4 >= hidden) s[b][r] = -INFINITY;
+}
+// The largest score of the row, both halves of the wave, in the exponent's unit.
+template <int NB>
+__device__ __forceinline__ float row_max(const f32x16 (&s)[NB], float c) {
+  float v = s[0][0];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v = fmaxf(v, s[b][r]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1])) * c;
+}
+// The reference m and what is relative to it follow the tile's maximum mx.
+template <int N>
+__device__ __forceinline__ void follow(float mx, float& m, float& l, f32x16 (&o)[N]) {
+  if (__any(mx > m + kSlack)) {
+    const float now = fmaxf(mx, m), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+    m = now;
+    l *= alpha;
+#pragma unroll
+    for (int b = 0; b < N; ++b) o[b] *= alpha;
+  }
+}
+// Scores to weights, rounded to the 16-bit type as operands of the product with V; their sum, unrounded, goes to l.
+template <int DT, int NB>
+__device__ __forceinline__ void weights(f32x16 (&s)[NB], uint4 (&pf)[2 * NB], float c, float m, float& l) {
+  const float base = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+#pragma unroll
+  for (int t = 0; t < 2 * NB; ++t) {
+    f32x16& p = s[t / 2];
+    const int r0 = t % 2 * 8;
+#pragma unroll
+    for (int r = r0; r < r0 + 8; ++r) {
+      p[r] = exp2_hw(fmaf(p[r], c, -base));
+      sum += p[r];
+    }
+    pf[t] = make_uint4(pack2<DT>(p[r0], p[r0 + 1]), pack2<DT>(p[r0 + 2], p[r0 + 3]), pack2<DT>(p[r0 + 4], p[r0 + 5]),
+                       pack2<DT>(p[r0 + 6], p[r0 + 7]));
+  }
+  l += sum;
+  asm volatile("" : "+v"(l));      // the sum is taken here, not after the product that follows
+}
+
+// Writes blocks of 32 dimensions, from `first` on, of the wave's outputs or of its piece of them; l is the row's sum.
+template <int DT, int N>
+__device__ __forceinline__ void store_blocks(const PrefillAttnArgs& a, const Place& p, int row, int g, const f32x16 (&o)[N],
+                                             int first, float m, float l) {
+  if (row >= p.lq) return;
+  const size_t to = (size_t)(p.q_first + row) * a.hq + p.head;
+  const bool stats = first == 0 && g == 0;
+  if (!p.whole) {
+    const size_t at = (size_t)p.split * a.tq * a.hq + to;
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int dim = 32 * (first + b) + 8 * r + 4 * g;
+        if (dim < a.d)
+          *reinterpret_cast<float4*>(a.part_o + at * a.d + dim) =
+              make_float4(o[b][4 * r], o[b][4 * r + 1], o[b][4 * r + 2], o[b][4 * r + 3]);
+      }
+    if (stats) a.part_ml[at] = make_float2(m, l);
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int b = 0; b < N; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int at = 32 * (first + b) + 8 * r + 4 * g;
+      if (at < a.d)
+        *reinterpret_cast<uint2*>(a.out + to * a.d + at) =
+            make_uint2(pack2<DT>(o[b][4 * r] * inv, o[b][4 * r + 1] * inv),
+                       pack2<DT>(o[b][4 * r + 2] * inv, o[b][4 * r + 3] * inv));
+    }
+  if (a.lse && stats) a.lse[to] = l == 0.f ? -INFINITY : kLn2 * (m + log2_hw(l));
+}
+
+// The wave's work again, by itself, from memory and 32 dimensions at a time: infinities and NaN are taken out of the values,
+// and two more products with 1 for each key that a row sees find the rows that they belong to.  The arguments and the place
+// are found anew, so that nothing for this stays in registers beside the first walk.
+template <int DT, int DP, int BN>
+__device__ __forceinline__ void walk_again(int wave) {
+  constexpr int KS = DP / 16, NB = BN / 32, DB = DP / 32;
+  auto kernarg = __builtin_amdgcn_kernarg_segment_ptr();
+  int block = blockIdx.x;
+  asm volatile("" : "+s"(kernarg), "+s"(block));
+  const PrefillAttnArgs a = *(const PrefillAttnArgs*)kernarg;
+  Tile tile;
+  Place p;
+  if (!find_tile<DP>(a, tile_number(a, block), tile) || !place_wave<BN>(a, block, wave, tile, p)) return;
+  const int lane = threadIdx.x & (kWave - 1), l32 = lane & 31, g = lane >> 5;
+  const int row = p.w0 + l32, sees = visible_end(min(row, p.lq - 1), p.lq, p.lk, a.causal);
+  const uint16_t* q = a.q + (size_t)(p.q_first + min(row, p.lq - 1)) * a.q_row + (size_t)p.head * a.q_head;
+  const uint16_t* kbase = a.k + (size_t)p.k_first * a.k_row + (size_t)p.kvh * a.k_head;
+  const uint16_t* vbase = a.v + (size_t)p.k_first * a.v_row + (size_t)p.kvh * a.v_head;
+#pragma unroll 1
+  for (int b = 0; b < DB; ++b) {
+    const int dim = min(32 * b + l32, a.d - 1);
+    f32x16 ob[1], zero;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) ob[0][r] = zero[r] = 0.f;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j0 = p.k_begin; j0 < p.wave_end; j0 += BN) {
+      f32x16 s0[NB];
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        s0[c] = zero;
+        const uint16_t* k = kbase + (size_t)min(j0 + 32 * c + l32, p.lk - 1) * a.k_row;
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+          const int at = 16 * t + 8 * g;
+          uint4 kf = make_uint4(0, 0, 0, 0), qf = kf;
+          if (at < a.d) {
+            kf = *reinterpret_cast<const uint4*>(k + at);
+            qf = *reinterpret_cast<const uint4*>(q + at);
+          }
+          s0[c] = mfma32<DT>(kf, qf, s0[c]);
+        }
+      }
+      hide<BN>(s0, j0, p.full, sees, g);
+      follow(row_max(s0, a.c), m, l, ob);
+      uint4 pf[BN / 16];
+      weights<DT>(s0, pf, a.c, m, l);
+#pragma unroll
+      for (int t = 0; t < BN / 16; ++t) {
+        uint32_t v[4] = {}, plus[4] = {}, minus[4] = {}, one[4] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int key = j0 + 16 * t + 8 * (e / 4) + 4 * g + e % 4, sh = 16 * (e % 2);
+          take_out<DT>(vbase[(size_t)min(key, p.lk - 1) * a.v_row + dim], sh, v[e / 2], plus[e / 2], minus[e / 2]);
+          if (key < sees) one[e / 2] |= kOne16<DT> << sh;
+        }
+        const auto part = [](const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); };
+        ob[0] = mfma32<DT>(part(v), pf[t], ob[0]);
+        const f32x16 up = mfma32<DT>(part(plus), part(one), zero);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ob[0][r] = up[r] > 0.f ? ob[0][r] + INFINITY : ob[0][r];
+        const f32x16 down = mfma32<DT>(part(minus), part(one), zero);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ob[0][r] = down[r] > 0.f ? ob[0][r] - INFINITY : ob[0][r];
+      }
+    }
+    l += __shfl_xor(l, 32, kWave);
+    store_blocks<DT>(a, p, row, g, ob, b, m, l);
+  }
+}
+
 template <int DT, int DP, int BN>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefill(PrefillAttnArgs a) {
   constexpr int CH = DP / 8;             // 16-byte pieces of a row
@@ -174,27 +380,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l32 = lane & 31, g = lane >> 5;
 
-  // key-value heads fastest (one XCD keeps to as few of them as there are), then the query heads that share one
-  const int kvh = blockIdx.x % a.hkv;
-  const int rest = blockIdx.x / a.hkv;
-  const int head = kvh * a.group + rest % a.group;
-  const int split = rest / a.group % a.splits;
-  Tile t;
-  if (!find_tile<DP>(a, rest / a.group / a.splits, t)) return;
-  // one value for the wave, whichever way it was found: tile bases stay in scalar registers
-  const int q_first = __builtin_amdgcn_readfirstlane(t.q_first), lq = __builtin_amdgcn_readfirstlane(t.lq);
-  const int k_first = __builtin_amdgcn_readfirstlane(t.k_first), lk = __builtin_amdgcn_readfirstlane(t.lk);
-  const int m0 = __builtin_amdgcn_readfirstlane(t.m0), tile_end = __builtin_amdgcn_readfirstlane(t.k_end);
-  const int per = piece_keys<BN>(tile_end, a.splits);
-  const int k_begin = split * per;                              // this piece's keys: [k_begin, k_end)
-  if (split && k_begin >= tile_end) return;
-  const int k_end = min(k_begin + per, tile_end);
-  const bool whole = tile_end <= per;
-  const int w0 = m0 + wave * kWaveRows;
-  const int row = w0 + l32;                                     // this lane's query
+  Tile tile;
+  if (!find_tile<DP>(a, tile_number(a, blockIdx.x), tile)) return;
+  Place p;
+  if (!place_wave<BN>(a, blockIdx.x, wave, tile, p)) return;
+  const int head = p.head, kvh = p.kvh, q_first = p.q_first, lq = p.lq, k_first = p.k_first, lk = p.lk;
+  const int k_begin = p.k_begin, k_end = p.k_end, full = p.full, wave_end = p.wave_end;
+  const int row = p.w0 + l32;                                   // this lane's query
   const int sees = visible_end(min(row, lq - 1), lq, lk, a.causal);                       // its first hidden key
-  const int full = visible_end(w0, lq, lk, a.causal);                                     // keys that all its wave sees
-  const int wave_end = min(visible_end(w0 + kWaveRows - 1, lq, lk, a.causal), k_end);     // and that any does
 
   // a tile's direct loads: lane -> (row, stored piece); rows past the end repeat the last one, pieces past
   // head_dim repeat the first (they meet zeros of Q, or give columns of O that are not stored)
@@ -256,51 +449,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
       }
     }
   };
-  auto mask = [&](f32x16 (&s)[NB], int j0) {
-    if (j0 + BN <= full) return;
-    const int hidden = sees - j0 - 4 * g;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (32 * b + 8 * (r / 4) + r % 4 >= hidden) s[b][r] = -INFINITY;
-  };
-  auto row_max = [&](const f32x16 (&s)[NB]) {
-    float v = s[0][0];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) v = fmaxf(v, s[b][r]);
-    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1])) * a.c;
-  };
-  auto follow = [&]() {
-    if (__any(mx > m + kSlack)) {
-      const float now = fmaxf(mx, m), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
-      m = now;
-      l *= alpha;
-#pragma unroll
-      for (int b = 0; b < DB; ++b) o[b] *= alpha;
-    }
-  };
-  auto weights = [&](f32x16 (&s)[NB], uint4 (&pf)[BN / 16]) {
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-#pragma unroll
-    for (int t = 0; t < BN / 16; ++t) {
-      f32x16& p = s[t / 2];
-      const int r0 = t % 2 * 8;
-#pragma unroll
-      for (int r = r0; r < r0 + 8; ++r) {
-        p[r] = exp2_hw(fmaf(p[r], a.c, -base));
-        sum += p[r];
-      }
-      pf[t] = make_uint4(pack2<DT>(p[r0], p[r0 + 1]), pack2<DT>(p[r0 + 2], p[r0 + 3]), pack2<DT>(p[r0 + 4], p[r0 + 5]),
-                         pack2<DT>(p[r0 + 6], p[r0 + 7]));
-    }
-    l += sum;
-    asm volatile("" : "+v"(l));      // the sum is taken here, not after the product that follows
-  };
   auto values = [&](const uint4 (&pf)[BN / 16], int buf) {
     const char* vs = s_kv + (2 + buf) * kTileBytes;
 #pragma unroll
@@ -344,20 +492,20 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   };
   auto step = [&](f32x16 (&cur)[NB], f32x16 (&nxt)[NB], int j0, int buf) {
     arrive(j0, buf);
-    follow();
+    follow(mx, m, l, o);
     uint4 pf[BN / 16];
     scores(nxt, buf ^ 1);
-    weights(cur, pf);
+    weights<DT>(cur, pf, a.c, m, l);
     values(pf, buf);
     interleave();
-    mask(nxt, j0 + BN);
-    mx = row_max(nxt);
+    hide<BN>(nxt, j0 + BN, full, sees, g);
+    mx = row_max(nxt, a.c);
   };
   auto last = [&](f32x16 (&cur)[NB], int j0, int buf) {
     arrive(j0, buf);
-    follow();
+    follow(mx, m, l, o);
     uint4 pf[BN / 16];
-    weights(cur, pf);
+    weights<DT>(cur, pf, a.c, m, l);
     values(pf, buf);
   };
 
@@ -372,18 +520,18 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
         arrive(j0, buf);
         f32x16 s0[NB];
         scores(s0, buf);
-        mask(s0, j0);
-        mx = row_max(s0);
-        follow();
+        hide<BN>(s0, j0, full, sees, g);
+        mx = row_max(s0, a.c);
+        follow(mx, m, l, o);
         uint4 pf[BN / 16];
-        weights(s0, pf);
+        weights<DT>(s0, pf, a.c, m, l);
         values(pf, buf);
       }
     } else if (j0 < wave_end) {
       f32x16 s0[NB], s1[NB];
       scores(s0, 0);
-      mask(s0, j0);
-      mx = row_max(s0);
+      hide<BN>(s0, j0, full, sees, g);
+      mx = row_max(s0, a.c);
       for (; j0 + 2 * BN < wave_end; j0 += 2 * BN) {
         step(s0, s1, j0, 0);
         step(s1, s0, j0 + BN, 1);
@@ -401,35 +549,22 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
     for (; j0 < k_end; j0 += BN, buf ^= 1) arrive(j0, buf);      // the other waves' tiles: this wave brings its part
   }
 
-  l += __shfl_xor(l, 32, kWave);
-  if (row >= lq) return;
-  const size_t to = (size_t)(q_first + row) * a.hq + head;
-  if (!whole) {
-    const size_t at = (size_t)split * a.tq * a.hq + to;
+  // A value that a row does not see has weight 0, and 0 times an infinity or NaN is NaN.  Such a value in a tile that some
+  // row sees in part, or in the last key's copies past the end, shows in the wave's sums.
+  float none[DB];
 #pragma unroll
-    for (int b = 0; b < DB; ++b)
+  for (int b = 0; b < DB; ++b) {
+    none[b] = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int dim = 32 * b + 8 * r + 4 * g;
-        if (dim < a.d)
-          *reinterpret_cast<float4*>(a.part_o + at * a.d + dim) =
-              make_float4(o[b][4 * r], o[b][4 * r + 1], o[b][4 * r + 2], o[b][4 * r + 3]);
-      }
-    if (g == 0) a.part_ml[at] = make_float2(m, l);
+    for (int r = 0; r < 16; ++r) none[b] = fmaf(o[b][r], 0.f, none[b]);
+    if (b) none[0] += none[b];
+  }
+  if (__any(none[0] != 0.f)) {                                  // one is NaN
+    walk_again<DT, DP, BN>(wave);
     return;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int b = 0; b < DB; ++b)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int at = 32 * b + 8 * r + 4 * g;
-      if (at < a.d)
-        *reinterpret_cast<uint2*>(a.out + to * a.d + at) =
-            make_uint2(pack2<DT>(o[b][4 * r] * inv, o[b][4 * r + 1] * inv),
-                       pack2<DT>(o[b][4 * r + 2] * inv, o[b][4 * r + 3] * inv));
-    }
-  if (a.lse && g == 0) a.lse[to] = l == 0.f ? -INFINITY : kLn2 * (m + log2_hw(l));
+  l += __shfl_xor(l, 32, kWave);
+  store_blocks<DT>(a, p, row, g, o, 0, m, l);
 }
 
 // One workgroup per row and 1024 of its outputs: the pieces of the row's tile brought to their common maximum and

@@ -506,6 +506,8 @@ spa_status attention_decode(const spa_heads* q, int32_t n_seqs, int32_t n_q_head
  * causal != 0, j <= i + lk - lq (the last query sees every key: prompts
  * whose beginning is cached have lk > lq), and every key otherwise.  A query
  * that sees none gets zeros and lse -inf.
+ * Keys and values that a query does not see do not enter its output,
+ * whatever they hold; a NaN or an infinity that it sees does.
  *  q, k, v   tq rows of n_q_heads and tk rows of n_kv_heads vectors of dtype
  *            (SPA_F16 or SPA_BF16)
  *  cu_q, cu_k [device] [n_seqs + 1] int32, ascending from 0

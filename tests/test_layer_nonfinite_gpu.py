@@ -47,6 +47,86 @@ def check_rows(got, got_lse, q, k, v, visible, scale, dtype, codes=False):
 # ---------------------------------------------------------------------------------------------------------------
 # prompts
 # ---------------------------------------------------------------------------------------------------------------
+def prompt(dtype, hq, hkv, d, lens_q, lens_k, causal, bad, seed=0):
+    """bad: (sequence, position, dimensions, value of k or None, value of v or None)."""
+    print(f"[prompt] {dtype} heads {hq}/{hkv}x{d} q {lens_q} k {lens_k} causal {causal}", flush=True)
+    g = gen(seed)
+    q, k, v = (torch.randn((sum(n), h, d), generator=g, device="cuda").to(dtype)
+               for n, h in ((lens_q, hq), (lens_k, hkv), (lens_k, hkv)))
+    first = [sum(lens_k[:s]) for s in range(len(lens_k))]
+    for s, at, dims, of_k, of_v in bad:
+        if of_k is not None:
+            k[first[s] + at, :, dims] = of_k
+        if of_v is not None:
+            v[first[s] + at, :, dims] = of_v
+    out, lse = spa.attention_prefill(q, k, v, offsets(lens_q), offsets(lens_k), causal=causal, want_lse=True)
+    a = c = 0
+    for lq, lk in zip(lens_q, lens_k):
+        i, j = torch.arange(lq, device="cuda")[:, None], torch.arange(lk, device="cuda")[None, :]
+        visible = (j <= i + lk - lq) if causal else torch.ones((lq, lk), dtype=torch.bool, device="cuda")
+        ks = k[c:c + lk].double()
+        sick = ~torch.isfinite(ks).all(-1).all(-1)
+        hit = (visible & sick).any(-1)                  # rows that see a key with a NaN or an infinity
+        if bool(hit.any()):
+            assert out[a:a + lq][hit].isnan().all() and lse[a:a + lq][hit].isnan().all()
+        ok = ~hit
+        check_rows(out[a:a + lq][ok], lse[a:a + lq][ok], q[a:a + lq][ok].double(), ks.masked_fill(~torch.isfinite(ks), 0.0),
+                   v[c:c + lk].double(), visible[ok] & ~sick, d ** -0.5, dtype)
+        a, c = a + lq, c + lk
+
+
+ALL, SOME = slice(None), slice(3, 6)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256, 40, 96, 160])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_prompt_values_of_hidden_keys(dtype, d, value):
+    # later positions of the same sequence, in the tile of the diagonal and in later ones
+    prompt(dtype, 4, 2, d, [200], [200], True, [(0, 199, SOME, None, value)], seed=d)
+    prompt(dtype, 4, 2, d, [130, 90], [130, 90], True, [(0, 70, ALL, None, value), (1, 33, SOME, None, value)], seed=d + 1)
+    prompt(dtype, 2, 2, d, [37], [300], True, [(0, 290, SOME, None, value), (0, 264, SOME, None, value)], seed=d + 2)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_both_infinities_and_the_last_key(d):
+    # the tail past the last key repeats nothing that a row does not see
+    prompt(BF16, 4, 2, d, [70], [70], False, [(0, 69, SOME, None, INF)], seed=1)
+    prompt(BF16, 4, 2, d, [70], [70], True, [(0, 69, SOME, None, -INF)], seed=2)
+    prompt(F16, 4, 2, d, [150], [150], True, [(0, 10, SOME, None, INF), (0, 80, SOME, None, -INF)], seed=3)
+    prompt(BF16, 4, 2, d, [5, 1], [1, 65], False, [(0, 0, SOME, None, INF), (1, 64, SOME, None, NAN)], seed=4)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_divided_keys_with_hidden_values(d):
+    assert spa.lib().spa_attention_prefill_workspace_bytes(100, 3000, 1, 4, d) > 0
+    prompt(BF16, 4, 2, d, [100], [3000], True, [(0, 2950, SOME, None, NAN)], seed=5)
+    prompt(F16, 4, 2, d, [100], [3000], True, [(0, 700, SOME, None, INF), (0, 2999, ALL, None, NAN)], seed=6)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 40])
+def test_prompt_hidden_keys(d):
+    # NaN and infinities in keys themselves; rows that see one have no softmax
+    prompt(BF16, 4, 2, d, [200], [200], True, [(0, 100, slice(1), NAN, None)], seed=7)
+    prompt(F16, 4, 2, d, [33], [150], True, [(0, 130, ALL, NAN, NAN)], seed=8)
+
+
+@pytest.mark.parametrize("d", [64, 128, 40, 96, 160])
+def test_prompt_scores_of_minus_infinity(d):
+    # a key with an infinite element that every query meets with the other sign weighs nothing
+    g = gen(d)
+    for lk in (50, 2500):
+        q, k, v = (torch.randn((n, 2, d), generator=g, device="cuda").to(BF16) for n in (20, lk, lk))
+        q[:, :, 2] = q[:, :, 2].abs() + 0.25
+        k[31, :, 2] = -INF
+        out, lse = spa.attention_prefill(q, k, v, offsets([20]), offsets([lk]), causal=False, want_lse=True)
+        visible = torch.ones((20, lk), dtype=torch.bool, device="cuda")
+        visible[:, 31] = False
+        kf = k.double()
+        kf[31] = 0.0
+        A.check(out, lse, A.reference(q, kf, v, d ** -0.5, visible), BF16)
+
+
 @pytest.mark.parametrize("lk", [40, 3000])
 @pytest.mark.parametrize("d", [64, 256])
 def test_prompt_rows_of_nan(d, lk):
