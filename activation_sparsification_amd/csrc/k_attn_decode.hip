@@ -232,6 +232,12 @@ __device__ __forceinline__ uint4 stream_load16(const void* p) {
   const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// The same from an address of 8-byte alignment: rows of 8-bit codes where head_dim is an odd multiple of 8.
+typedef uint32_t u32x4_by8 __attribute__((ext_vector_type(4), aligned(8)));
+__device__ __forceinline__ uint4 stream_load16_by8(const void* p) {
+  const u32x4_by8 v = __builtin_nontemporal_load(static_cast<const u32x4_by8*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
 // The first `live` of W words, the others 0 (live is W, W / 2 or 0: whole 8-element pieces).
 template <int W>
 __device__ __forceinline__ void stream_load(const char* p, int live, uint32_t (&w)[W]) {
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
             const int bytes = d * ES - (16 * g + 64 * c);              // left in the row; whole 8-element pieces
             const char* from = base + (k_lane + 64 * c);
             if (bytes >= 16) {
-              const uint4 v = stream_load16(from);
+              const uint4 v = FMT == SPA_KV_NATIVE ? stream_load16(from) : stream_load16_by8(from);
               w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
             } else if (bytes > 0) {
               w[0] = reinterpret_cast<const uint32_t*>(from)[0];

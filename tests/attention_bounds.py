@@ -35,6 +35,7 @@ def reference(q, k, v, scale, visible):
         r[name] = torch.zeros_like(r["lse"])
     r["top"] += 1.0
     r["vmax"] = float(v.abs().max()) if lk else 0.0
+    r["keys"] = visible.sum(-1).double()[:, None, None]
     if lk == 0 or lq == 0:
         return r
     seen = visible.double()
@@ -64,7 +65,6 @@ def reference(q, k, v, scale, visible):
         r["top"][:, heads] = total.squeeze(-1).clamp(min=1.0).T
         r["ds"][:, heads] = ((d + 8) * 2.0 ** -24 * size).T
         r["smax"][:, heads] = s.masked_fill(~visible, 0.0).abs().amax(-1).T
-    r["keys"] = visible.sum(-1).double()[:, None, None]
     return r
 
 
