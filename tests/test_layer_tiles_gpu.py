@@ -70,3 +70,35 @@ FORMATS = ["native", "fp8", "int8"]
 def test_rows_that_start_on_8_bytes(fmt, dtype, d):
     walk(dtype, fmt, 1024, 2, d, 16, [2500, 3001], (4, 12))
 
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256, 40, 96, 200])
+@pytest.mark.parametrize("page", [16, 48, 7, 8])
+def test_tiles_of_a_wave(fmt, dtype, d, page):
+    walk(dtype, fmt, 1024, 2, d, page, [6001, 3, 4100, 0, 777], (6, 24))
+    walk(dtype, fmt, 1024, 2, d, page, [6001, 3, 4100, 0, 777], (6, 24), rising=12.0, seed=1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d,n", [(64, 60000), (128, 40000), (256, 20000), (96, 40000)])
+@pytest.mark.parametrize("page", [16, 7])
+def test_more_tiles_than_page_numbers_held(fmt, dtype, d, n, page):
+    # a wave holds the page numbers of 32 tiles and reads the next ones on its way
+    walk(dtype, fmt, 1024, 2, d, page, [n, 5, n // 3 + 1], (33, 64), rising=6.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("page", [16, 32, 7])
+def test_absent_pages_on_the_way(fmt, page):
+    last = 5000 // page
+    gone = [(0, c) for c in (0, 1, 17, 18, 19, 20, 100, last - 1)] + [(1, c) for c in range(40)] + [(2, 3)]
+    walk(BF16, fmt, 1024, 2, 128, page, [5000, 3000, 6000], (10, 24), absent=gone, rising=8.0)
+    walk(F16, fmt, 1024, 2, 72, page, [5000, 3000, 6000], (10, 24), absent=gone)
+
+
+def test_many_key_value_heads():
+    # 32 key-value heads leave 16 workgroups to each
+    walk(BF16, "fp8", 32, 32, 128, 16, [30000, 9000], (17, 32), rising=6.0)
+    walk(F16, "int8", 64, 32, 64, 16, [20000, 17], (6, 16))
