@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -119,12 +120,13 @@ int dtype_code(at::ScalarType t) {
 // Refuses a tensor whose storage no longer holds it (resized, or given back): elements up to the last one named by
 // sizes and strides.
 void held(const at::Tensor& x, const char* name) {
+  const auto sizes = x.sizes(), strides = x.strides();
   int64_t end = x.storage_offset() + 1;
-  for (int64_t i = 0; i < x.dim(); ++i) {
-    if (x.size(i) == 0) return;
-    end += (x.size(i) - 1) * x.stride(i);
+  for (size_t i = 0; i < sizes.size(); ++i) {
+    if (sizes[i] == 0) return;
+    end += (sizes[i] - 1) * strides[i];
   }
-  if ((int64_t)x.storage().nbytes() < end * (int64_t)x.element_size())
+  if (x.unsafeGetTensorImpl()->unsafe_storage().nbytes() < (uint64_t)end * x.element_size())
     refuse(std::string(name) + ": its storage is smaller than the tensor");
 }
 
@@ -151,6 +153,8 @@ spa_heads heads(const at::Tensor& x, const char* name) {
   return spa_heads{x.data_ptr(), x.size(0) > 1 ? x.stride(0) : 0, x.size(1) > 1 ? x.stride(1) : 0};
 }
 
+// The current stream of a device.  Kernels go to the current device whatever their stream: every call holds a guard of its
+// tensors' device around its allocations and the library's entry.
 void* stream_of(at::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
 at::Tensor fresh(c10::IntArrayRef shape, at::ScalarType type, at::Device dev) {
@@ -317,6 +321,7 @@ PyObject* py_kv_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const at::Tensor &k = tensor(a.v[0], "k"), &v = tensor(a.v[1], "v"), &slots = tensor(a.v[2], "slots");
     const Pages kv = cache(a.v[3]);
     const spa_heads kh = heads(k, "k"), vh = heads(v, "v");
+    const c10::DeviceGuard on(kv.dev);
     need(k.device() == kv.dev && v.device() == kv.dev, "kv_write: tensors on several devices");
     need(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(), "kv_write: k and v differ in shape or type");
     need(k.size(1) == kv.c.n_heads && k.size(2) == kv.c.head_dim, "kv_write: the cache has other heads");
@@ -349,6 +354,7 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObje
     const at::Tensor &table = tensor(a.v[1], "page_table"), &cu = tensor(a.v[2], "cu_seqlens");
     const int32_t total = integer(a.v[3], "total");
     need(total >= 0, "total: expected 0 or more");
+    const c10::DeviceGuard on(kv.dev);
     const int32_t max_pages = table_width(table, -1, kv.dev);
     const int32_t n = size32(table.size(0), "page_table");
     given(cu, {(int64_t)n + 1}, at::kInt, kv.dev, "cu_seqlens");
@@ -403,6 +409,7 @@ PyObject* py_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n_arg
     const spa_heads qh = heads(q, "q");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
+    const c10::DeviceGuard on(dev);
     need(kv.dev == dev, "attention_decode: tensors on several devices");
     need(q.size(2) == kv.c.head_dim, "attention_decode: the cache has another head_dim");
     const int32_t n = size32(q.size(0), "q"), hq = size32(q.size(1), "q"), d = kv.c.head_dim;
@@ -438,6 +445,7 @@ PyObject* py_attention_prefill(PyObject*, PyObject* const* args, Py_ssize_t n_ar
     const spa_heads qh = heads(q, "q"), kh = heads(k, "k"), vh = heads(v, "v");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
+    const c10::DeviceGuard on(dev);
     need(k.sizes() == v.sizes() && k.size(2) == q.size(2), "attention_prefill: k and v are [tk, n_kv_heads, head_dim]");
     need(dtype_code(type) >= 0 && k.scalar_type() == type && v.scalar_type() == type,
          "attention_prefill: q, k and v differ in type");
@@ -499,6 +507,7 @@ PyObject* py_gated_residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n_
     need(x.is_cuda() && x.dim() == 2 && x.is_contiguous(), "x: expected a contiguous device tensor [t, c]");
     const int64_t t = x.size(0), c = x.size(1);
     const at::Device dev = x.device();
+    const c10::DeviceGuard on(dev);
     const at::ScalarType type = x.scalar_type();
     need(dtype_code(type) >= 0, "x: expected float32, float16 or bfloat16");
     held(x, "x");
