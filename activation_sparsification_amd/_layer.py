@@ -1,7 +1,8 @@
 """The cache, attention and norm calls: thin native binding (``_layer_native``) of the C entries in ``libspa.so``.
 
 Tensors of several heads are ``[rows, heads, head_dim]`` with the last axis dense; the row and head strides are
-free (a slice of a packed projection is passed as it is).  Workspaces come from torch's allocator on the current
+free (a slice of a packed projection is passed as it is).  Forward only: a tensor that requires a gradient is refused
+while gradients are recorded.  Workspaces come from torch's allocator on the current
 stream for each call, so calls on several streams do not share one.  If the library or the binding is not built,
 importing this module raises: there is no fallback path.
 """

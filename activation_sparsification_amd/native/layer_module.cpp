@@ -7,6 +7,7 @@
 #include <structmember.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -90,7 +91,14 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     PyErr_Format(PyExc_TypeError, "%s: expected a tensor, not %s", name, Py_TYPE(o)->tp_name);
     throw Raised();
   }
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // forward only: a graph must not end here unnoticed
+  if (t.requires_grad() && at::GradMode::is_enabled()) {
+    PyErr_Format(PyExc_ValueError, "%s: requires a gradient, and this call has no backward; detach it or call under "
+                 "torch.no_grad()", name);
+    throw Raised();
+  }
+  return t;
 }
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
