@@ -175,9 +175,15 @@ at::Tensor output(PyObject* o, Shape shape, at::ScalarType type, at::Device dev,
   given(t, shape, type, dev, name);
   return t;
 }
+// Tells autograd that a tensor was written, as torch's own operations in place do: a backward that kept its old values is
+// then an error.
+void written(const at::Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 // `o` itself where it was given (callers compare identity), else a new Python tensor.
 PyObject* back(PyObject* o, const at::Tensor& t) {
   if (o) {
+    written(t);
     Py_INCREF(o);
     return o;
   }
@@ -337,6 +343,8 @@ PyObject* py_kv_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const spa_kv_cache c = cache_for(kv, k.scalar_type());
     check(spa_kv_write(&kh, &vh, size32(k.size(0), "k"), static_cast<const int32_t*>(slots.data_ptr()), &c,
                        stream_of(kv.dev)), "spa_kv_write");
+    for (PyObject* part : reinterpret_cast<const KvCache*>(a.v[3])->part)
+      if (part && part != Py_None) written(THPVariable_Unpack(part));
     Py_RETURN_NONE;
   });
 }

@@ -55,3 +55,45 @@ def test_outputs_that_require_a_gradient_are_refused():
         spa.attention_prefill(given["q"], given["k"], given["v"], cu, out=out)
     with torch.no_grad():
         assert spa.attention_prefill(given["q"], given["k"], given["v"], cu, out=out)[0] is out
+
+
+def saved(t):
+    """A loss whose backward needs the present values of t (which shares memory with what is returned)."""
+    leaf = torch.ones_like(t, requires_grad=True)
+    return (leaf * t).sum()
+
+
+def test_writes_are_known_to_autograd():
+    # a backward that kept the values a call has since overwritten is an error, not a wrong gradient
+    all_calls = arguments()
+    (_, a), (_, p), (_, n) = all_calls["prefill"], all_calls["decode"], all_calls["norm"]
+    cu, table = torch.tensor([0, 6], dtype=I32, device="cuda"), torch.tensor([[1, 0]], dtype=I32, device="cuda")
+    slots, ln = torch.arange(16, 22, dtype=I32, device="cuda"), torch.tensor([6], dtype=I32, device="cuda")
+    cache = spa.new_kv_cache(2, 16, 2, 64, BF16, "int8")
+    native = spa.KvCache(p["ck"], p["cv"])
+    out, one = torch.zeros((6, 4, 64), dtype=BF16, device="cuda"), torch.zeros((1, 4, 64), dtype=BF16, device="cuda")
+    k, v = torch.zeros_like(a["k"]), torch.zeros_like(a["v"])
+    for name, targets, call in (
+            ("prefill", [out], lambda: spa.attention_prefill(a["q"], a["k"], a["v"], cu, out=out)),
+            ("decode", [one], lambda: spa.attention_decode(a["q"][:1], native, table, ln, out=one)),
+            ("write", [native.k, native.v], lambda: spa.kv_write(a["k"], a["v"], slots, native)),
+            ("write int8", [cache.k_scale, cache.v_scale], lambda: spa.kv_write(a["k"], a["v"], slots, cache)),
+            ("read", [k, v], lambda: spa.kv_read(native, table, cu, 6, k_out=k, v_out=v)),
+            ("norm", [n["r"], n["x"]], lambda: spa.gated_residual_norm(n["x"], n["r"], h_out=n["r"], y_out=n["x"]))):
+        losses = [saved(t) for t in targets]
+        call()
+        for loss in losses:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+        call()
+        for t in targets:
+            saved(t).backward()
+
+
+def test_inference_tensors_are_written():
+    with torch.inference_mode():
+        call, given = arguments()["norm"]
+        want = spa.gated_residual_norm(given["x"], given["r"])
+        h, y = torch.empty_like(given["r"]), torch.empty_like(given["x"])
+    got = spa.gated_residual_norm(given["x"], given["r"], h_out=h, y_out=y)
+    assert got[0] is h and torch.equal(h, want[0]) and torch.equal(y, want[1])
