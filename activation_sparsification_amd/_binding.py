@@ -7,8 +7,10 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -189,6 +191,25 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _current(device):
+    """Makes a device the current one, where it is not: kernels go to the current device whatever their stream."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _on_device(call):
+    """A call with its first tensor's device current."""
+    @functools.wraps(call)
+    def on(*args, **kwargs):
+        first = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
+        if first is None:
+            return call(*args, **kwargs)
+        with _current(first.device):
+            return call(*args, **kwargs)
+    return on
+
+
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -242,6 +263,7 @@ def workspace(entry: int, t: int, k: int, n_out: int, dtype: torch.dtype, cfg: P
     return ws
 
 
+@_on_device
 def prepare_weight(w: torch.Tensor, alpha: float = 0.0, want_wt: bool = True) -> PreparedWeight:
     """Channel-major copy, per-channel norm^alpha and row sums of W[n_out, k]."""
     dev = _dev(w)
@@ -254,6 +276,7 @@ def prepare_weight(w: torch.Tensor, alpha: float = 0.0, want_wt: bool = True) ->
     return PreparedWeight(w, wt, cs, rs)
 
 
+@_on_device
 def prune_nm(x: torch.Tensor, cfg: PruneConfig, chan_scale: Optional[torch.Tensor] = None,
              eta_in: Optional[torch.Tensor] = None, want_idx: bool = True):
     """Returns ``(vals [t, k*n/m], idx [t, k*n/m] uint8 or None, eta [t], nu [t])``."""
@@ -272,6 +295,7 @@ def prune_nm(x: torch.Tensor, cfg: PruneConfig, chan_scale: Optional[torch.Tenso
     return vals, idx, eta, nu
 
 
+@_on_device
 def sparse_ffn_relu2_prefill(x: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, want_idx: bool = False,
                              out: Optional[torch.Tensor] = None):
     """y = prune24(max(x W_up^T, 0)^2) W_down^T; returns (y [t, n_out], idx [t, ffn/2] uint8 or None)."""
@@ -302,6 +326,7 @@ class EtaCalibration:
         self.sums = torch.zeros(vocab, dtype=torch.float64, device=device)
         self.counts = torch.zeros(vocab, dtype=torch.int32, device=device)
 
+    @_on_device
     def add(self, x: torch.Tensor, token_ids: torch.Tensor) -> None:
         dev = _dev(x)
         t, k = x.shape
@@ -312,11 +337,13 @@ class EtaCalibration:
     def table(self) -> torch.Tensor:
         dev = self.sums.device
         out = torch.empty(self.vocab, dtype=torch.float32, device=dev)
-        _check(lib().spa_eta_table(_ptr(self.sums), _ptr(self.counts), self.vocab, _ptr(out), _stream(dev)),
-               "spa_eta_table")
+        with _current(dev):
+            _check(lib().spa_eta_table(_ptr(self.sums), _ptr(self.counts), self.vocab, _ptr(out), _stream(dev)),
+                   "spa_eta_table")
         return out
 
 
+@_on_device
 def eta_lookup(table: torch.Tensor, token_ids: torch.Tensor) -> torch.Tensor:
     """Per-token static shift: the table entry of each token id (0 outside the table)."""
     dev = _dev(table)
@@ -327,6 +354,7 @@ def eta_lookup(table: torch.Tensor, token_ids: torch.Tensor) -> torch.Tensor:
     return out
 
 
+@_on_device
 def prepare_amber(w: torch.Tensor, alpha: float = 1.0) -> torch.Tensor:
     """Amber-Pruner channel factor of W[n_out, k]: a float32 [k] chan_scale for the weight-aware score."""
     dev = _dev(w)
@@ -344,6 +372,7 @@ def meta_row_bytes(k: int, n: int, m: int, fmt: str = "comb") -> int:
     return int(lib().spa_meta_row_bytes(k, n, m, META[fmt]))
 
 
+@_on_device
 def encode_meta(idx: torch.Tensor, n: int, m: int, fmt: str = "comb") -> torch.Tensor:
     """uint8 in-block positions [t, k*n/m] -> packed codes, uint32 [t, row_bytes/4] (as int32 storage)."""
     dev = _dev(idx)
@@ -356,6 +385,7 @@ def encode_meta(idx: torch.Tensor, n: int, m: int, fmt: str = "comb") -> torch.T
     return codes
 
 
+@_on_device
 def decode_meta(codes: torch.Tensor, k: int, n: int, m: int, fmt: str = "comb") -> torch.Tensor:
     """Packed codes [t, row_words] -> uint8 in-block positions [t, k*n/m]."""
     dev = _dev(codes)
@@ -384,12 +414,14 @@ def _linear(fn_name: str, entry: int, x: torch.Tensor, pw: PreparedWeight, cfg: 
     return y, idx, nu
 
 
+@_on_device
 def sparse_linear_decode(x, pw: PreparedWeight, cfg: PruneConfig, eta_in=None, want_idx=False, want_nu=False,
                          out=None, ws=None, wt=None):
     """Fused prune + row-skipping GEMV for 1..32 tokens.  Returns ``(y, idx, nu)``."""
     return _linear("sparse_linear_decode", ENTRY_DECODE, x, pw, cfg, eta_in, want_idx, want_nu, out, ws, wt)
 
 
+@_on_device
 def sparse_linear_decode_static(x, pw: PreparedWeight, cfg: PruneConfig, eta_in=None, want_idx=False, want_nu=False,
                                 out=None, wt=None):
     """sparse_linear_decode on the library's static per-GPU scratch (no workspace).  Returns ``(y, idx, nu)``."""
@@ -405,6 +437,7 @@ def sparse_linear_decode_static(x, pw: PreparedWeight, cfg: PruneConfig, eta_in=
     return y, idx, nu
 
 
+@_on_device
 def sparse_linear_prefill(x, pw: PreparedWeight, cfg: PruneConfig, eta_in=None, want_idx=False, want_nu=False,
                           out=None, ws=None):
     """Prune/pack pass + matrix-core GEMM (sparse MFMA for 2:4).  Returns ``(y, idx, nu)``."""
@@ -418,6 +451,7 @@ class Fp8Weight:
     scale: torch.Tensor                  # [n_out] float32
 
 
+@_on_device
 def prepare_weight_fp8(w: torch.Tensor) -> Fp8Weight:
     """Row-scaled e4m3 copy of a 16-bit weight ``[n_out, k]`` for the FP8 2:4 prefill."""
     dev = _dev(w)
@@ -429,6 +463,7 @@ def prepare_weight_fp8(w: torch.Tensor) -> Fp8Weight:
     return Fp8Weight(codes, scale)
 
 
+@_on_device
 def sparse_linear_prefill_fp8(x, pw: PreparedWeight, w8: Fp8Weight, cfg: PruneConfig, eta_in=None, want_idx=False,
                               want_nu=False, out=None, ws=None):
     """2:4 prefill with FP8 operands (pruning pass + FP8 sparse MFMA GEMM).  Returns ``(y, idx, nu)``."""
@@ -462,6 +497,7 @@ class PreparedCall:
         self._wd = pw.c(wt=wt, w=w)
         self._fn = getattr(lib(), fn_name)
         self._name = fn_name
+        self._device = x.device
         t = x.shape[0]
         fp8 = fn_name == "sparse_linear_prefill_fp8"
         if fp8 != (w8 is not None):
@@ -473,6 +509,7 @@ class PreparedCall:
                              0 if ws is None else ws.numel(), _stream(x.device))
 
     def __call__(self):
-        st = self._fn(*self._args)
+        with _current(self._device):
+            st = self._fn(*self._args)
         if st != SPA_OK:
             raise SpaError(st, self._name)
