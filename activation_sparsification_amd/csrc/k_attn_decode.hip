@@ -1,12 +1,14 @@
 // Attention of one new token per sequence over its paged cache: out = softmax(scale q K^T) V.
 //
-// Bound: the cache is read once and every cached vector meets only the G query heads that share it, so the
-// call is bound by HBM.  A wave works on tiles of 32 positions of one (sequence, key-value head) and keeps
+// Bound: the cache is read once for every 16 query heads that share it, and does little work: bound by HBM, at 0.71 to
+// 0.79 of the rate of a stream that is only read (7.2 TB/s on this card; a copy moves 4.9).  A wave works on tiles of 32 positions of one (sequence, key-value head) and keeps
 // everything in registers:
 //   S^T = K Q^T on v_mfma_f32_16x16x32: a lane's K operand is 16 consecutive bytes of a cached row, so keys go
 //         from memory to the matrix cores with no LDS; the 16 columns are the query heads (zeros past G);
-//   O^T = V^T P^T: the scores' own registers are the P operand (the order of the 32 positions along the
-//         product is free, so it is taken as S^T leaves it: lane group g holds 4g..4g+3 and 16+4g..16+4g+3).
+//   O^T = V^T P^T: the scores' own registers are the P operand, each weight rounded to 16 bits, which is the output's own
+//         unit roundoff (0.0023 of the 2-norm against 0.0017 for float32 weights, bfloat16 over e4m3; more bits would take
+//         a second product).  The order of the 32 positions along the product is free, so it is taken as S^T leaves it:
+//         lane group g holds 4g..4g+3 and 16+4g..16+4g+3.
 //         A lane reads those 8 positions' rows, 16 lanes to a row, and turns its 8 x 8 block with byte
 //         permutes into one V^T operand per dimension.
 // The running maximum and sum are one column (query head) per lane.  The tiles of all sequences, end to end, are cut
@@ -14,8 +16,8 @@
 // the lengths on the device.  A sequence that is cut leaves unnormalised float32 sums with their maximum, and a
 // second kernel joins them in a fixed order.
 //
-// 64 ragged sequences of up to 4099 positions (32 heads on 8 of 128, e4m3): 62 us, 5.1 TB/s; two of 100003 (int8): 74.5 us,
-// 5.7 TB/s; one of 61 (16 bits): 5.7 us.
+// 64 ragged sequences of up to 4099 positions (32 heads on 8 of 128, e4m3): 62 us, 5.1 TB/s; two of 100003 (int8,
+// float16): 75 us, 5.6 TB/s; one of 61 (16 bits): 5.8 us.
 #include <algorithm>
 
 #include "spa_attn.h"
@@ -440,8 +442,9 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
 }
 
 // Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave
-// shares.  EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  The page numbers of a wave's next 32 tiles are held one to a lane; keys of the next
-// tile are on their way while this tile's softmax and V product run, and values while its scores are formed.
+// shares.  EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  The page numbers of a wave's next
+// 32 tiles are held one to a lane; keys of the next tile are on their way while this tile's softmax and V product run, and
+// values while its scores are formed.
 template <int DT, int FMT, int DP, bool EXACT>
 __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(DecodeAttnArgs a) {
   constexpr int KC = DP / 32, NV = DP / 16;

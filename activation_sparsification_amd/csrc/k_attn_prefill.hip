@@ -12,9 +12,9 @@
 // tile's keys are divided over workgroups and a second kernel joins the pieces.
 //
 // Bound by the matrix cores and the vector unit together (32 exponentials of 16 cycles beside 32 matrix instructions
-// of 32 per lane and 64 keys).  One causal prompt of 8192 by 32 heads of 128 on 8: 523 us, 1051 TFLOP/s (a large
+// of 32 per lane and 64 keys).  One causal prompt of 8192 by 32 heads of 128 on 8: 522 us, 1053 TFLOP/s (a large
 // library product reaches 1112 on the same card), matrix cores busy 54 % at a sustained 1.98 GHz, no bank conflicts.
-// Nine prompts of up to 1531: 93 us; three pieces over 4093 cached keys by 16 heads of 64: 30 us.
+// Nine prompts of up to 1531: 94 us; three pieces over 4093 cached keys by 16 heads of 64: 30 us.
 #include "spa_attn.h"
 #include "spa_layer.h"
 
@@ -238,7 +238,9 @@ __device__ __forceinline__ void follow(float mx, float& m, float& l, f32x16 (&o)
     for (int b = 0; b < N; ++b) o[b] *= alpha;
   }
 }
-// Scores to weights, rounded to the 16-bit type as operands of the product with V; their sum, unrounded, goes to l.
+// Scores to weights, rounded to the 16-bit type as operands of the product with V; their sum, unrounded, goes to l.  The
+// rounding is the output's own unit roundoff on each weight: 0.0021 of the 2-norm against 0.0016 for float32 weights
+// (8192 bfloat16 keys); two 16-bit parts of a weight would double the product with V, half of all matrix work.
 template <int DT, int NB>
 __device__ __forceinline__ void weights(f32x16 (&s)[NB], uint4 (&pf)[2 * NB], float c, float m, float& l) {
   const float base = m == -INFINITY ? 0.f : m;
@@ -390,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_attention_prefi
   const int sees = visible_end(min(row, lq - 1), lq, lk, a.causal);                       // its first hidden key
 
   // a tile's direct loads: lane -> (row, stored piece); rows past the end repeat the last one, pieces past
-  // head_dim repeat the first (they meet zeros of Q, or give columns of O that are not stored)
+  // head_dim repeat the first (they meet zeros of Q, or give columns of O that are not stored; where they hold an infinity
+  // the sums show it, and the second walk reads neither)
   const uint16_t* kbase = a.k + (size_t)k_first * a.k_row + (size_t)kvh * a.k_head;
   const uint16_t* vbase = a.v + (size_t)k_first * a.v_row + (size_t)kvh * a.v_head;
   auto stage = [&](const uint16_t* base, int64_t stride, int j0, uint32_t lds) {

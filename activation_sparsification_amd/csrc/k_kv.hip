@@ -5,7 +5,7 @@
 // its largest magnitude is a butterfly over the group and nothing passes through memory twice.  A workgroup
 // handles consecutive tokens of one head, keys and values together: consecutive tokens are consecutive positions of
 // a page, so the codes and the 4-byte scales of a workgroup are runs.  8191 tokens by 8 heads of 128 into int8 pages:
-// 11.4 us, 4.5 TB/s; twelve ragged sequences read back from them: 83 us, 4.7 TB/s (a large copy moves 4.9).
+// 11.5 us, 4.5 TB/s; twelve ragged sequences read back from them: 83 us, 4.7 TB/s (a large copy moves 4.9).
 #include "spa_common.h"
 #include "spa_attn.h"
 #include "spa_layer.h"
@@ -209,7 +209,6 @@ hipError_t dispatch(const spa_kv_cache& c, bool write, KvArgs& a, hipStream_t st
   a.scale[0] = c.k_scale; a.scale[1] = c.v_scale;
   a.heads = c.n_heads; a.d = c.head_dim; a.n_pages = c.n_pages;
   a.page = FastDiv((uint32_t)c.page_size);
-  // a native write moves bits: one instance serves both 16-bit types
   if (c.dtype == SPA_F16) return by_format<SPA_F16>(c.format, write, a, st);
   return by_format<SPA_BF16>(c.format, write, a, st);
 }

@@ -97,7 +97,8 @@ inline spa_status check_attention_decode(const spa_heads* q, int32_t n_seqs, int
 // Query heads of one key-value head are worked on 16 at a time (the matrix instruction's columns).
 inline int head_tiles(int n_q_heads, int n_kv_heads) { return (n_q_heads / n_kv_heads + 15) / 16; }
 // Workgroups that share the cache of one key-value head and head tile: as many as the chip holds at a time over all
-// heads, 3, 2 or 1 to a compute unit as the registers for the head's dimensions allow.
+// heads, 3, 2 or 1 to a compute unit as the registers for the head's dimensions allow.  Rounded up: heads that do not
+// divide the places get a few more workgroups than the chip holds (20 heads of 128: 520 on 512).
 inline int decode_groups(int n_q_heads, int n_kv_heads, int head_dim) {
   const int places = head_dim <= 64 ? 768 : head_dim <= 128 ? 512 : 256;
   const int per_unit = n_kv_heads * head_tiles(n_q_heads, n_kv_heads);
@@ -142,8 +143,9 @@ inline spa_status check_attention_prefill(const spa_heads* q, const spa_heads* k
 // estimated (every sequence ends with half a tile); sequences' keys stay on the device, where a piece is at least 4
 // key steps, so a call whose keys altogether are no more than that is not divided.  Of those the number is taken that
 // ends soonest by what was measured: a tile walks its keys at 400 + 6 head_dim ns per 64, whether one workgroup or
-// two stand on its unit (the longest of n sequences is taken as 2n / (n + 1) times their mean); a join costs 5 us, and
-// each piece 4 bytes per output element written and read at 4 TB/s.  Against pieces up to two workgroups on each unit
+// two stand on its unit (the longest of n sequences is taken as 2n / (n + 1) times their mean, which is too short for one
+// long sequence among many short ones: such a call is divided little or not at all); a join costs 5 us, and each piece
+// 4 bytes per output element written and read at 4 TB/s.  Against pieces up to two workgroups on each unit
 // (us): a prompt of 700 by 32 heads of 128 26.4 -> 18.7, six of up to 300 by 16 19.2 -> 12.3, four of 300 18.3 ->
 // 12.4; worst 2000 by 8 heads 29.6 -> 31.5.  One workgroup to a unit takes 75 us for 4000 by 8 heads, this 59.
 constexpr int kPrefillTarget = 512, kMaxSplits = 8;

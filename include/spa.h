@@ -399,8 +399,12 @@ size_t spa_workspace_bytes(int32_t entry, int32_t t, int32_t k, int32_t n_out, i
 
 /* ------------------------------------------------------------------------
  * Between the linear layers: the key-value cache, attention over it and over
- * prompts, and the norms around a block.  float32 throughout for sums,
- * softmax statistics and norms; 16-bit dtypes for the vectors.
+ * prompts, and the norms around a block.  16-bit dtypes for the vectors;
+ * float32 for scores, sums, softmax statistics, partial results and norms.
+ * One value is rounded to the vectors' 16-bit type on the way: a softmax
+ * weight (with an 8-bit cache, times its value's scale) where it meets the
+ * values in the matrix product.  The sum that divides is of the unrounded
+ * weights.
  * ------------------------------------------------------------------------ */
 enum { SPA_KV_NATIVE = 0, SPA_KV_FP8 = 1, SPA_KV_INT8 = 2 };
 enum { SPA_NORM_NONE = 0, SPA_NORM_RMS = 1, SPA_NORM_LAYER = 2 };

@@ -1,4 +1,4 @@
-"""The attention checker of the GPU tests, on the CPU: it passes outputs that are only rounded and rejects outputs with
+"""The attention bounds of the GPU tests, on the CPU: they pass outputs that are only rounded and reject outputs with
 a mistake in them.  The mistakes are planted in what the reference computes."""
 import pytest
 import torch
