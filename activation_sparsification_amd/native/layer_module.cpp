@@ -17,6 +17,7 @@
 #include <cstring>
 #include <exception>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "spa.h"
@@ -125,16 +126,10 @@ int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? SPA_F32 : t == at::kHalf ? SPA_F16 : t == at::kBFloat16 ? SPA_BF16 : -1;
 }
 
-// Refuses a tensor whose storage no longer holds it (resized, or given back): elements up to the last one named by
-// sizes and strides.
-void held(const at::Tensor& x, const char* name) {
-  const auto sizes = x.sizes(), strides = x.strides();
-  int64_t end = x.storage_offset() + 1;
-  for (size_t i = 0; i < sizes.size(); ++i) {
-    if (sizes[i] == 0) return;
-    end += (sizes[i] - 1) * strides[i];
-  }
-  if (x.unsafeGetTensorImpl()->unsafe_storage().nbytes() < (uint64_t)end * x.element_size())
+// Refuses a tensor whose storage no longer holds it (resized, or given back): `elements` from its first to its last.
+void held(const at::Tensor& x, int64_t elements, const char* name) {
+  const c10::TensorImpl* t = x.unsafeGetTensorImpl();
+  if (elements > 0 && t->unsafe_storage().nbytes() < (uint64_t)(t->storage_offset() + elements) * t->itemsize())
     refuse(std::string(name) + ": its storage is smaller than the tensor");
 }
 
@@ -143,7 +138,7 @@ using Shape = std::initializer_list<int64_t>;
 void given(const at::Tensor& x, Shape shape, at::ScalarType type, at::Device dev, const char* name) {
   if (x.scalar_type() == type && x.device() == dev && x.sizes() == c10::IntArrayRef(shape.begin(), shape.size()) &&
       x.is_contiguous()) {
-    held(x, name);
+    held(x, x.numel(), name);
     return;
   }
   std::string s = std::string(name) + ": expected a contiguous " + c10::toString(type) + " tensor of shape [";
@@ -156,13 +151,23 @@ void given(const at::Tensor& x, Shape shape, at::ScalarType type, at::Device dev
 spa_heads heads(const at::Tensor& x, const char* name) {
   if (!x.is_cuda()) refuse(std::string(name) + ": expected a device tensor");
   if (x.dim() != 3) refuse(std::string(name) + ": expected [rows, heads, head_dim]");
-  if (x.size(2) > 1 && x.stride(2) != 1) refuse(std::string(name) + ": expected a dense last axis");
-  held(x, name);
-  return spa_heads{x.data_ptr(), x.size(0) > 1 ? x.stride(0) : 0, x.size(1) > 1 ? x.stride(1) : 0};
+  const int64_t* n = x.sizes().data();
+  const int64_t* step = x.strides().data();
+  if (n[2] > 1 && step[2] != 1) refuse(std::string(name) + ": expected a dense last axis");
+  const spa_heads h{x.data_ptr(), n[0] > 1 ? step[0] : 0, n[1] > 1 ? step[1] : 0};
+  held(x, x.numel() ? (n[0] - 1) * h.row_stride + (n[1] - 1) * h.head_stride + n[2] : 0, name);
+  return h;
 }
 
-// The current stream of a device.  Kernels go to the current device whatever their stream: every call holds a guard of its
-// tensors' device around its allocations and the library's entry.
+// Makes a device current while it lives, if it is not.  Kernels go to the current device whatever their stream: every call
+// holds one around its allocations and the library's entry.
+struct OnDevice {
+  std::optional<c10::DeviceGuard> guard;
+  explicit OnDevice(at::Device dev) {
+    if (c10::impl::getDeviceGuardImpl(dev.type())->getDevice() != dev) guard.emplace(dev);
+  }
+};
+// The current stream of a device.
 void* stream_of(at::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
 at::Tensor fresh(c10::IntArrayRef shape, at::ScalarType type, at::Device dev) {
@@ -231,8 +236,8 @@ Pages pages_of(PyObject* const (&p)[4]) {
   need(k.is_cuda(), "KvCache: expected device tensors");
   need(k.dim() == 4 && k.is_contiguous(), "KvCache: k is [n_pages, n_heads, page_size, head_dim], contiguous");
   const at::ScalarType type = k.scalar_type();
-  const int64_t n = k.size(0), h = k.size(1), s = k.size(2), d = k.size(3);
-  given(k, {n, h, s, d}, type, k.device(), "KvCache.k");
+  const int64_t n = k.sizes()[0], h = k.sizes()[1], s = k.sizes()[2], d = k.sizes()[3];
+  held(k, k.numel(), "KvCache.k");
   given(v, {n, h, s, d}, type, k.device(), "KvCache.v");
   spa_kv_cache c{};
   c.format = type == at::kFloat8_e4m3fn ? SPA_KV_FP8 : type == at::kChar ? SPA_KV_INT8 : SPA_KV_NATIVE;
@@ -335,7 +340,7 @@ PyObject* py_kv_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const at::Tensor &k = tensor(a.v[0], "k"), &v = tensor(a.v[1], "v"), &slots = tensor(a.v[2], "slots");
     const Pages kv = cache(a.v[3]);
     const spa_heads kh = heads(k, "k"), vh = heads(v, "v");
-    const c10::DeviceGuard on(kv.dev);
+    const OnDevice on(kv.dev);
     need(k.device() == kv.dev && v.device() == kv.dev, "kv_write: tensors on several devices");
     need(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(), "kv_write: k and v differ in shape or type");
     need(k.size(1) == kv.c.n_heads && k.size(2) == kv.c.head_dim, "kv_write: the cache has other heads");
@@ -370,7 +375,7 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObje
     const at::Tensor &table = tensor(a.v[1], "page_table"), &cu = tensor(a.v[2], "cu_seqlens");
     const int32_t total = integer(a.v[3], "total");
     need(total >= 0, "total: expected 0 or more");
-    const c10::DeviceGuard on(kv.dev);
+    const OnDevice on(kv.dev);
     const int32_t max_pages = table_width(table, -1, kv.dev);
     const int32_t n = size32(table.size(0), "page_table");
     given(cu, {(int64_t)n + 1}, at::kInt, kv.dev, "cu_seqlens");
@@ -403,7 +408,7 @@ at::Tensor workspace(PyObject* o, size_t bytes, at::Device dev) {
   if (o) {
     const at::Tensor& t = tensor(o, "ws");
     need(t.device() == dev && t.is_contiguous() && t.scalar_type() == at::kByte, "ws: expected a contiguous uint8 tensor");
-    held(t, "ws");
+    held(t, t.numel(), "ws");
     return t;
   }
   return bytes ? fresh({(int64_t)bytes}, at::kByte, dev) : at::Tensor();
@@ -425,7 +430,7 @@ PyObject* py_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n_arg
     const spa_heads qh = heads(q, "q");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
-    const c10::DeviceGuard on(dev);
+    const OnDevice on(dev);
     need(kv.dev == dev, "attention_decode: tensors on several devices");
     need(q.size(2) == kv.c.head_dim, "attention_decode: the cache has another head_dim");
     const int32_t n = size32(q.size(0), "q"), hq = size32(q.size(1), "q"), d = kv.c.head_dim;
@@ -461,7 +466,7 @@ PyObject* py_attention_prefill(PyObject*, PyObject* const* args, Py_ssize_t n_ar
     const spa_heads qh = heads(q, "q"), kh = heads(k, "k"), vh = heads(v, "v");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
-    const c10::DeviceGuard on(dev);
+    const OnDevice on(dev);
     need(k.sizes() == v.sizes() && k.size(2) == q.size(2), "attention_prefill: k and v are [tk, n_kv_heads, head_dim]");
     need(dtype_code(type) >= 0 && k.scalar_type() == type && v.scalar_type() == type,
          "attention_prefill: q, k and v differ in type");
@@ -523,10 +528,10 @@ PyObject* py_gated_residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n_
     need(x.is_cuda() && x.dim() == 2 && x.is_contiguous(), "x: expected a contiguous device tensor [t, c]");
     const int64_t t = x.size(0), c = x.size(1);
     const at::Device dev = x.device();
-    const c10::DeviceGuard on(dev);
+    const OnDevice on(dev);
     const at::ScalarType type = x.scalar_type();
     need(dtype_code(type) >= 0, "x: expected float32, float16 or bfloat16");
-    held(x, "x");
+    held(x, x.numel(), "x");
     at::ScalarType stream_type = type;
     const void* residual = nullptr;
     if (a.v[1]) {
