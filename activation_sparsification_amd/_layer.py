@@ -26,15 +26,21 @@ attention_decode = _native.attention_decode
 attention_prefill = _native.attention_prefill
 gated_residual_norm = _native.gated_residual_norm
 
-PAGE_TYPES = {"native": None, "fp8": torch.float8_e4m3fn, "int8": torch.int8}
+PAGE_TYPES = {"native": None, "fp8": torch.float8_e4m3fn, "int8": torch.int8, "mxfp4": torch.uint8}
 
 
 def new_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, dtype: torch.dtype, fmt: str = "native",
                  device="cuda") -> KvCache:
-    """A zero-filled cache of ``fmt`` "native" (pages of ``dtype``), "fp8" or "int8"."""
+    """A zero-filled cache of ``fmt`` "native" (pages of ``dtype``), "fp8", "int8" or "mxfp4" (two codes to a byte)."""
     if fmt not in PAGE_TYPES:
         raise ValueError(f"new_kv_cache: unknown format {fmt!r}")
     shape = (n_pages, n_heads, page_size, head_dim)
+    if fmt == "mxfp4":
+        if head_dim % 2:
+            raise ValueError(f"new_kv_cache: head_dim {head_dim} leaves half a byte")
+        pages = [torch.zeros((*shape[:3], head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros((n_pages, n_heads, -(-head_dim // 32), page_size), dtype=torch.uint8, device=device) for _ in range(2)]
+        return KvCache(*pages, *scales)
     pages = [torch.zeros(shape, dtype=PAGE_TYPES[fmt] or dtype, device=device) for _ in range(2)]
     scales = [None if fmt == "native" else torch.zeros(shape[:3], device=device) for _ in range(2)]
     return KvCache(*pages, *scales)

@@ -18,39 +18,11 @@
 //
 // 64 ragged sequences of up to 4099 positions (32 heads on 8 of 128, e4m3): 62 us, 5.1 TB/s; two of 100003 (int8,
 // float16): 75 us, 5.6 TB/s; one of 61 (16 bits): 5.8 us.
-#include <algorithm>
-
-#include "spa_attn.h"
-#include "spa_check_layer.h"
-#include "spa_layer.h"
+#include "spa_attn_decode.h"
 
 namespace spa {
 
 namespace {
-
-constexpr int kTile = 32;           // positions a wave takes at a time
-constexpr int kWaves = 4;
-constexpr int kMinTiles = 4;        // tiles of a piece at the least: one for each wave
-
-struct DecodeAttnArgs {
-  const uint16_t* q;
-  int64_t q_row, q_head;
-  const void* k;
-  const void* v;
-  const float* k_scale;
-  const float* v_scale;
-  const int32_t* table;
-  const int32_t* lens;
-  void* out;
-  float* lse;
-  float* part_o;             // [2 workgroups][n_q_heads][d]
-  float2* part_ml;           // [2 workgroups][n_q_heads]
-  int2* part_of;             // [n_seqs]: a sequence's first slot and its number of pieces
-  int n_seqs, hq, hkv, group, d, n_pages, max_pages, head_tiles;
-  int target;                // workgroups of a head at the most
-  float c;                   // scale * log2 e
-  FastDiv page;
-};
 
 // With an 8-bit cache a softmax weight carries its value vector's scale when it is rounded to 16 bits for the matrix
 // product.  bfloat16 has the exponents for it.  For float16 the scales are taken relative to the largest that the wave
@@ -71,91 +43,6 @@ struct ValueScale {
   __device__ __forceinline__ float up() const { return __uint_as_float((uint32_t)(267 - top) << 23); }       // 2^(140 - top)
   __device__ __forceinline__ float down() const { return __uint_as_float((uint32_t)(top - 13) << 23); }      // 2^(top - 140)
 };
-
-// Positions of sequence s that can count, and their tiles.
-__device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int s) {
-  return min(max(a.lens[s], 0), a.max_pages * (int)a.page.d);
-}
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// What a workgroup works through: `per` consecutive tiles of all sequences' tiles laid end to end, so every
-// workgroup of a head has the same share whatever the lengths.  An empty sequence stands as one tile of nothing.
-struct Span {
-  int per;
-  int seq, local;              // where the next piece starts: sequence, tile within it
-  int left;                    // tiles still to do
-  bool fresh;                  // nothing done yet
-  int lens;                    // lane i: the positions of sequence i < 64
-};
-// One piece of a sequence, for one key-value head and up to 16 of its query heads.
-struct Piece {
-  int seq, head, h0, heads;    // key-value head; first query head and their number
-  int len;                     // positions of the sequence
-  int begin, end;              // tiles
-  bool whole;                  // the sequence is this piece alone
-  int slot;                    // where the piece's sums go if not: two slots to a workgroup
-};
-__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(tiles_of(seq_len(a, s)), 1); }
-
-__device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
-  const int lane = threadIdx.x & (kWave - 1);
-  s.lens = lane < a.n_seqs ? seq_len(a, lane) : 0;
-  const int c0 = lane < a.n_seqs ? max(tiles_of(s.lens), 1) : 0;
-  const int incl0 = wave_scan(c0);
-  long long total = __builtin_amdgcn_readlane(incl0, kWave - 1);
-  for (int base = kWave; base < a.n_seqs; base += kWave) {
-    long long c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) c += __shfl_xor(c, off, kWave);
-    total += c;
-  }
-  const int per = (int)max((total + a.target - 1) / a.target, (long long)kMinTiles);
-  const long long start = (long long)blockIdx.x * per;
-  if (start >= total) return false;
-  long long before = 0;
-  int c = c0, incl = incl0, base = 0;
-  uint64_t past;
-  while (!(past = __ballot(before + incl > start))) {
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
-    base += kWave;
-    if (base >= a.n_seqs) return false;
-    c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
-    incl = wave_scan(c);
-  }
-  const int at = __ffsll((unsigned long long)past) - 1;
-  s.per = per;
-  s.seq = base + at;
-  s.local = (int)(start - before) - __builtin_amdgcn_readlane(incl - c, at);
-  s.left = (int)min((long long)per, total - start);
-  s.fresh = true;
-  return true;
-}
-
-__device__ __forceinline__ Piece next_piece(const DecodeAttnArgs& a, Span& s) {
-  Piece p;
-  p.seq = s.seq;
-  const int ht = blockIdx.y / a.hkv;
-  p.head = blockIdx.y % a.hkv;
-  p.heads = min(a.group - 16 * ht, 16);
-  p.h0 = p.head * a.group + 16 * ht;
-  p.len = s.seq < kWave ? __builtin_amdgcn_readlane(s.lens, s.seq) : seq_len(a, s.seq);
-  const int tiles = tiles_of(p.len), share = max(tiles, 1);
-  const int take = min(share - s.local, s.left);
-  p.begin = s.local;
-  p.end = min(s.local + take, tiles);
-  p.whole = take == share;
-  // a piece that starts inside its sequence is its workgroup's first, one that ends inside its last
-  p.slot = 2 * blockIdx.x + (s.local == 0 && !s.fresh);
-  if (s.local == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    const int more = share - take;                              // tiles in the workgroups after this one
-    a.part_of[p.seq] = make_int2(p.slot, 1 + (more + s.per - 1) / s.per);
-  }
-  s.left -= take;
-  ++s.seq;
-  s.local = 0;
-  s.fresh = false;
-  return p;
-}
 
 // Four 8-bit codes as two words of 16-bit values (exact in both types: e4m3 has 4 significant bits, int8 7).
 template <int DT, int FMT>
@@ -193,14 +80,6 @@ __device__ __forceinline__ void widen_row(const uint32_t (&raw)[VW], uint32_t (&
   }
 }
 
-// Largest of the four lanes that hold one column (lanes col, col + 16, + 32, + 48), on each of them.
-__device__ __forceinline__ float across_groups_max(float v) {
-  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
-  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-
 // Largest magnitude of a tile's scales, eight on each lane of a group, on every lane.
 __device__ __forceinline__ float largest(const float (&vs)[8]) {
   float v = fabsf(vs[0]);
@@ -227,13 +106,6 @@ __device__ __forceinline__ void load_q(const DecodeAttnArgs& a, const Piece& p, 
   }
 }
 
-// 16 bytes, or a lane's share of a value row, that are read once.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint4 stream_load16(const void* p) {
-  const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
 // The same from an address of 8-byte alignment: rows of 8-bit codes where head_dim is an odd multiple of 8.
 typedef uint32_t u32x4_by8 __attribute__((ext_vector_type(4), aligned(8)));
 __device__ __forceinline__ uint4 stream_load16_by8(const void* p) {
@@ -279,53 +151,6 @@ __device__ __forceinline__ void stream_load(const char* p, uint32_t (&w)[W]) {
   }
 }
 
-// Joins the four waves and writes the piece's result: lane (col, g) holds dimensions NV * (4 g + r) + i of query
-// head col, its maximum and its own positions' sum; `unit` is what one of o stands for.
-template <int DT, int FMT, int DP>
-__device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, const f32x4 (&o)[DP / 16], float unit, float m,
-                                       float l) {
-  constexpr int NV = DP / 16;
-  __shared__ float s_o[kWaves][16][DP + 4];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int col = lane & 15, g = lane >> 4;
-  l += __shfl_xor(l, 16, kWave);
-  l += __shfl_xor(l, 32, kWave);
-  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = kFollowScale<DT, FMT> ? o[i][r] * unit : o[i][r];
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.heads * (DP / 2); e += kWaves * kWave) {
-    const int h = e / (DP / 2), dim = e % (DP / 2) * 2;
-    if (dim >= a.d) continue;
-    float mx = s_m[0][h];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_hw(s_m[w][h] - base);
-      sum += f * s_l[w][h];
-      x0 += f * s_o[w][h][dim];
-      x1 += f * s_o[w][h][dim + 1];
-    }
-    if (p.whole) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t to = (size_t)p.seq * a.hq + p.h0 + h;
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) = pack2<DT>(x0 * inv, x1 * inv);
-      if (dim == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : kLn2 * (base + log2_hw(sum));
-    } else {
-      const size_t to = (size_t)p.slot * a.hq + p.h0 + h;
-      *reinterpret_cast<float2*>(a.part_o + to * a.d + dim) = make_float2(x0, x1);
-      if (dim == 0) a.part_ml[to] = make_float2(mx, sum);
-    }
-  }
-  __syncthreads();      // the next piece writes here again
-}
-
 // Any page size: a lane finds one position's cell and the others get it by lane exchange.
 template <int DT, int FMT, int DP>
 __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnArgs a) {
@@ -358,8 +183,8 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
       const uint32_t gone = (uint32_t)__ballot(!counts);       // the scores are hidden and the values dropped
       float ksc = 1.f, vsc = 1.f;
       if constexpr (FMT != SPA_KV_NATIVE) {
-        ksc = a.k_scale[cell];
-        vsc = counts ? a.v_scale[cell] : 0.f;
+        ksc = static_cast<const float*>(a.k_scale)[cell];
+        vsc = counts ? static_cast<const float*>(a.v_scale)[cell] : 0.f;
       }
       float t[2][4];
 #pragma unroll
@@ -437,7 +262,7 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode(DecodeAttnA
       }
     }
 
-    finish<DT, FMT, DP>(a, p, o, vmax.down(), m, l);
+    finish<DT, DP, kFollowScale<DT, FMT>>(a, p, o, vmax.down(), m, l);
   } while (span.left > 0);
 }
 
@@ -515,8 +340,8 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
           }
         }
         if constexpr (FMT != SPA_KV_NATIVE) {
-          ksc[b] = *reinterpret_cast<const float4*>(a.k_scale + (size_t)cell[b] + 4 * g);
-          vsc[b] = *reinterpret_cast<const float4*>(a.v_scale + (size_t)cell[b] + 4 * g);
+          ksc[b] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k_scale) + (size_t)cell[b] + 4 * g);
+          vsc[b] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v_scale) + (size_t)cell[b] + 4 * g);
         }
       }
     };
@@ -642,93 +467,13 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_blocks(Deco
         }
       }
     }
-    finish<DT, FMT, DP>(a, p, o, vmax.down(), m, l);
+    finish<DT, DP, kFollowScale<DT, FMT>>(a, p, o, vmax.down(), m, l);
   } while (span.left > 0);
-}
-
-// Joins a sequence's pieces in a fixed order.  A thread takes four dimensions of one head, brings the pieces' sums to
-// their common maximum and adds them; with RUNS > 1 that many threads take every RUNS-th piece of the same four
-// dimensions, and the first of them adds the runs up.
-constexpr int kJoinThreads = 256;
-struct JoinSums {
-  float m, sum;
-  float4 x;
-};
-__device__ __forceinline__ void rescale(JoinSums& j, float m) {
-  const float f = exp2_hw(j.m - (m == -INFINITY ? 0.f : m));
-  j.m = m;
-  j.sum *= f;
-  j.x.x *= f; j.x.y *= f; j.x.z *= f; j.x.w *= f;
-}
-template <int DT, int FMT, int RUNS>
-__global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAttnArgs a) {
-  constexpr int kCols = kJoinThreads / RUNS, U = RUNS > 1 ? 4 : 8;
-  __shared__ JoinSums s_run[RUNS > 1 ? RUNS : 1][RUNS > 1 ? kCols : 1];
-  const int2 of = a.part_of[blockIdx.x];
-  if (of.y == 1) return;
-  const int quads = a.d / 4;
-  const int run = threadIdx.x / kCols, at = blockIdx.y * kCols + threadIdx.x % kCols;
-  const int head = at / quads, dim = at % quads * 4;
-  const bool live = head < a.hq;
-  const int next = of.x & ~1;                  // piece k > 0 is in the first slot of the k-th workgroup after
-  JoinSums j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (live) {
-    for (int i = run; i < of.y; i += U * RUNS) {
-      float2 s[U];
-      float4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = min(i + u * RUNS, of.y - 1);
-        const size_t row = (size_t)(k ? next + 2 * k : of.x) * a.hq + head;
-        s[u] = a.part_ml[row];
-        v[u] = *reinterpret_cast<const float4*>(a.part_o + row * a.d + dim);
-        if (i + u * RUNS >= of.y) {               // none: not a piece of weight 0, whose infinities would give NaN
-          s[u].x = -INFINITY;
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-      float now = j.m;
-#pragma unroll
-      for (int u = 0; u < U; ++u) now = fmaxf(now, s[u].x);
-      rescale(j, now);
-      const float base = now == -INFINITY ? 0.f : now;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float f = exp2_hw(s[u].x - base);
-        j.sum += f * s[u].y;
-        j.x.x += f * v[u].x; j.x.y += f * v[u].y; j.x.z += f * v[u].z; j.x.w += f * v[u].w;
-      }
-    }
-  }
-  if constexpr (RUNS > 1) {
-    s_run[run][threadIdx.x % kCols] = j;
-    __syncthreads();
-    if (run) return;
-    float m = j.m;
-#pragma unroll
-    for (int r = 1; r < RUNS; ++r) m = fmaxf(m, s_run[r][threadIdx.x].m);
-    rescale(j, m);
-#pragma unroll
-    for (int r = 1; r < RUNS; ++r) {
-      JoinSums o = s_run[r][threadIdx.x];
-      rescale(o, m);
-      j.sum += o.sum;
-      j.x.x += o.x.x; j.x.y += o.x.y; j.x.z += o.x.z; j.x.w += o.x.w;
-    }
-  }
-  if (!live) return;
-  const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
-  const size_t to = (size_t)blockIdx.x * a.hq + head;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * a.d + dim) =
-      make_uint2(pack2<DT>(j.x.x * inv, j.x.y * inv), pack2<DT>(j.x.z * inv, j.x.w * inv));
-  if (dim == 0 && a.lse) a.lse[to] = j.sum == 0.f ? -INFINITY : kLn2 * (j.m + log2_hw(j.sum));
 }
 
 template <int DT, int FMT, int DP>
 hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
-  // no more workgroups than the table has room for
-  const int64_t room = ((int64_t)a.max_pages * a.page.d + kTile - 1) / kTile;
-  const int units = (int)std::min<int64_t>(a.target, (std::max<int64_t>(room, 1) * a.n_seqs + kMinTiles - 1) / kMinTiles);
+  const int units = units_of(a);
   const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
   if (a.page.d % 16 == 0 && a.d == DP)
     hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP, true>), grid, block, 0, st, a);
@@ -736,19 +481,7 @@ hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_attention_decode_blocks<DT, FMT, DP, false>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_attention_decode<DT, FMT, DP>), grid, block, 0, st, a);
   if (hipError_t e = hipGetLastError()) return e;
-  // one workgroup to a head cuts nothing
-  if (units == 1) return hipSuccess;
-  // runs side by side where a sequence has 8 pieces or more on the average: four sequences of up to 30000 on 2 heads take
-  // 18.5 us so and 29.0 us in one run; where most have few, more workgroups only cost their start
-  const int quads = a.hq * (a.d / 4);
-  if (units >= 8 * a.n_seqs) {
-    const dim3 join(a.n_seqs, (quads + kJoinThreads / 8 - 1) / (kJoinThreads / 8));
-    hipLaunchKernelGGL((k_attention_decode_join<DT, FMT, 8>), join, dim3(kJoinThreads), 0, st, a);
-  } else {
-    const dim3 join(a.n_seqs, (quads + kJoinThreads - 1) / kJoinThreads);
-    hipLaunchKernelGGL((k_attention_decode_join<DT, FMT, 1>), join, dim3(kJoinThreads), 0, st, a);
-  }
-  return hipGetLastError();
+  return join_pieces<DT>(a, units, st);
 }
 template <int DT, int FMT>
 hipError_t by_dim(const DecodeAttnArgs& a, hipStream_t st) {
@@ -768,19 +501,9 @@ hipError_t by_format(int fmt, const DecodeAttnArgs& a, hipStream_t st) {
 hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads, const spa_kv_cache& c,
                                    const int32_t* table, int max_pages, const int32_t* lens, float scale, void* out,
                                    float* lse, float* part_o, float* part_ml, int32_t* part_of, hipStream_t st) {
-  DecodeAttnArgs a{};
-  a.q = static_cast<const uint16_t*>(q.data);
-  a.q_row = q.row_stride; a.q_head = q.head_stride;
-  a.k = c.k; a.v = c.v; a.k_scale = c.k_scale; a.v_scale = c.v_scale;
-  a.table = table; a.lens = lens; a.out = out; a.lse = lse;
-  a.part_o = part_o; a.part_ml = reinterpret_cast<float2*>(part_ml);
-  a.part_of = reinterpret_cast<int2*>(part_of);
-  a.n_seqs = n_seqs; a.hq = n_q_heads; a.hkv = c.n_heads; a.group = n_q_heads / c.n_heads;
-  a.d = c.head_dim; a.n_pages = c.n_pages; a.max_pages = max_pages;
-  a.head_tiles = spa_check::head_tiles(n_q_heads, c.n_heads);
-  a.target = spa_check::decode_groups(n_q_heads, c.n_heads, c.head_dim);
-  a.c = scale * kLog2e;
-  a.page = FastDiv((uint32_t)c.page_size);
+  if (c.format == SPA_KV_MXFP4)
+    return launch_attention_decode_mx(q, n_seqs, n_q_heads, c, table, max_pages, lens, scale, out, lse, part_o, part_ml, part_of, st);
+  const DecodeAttnArgs a = decode_args(q, n_seqs, n_q_heads, c, table, max_pages, lens, scale, out, lse, part_o, part_ml, part_of);
   return c.dtype == SPA_F16 ? by_format<SPA_F16>(c.format, a, st) : by_format<SPA_BF16>(c.format, a, st);
 }
 

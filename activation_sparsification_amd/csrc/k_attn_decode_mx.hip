@@ -1,0 +1,434 @@
+// Attention of one new token per sequence over a cache held in 4 bits (SPA_KV_MXFP4): out = softmax(scale q K^T) V.
+//
+// Bound by HBM like the other formats (k_attn_decode.hip; the division into pieces is the same), with half the bytes of an
+// 8-bit cache, so there is half the time to unpack them.  Keys are not unpacked at all:
+//   S^T = K Q^T on v_mfma_scale_f32_16x16x128_f8f6f4, whose A operand is e2m1 with one power-of-two scale to 32 elements:
+//         a lane's 16 bytes of a cached row and the scale byte beside them, as they are.  The B operand, the queries, is
+//         e4m3, cut into pieces that together hold them: of each 32 elements (the operand's own blocks) the largest is
+//         brought below 16, and a piece is the nearest integer, the next one 32 times what is left.  Integers up to 16
+//         times codes up to 6 are whole multiples of one half below 2^7, so a product of 128 elements is exact: the unit
+//         aligns the products of 16 elements to the largest and drops what is 2^-14 of it, which a plain split of the
+//         queries into e4m3 numbers loses bits to.  Five pieces hold an element to 2^-24 of the largest.
+//   O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: values are unpacked, with their scales, by v_cvt_scalef32_pk_bf16_fp4 (exact: a
+//         code has two significant bits), pairs of positions brought together by byte permutes.  Softmax weights are
+//         rounded to bfloat16, for a float16 call taken as two bfloat16 numbers in two products (16 bits; bfloat16 keeps
+//         the scales' range).
+#include "spa_attn_decode.h"
+
+namespace spa {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kGroup = 32;           // elements of one scale
+constexpr int kPieces = 5;           // of a query element, 5 bits each
+
+// The query operands of 128 dimensions (one k step): lane (col, g) holds 16 g .. + 15 in the first half of a piece and 64 +
+// 16 g .. + 15 in the second, and the scale of dimensions 32 g .. + 31.  With 64 dimensions or fewer the keys stand twice in
+// the k step (lanes g and g + 2 hold the same), and the second half is the next piece: products p and p + 1 in one.
+template <int DP> constexpr int kProducts = DP == 64 ? (kPieces + 1) / 2 : kPieces;
+template <int DP>
+struct QueryPieces {
+  static constexpr int KS = DP == 64 ? 1 : DP / 128;
+  i32x8 w[KS][kProducts<DP>];
+  int scale[KS][kProducts<DP>];
+};
+
+__device__ __forceinline__ uint32_t fp8_quad(const float* x) { return fp8_pair(x[0], x[1]) | fp8_pair(x[2], x[3]) << 16; }
+
+// 16 elements from q (none of them past d), their pieces' integers, and the exponent byte of the first piece's unit for the
+// block of 32 that they are one half of.
+template <int DT, int N>
+__device__ __forceinline__ int cut_query(const uint16_t* q, int at, int d, bool live, uint32_t (&out)[N][4]) {
+  float x[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (live && at + 8 * h < d) raw = *reinterpret_cast<const uint4*>(q + at + 8 * h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[8 * h + e] = elem16<DT>(raw, e);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+  top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
+  const int up = max((int)(top >> 23), 24);                    // a block below 2^-103 is taken to 2^-127
+  const float k = __uint_as_float((uint32_t)(257 - up) << 23);      // 2^(130 - up): the largest comes to [8, 16)
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] *= k;
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    float n[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      n[e] = rintf(x[e]);
+      x[e] = (x[e] - n[e]) * 32.f;                             // exact; an infinity or a NaN stays NaN in every piece
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[p][i] = fp8_quad(n + 4 * i);
+  }
+  return up - 3;
+}
+
+template <int DT, int DP>
+__device__ __forceinline__ void load_query(const DecodeAttnArgs& a, const Piece& p, int col, int g, QueryPieces<DP>& qp) {
+  const uint16_t* q = a.q + (size_t)p.seq * a.q_row + (size_t)(p.h0 + min(col, p.heads - 1)) * a.q_head;
+  const bool live = col < p.heads;
+  if constexpr (DP == 64) {
+    uint32_t n[2 * kProducts<DP>][4];
+    const int unit = cut_query<DT>(q, 16 * g, a.d, live, n);
+    const int mine = __shfl(unit, col + 32 * (g & 1), kWave);  // of dimensions 32 (g % 2) .. + 31
+#pragma unroll
+    for (int i = 0; i < kProducts<DP>; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        qp.w[0][i][j] = (int)n[2 * i][j];
+        qp.w[0][i][4 + j] = (int)n[2 * i + 1][j];
+      }
+      qp.scale[0][i] = max(mine - 5 * (2 * i + (g >> 1)), 0);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < QueryPieces<DP>::KS; ++s) {
+      uint32_t lo[kPieces][4], hi[kPieces][4];
+      const int u0 = cut_query<DT>(q, 128 * s + 16 * g, a.d, live, lo), u1 = cut_query<DT>(q, 128 * s + 64 + 16 * g, a.d, live, hi);
+      const int a0 = __shfl(u0, col + 32 * (g & 1), kWave), a1 = __shfl(u1, col + 32 * (g & 1), kWave);
+      const int mine = g < 2 ? a0 : a1;                        // of dimensions 128 s + 32 g .. + 31
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qp.w[s][i][j] = (int)lo[i][j];
+          qp.w[s][i][4 + j] = (int)hi[i][j];
+        }
+        qp.scale[s][i] = max(mine - 5 * i, 0);
+      }
+    }
+  }
+}
+
+// S^T of 16 positions: lane (row, g) gives 16 bytes of position row and their scale for each k step.
+template <int DP>
+__device__ __forceinline__ f32x4 scores(const uint4 (&k)[QueryPieces<DP>::KS], const int (&ks)[QueryPieces<DP>::KS],
+                                        const QueryPieces<DP>& q) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < QueryPieces<DP>::KS; ++c) {
+    const i32x8 kf = {(int)k[c].x, (int)k[c].y, (int)k[c].z, (int)k[c].w, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kProducts<DP>; ++i)
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q.w[c][i], s, 4, 0, 0, ks[c], 0, q.scale[c][i]);
+  }
+  return s;
+}
+
+// The exponent byte b of a word as the scale that the conversions take.
+__device__ __forceinline__ float scale_of(uint32_t w, int b) { return __uint_as_float(((w >> (8 * b)) & 0xFFu) << 23); }
+
+template <int SEL>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+}
+
+// Adds this lane's 8 positions to o.  raw: their value rows' codes, NV dimensions each; w: their softmax weights.
+template <int DT, int NV>
+__device__ __forceinline__ void add_values(const uint32_t (&raw)[8][NV > 8 ? NV / 8 : 1], const float (&vs)[8], const float (&w)[8],
+                                           f32x4 (&o)[NV]) {
+  uint4 pf[DT == SPA_F16 ? 2 : 1];
+  {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = pack2<SPA_BF16>(w[2 * j], w[2 * j + 1]);
+      if constexpr (DT == SPA_F16) lo[j] = pack2<SPA_BF16>(w[2 * j] - bf16_to_f32(hi[j] & 0xFFFFu), w[2 * j + 1] - bf16_to_f32(hi[j] >> 16));
+    }
+    pf[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (DT == SPA_F16) pf[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV / 2; ++i) {
+    uint32_t vr[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t r = raw[j][i / 4];
+      vr[j] = i % 4 == 0 ? widen2<0>(r, vs[j]) : i % 4 == 1 ? widen2<1>(r, vs[j]) : i % 4 == 2 ? widen2<2>(r, vs[j]) : widen2<3>(r, vs[j]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sel = e ? 0x07060302u : 0x05040100u;      // the high or low halves of two rows
+      uint4 vf;
+      vf.x = __builtin_amdgcn_perm(vr[1], vr[0], sel);
+      vf.y = __builtin_amdgcn_perm(vr[3], vr[2], sel);
+      vf.z = __builtin_amdgcn_perm(vr[5], vr[4], sel);
+      vf.w = __builtin_amdgcn_perm(vr[7], vr[6], sel);
+#pragma unroll
+      for (const uint4& part : pf) o[2 * i + e] = mfma16<SPA_BF16>(vf, part, o[2 * i + e]);
+    }
+  }
+}
+
+// The running maximum, sum and outputs take in a tile's scores t; w receives its weights.
+template <int NV>
+__device__ __forceinline__ void softmax_step(const float (&t)[8], float& m, float& l, f32x4 (&o)[NV], float (&w)[8]) {
+  float mx = t[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) mx = fmaxf(mx, t[j]);
+  mx = across_groups_max(mx);
+  if (__any(mx > m)) {
+    const float now = fmaxf(m, mx), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+    m = now;
+    l *= alpha;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) o[i] *= alpha;
+  }
+  const float base = m == -INFINITY ? 0.f : m;                 // nothing seen yet: every weight is 0
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w[j] = exp2_hw(t[j] - base);
+    l += w[j];
+  }
+}
+
+// `bytes` of a row's codes from p (whole 4-byte pieces of 8 elements; 16 at the most), the others 0.
+__device__ __forceinline__ uint4 load_codes(const char* p, int bytes) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (4 * i < bytes) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// NV elements of a value row, at NV * col: NV / 2 bytes, none past the row's end.
+template <int NV>
+__device__ __forceinline__ void load_value(const char* row, int col, int bytes, bool live, uint32_t (&w)[NV > 8 ? NV / 8 : 1]) {
+  const int at = NV / 2 * col;
+#pragma unroll
+  for (int i = 0; i < (NV > 8 ? NV / 8 : 1); ++i) {
+    w[i] = 0;
+    if (!live || at + 4 * i >= bytes) continue;
+    if constexpr (NV == 4) w[0] = *reinterpret_cast<const uint16_t*>(row + at);
+    else w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
+  }
+}
+
+// Any page size: a lane finds one position's place and the others get it by lane exchange.
+template <int DT, int DP>
+__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx(DecodeAttnArgs a) {
+  constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = QueryPieces<DP>::KS;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int col = lane & 15, g = lane >> 4;
+  const int kg = DP == 64 ? g & 1 : g;                         // this lane's 32 dimensions of a k step
+  const int bytes = a.d / 2, groups = (a.d + kGroup - 1) / kGroup, page = (int)a.page.d;
+  const uint8_t *k_scale = static_cast<const uint8_t*>(a.k_scale), *v_scale = static_cast<const uint8_t*>(a.v_scale);
+  Span span;
+  if (!find_span(a, span)) return;
+  do {
+    const Piece p = next_piece(a, span);
+    QueryPieces<DP> qp;
+    load_query<DT, DP>(a, p, col, g, qp);
+    f32x4 o[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    for (int tile = p.begin + wave; tile < p.end; tile += kWaves) {
+      // lane i < 32 finds position i's place; a position that does not count is bit i of `gone`
+      const int pos = tile * kTile + (lane & 31);
+      const int p0 = min(pos, p.len - 1);
+      const int pc = (int)a.page.div((uint32_t)p0);
+      const int pg = a.table[(size_t)p.seq * a.max_pages + pc];
+      const bool ok = pg >= 0 && pg < a.n_pages;
+      const int block = ok ? pg * a.hkv + p.head : 0, off = ok ? p0 - pc * page : 0;       // page and head; place in it
+      const uint32_t gone = (uint32_t)__ballot(pos >= p.len || !ok);
+      float t[8];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const size_t kb = (uint32_t)__shfl(block, 16 * b + col, kWave);
+        const int ko = __shfl(off, 16 * b + col, kWave);
+        uint4 kf[KS];
+        int ks[KS];
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          const int at = 64 * c + 16 * kg;
+          kf[c] = load_codes(static_cast<const char*>(a.k) + (kb * page + ko) * bytes + at, bytes - at);
+          ks[c] = at < bytes ? k_scale[(kb * groups + at / 16) * page + ko] : 127;
+        }
+        const f32x4 s = scores<DP>(kf, ks, qp);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[4 * b + r] = (gone >> (16 * b + 4 * g + r)) & 1u ? -INFINITY : s[r] * a.c;
+      }
+      float w[8], vs[8];
+      softmax_step<NV>(t, m, l, o, w);
+      uint32_t raw[8][VW];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 16 * (j / 4) + 4 * g + j % 4;
+        const size_t vb = (uint32_t)__shfl(block, i, kWave);
+        const int vo = __shfl(off, i, kWave);
+        const bool live = !((gone >> i) & 1u) && NV * col < a.d;
+        load_value<NV>(static_cast<const char*>(a.v) + (vb * page + vo) * bytes, col, bytes, live, raw[j]);
+        vs[j] = live ? scale_of(v_scale[(vb * groups + NV * col / kGroup) * page + vo], 0) : 1.f;
+      }
+      add_values<DT, NV>(raw, vs, w, o);
+    }
+    finish<DT, DP, false>(a, p, o, 1.f, m, l);
+  } while (span.left > 0);
+}
+
+// Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave shares.
+// EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  The page numbers of a wave's next 32 tiles are
+// held one to a lane; keys of the next tile are on their way while this tile's softmax and V product run, and values while its
+// scores are formed.
+template <int DT, int DP, bool EXACT>
+__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
+  constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = QueryPieces<DP>::KS;
+  constexpr int kBatch = kWave / 2;                          // tiles whose page numbers are held
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, g = lane >> 4;
+  const int kg = DP == 64 ? g & 1 : g;                       // this lane's 32 dimensions of a k step
+  const int d = EXACT ? DP : a.d, bytes = d / 2, groups = (d + kGroup - 1) / kGroup, page = (int)a.page.d;
+  Span span;
+  if (!find_span(a, span)) return;
+  do {
+    const Piece p = next_piece(a, span);
+    QueryPieces<DP> qp;
+    load_query<DT, DP>(a, p, col, g, qp);
+    f32x4 o[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+
+    const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
+    int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
+    auto fetch_pages = [&](int it) {
+      const int at = ((first + kWaves * (it + lane / 2)) * 2 + (lane & 1)) * 16;
+      pages = -1;
+      if (at < p.len) {
+        pages = a.table[(size_t)p.seq * a.max_pages + a.page.div((uint32_t)at)];
+        if (pages >= a.n_pages) pages = -1;
+      }
+    };
+    // block b of tile number `it`: its page and head, its first place there, and whether the page is there (else the cache's
+    // first page stands in)
+    struct Place { uint32_t block, off; bool there; };
+    auto place_of = [&](int it, int b) {
+      const int pg = __builtin_amdgcn_readlane(pages, 2 * (it % kBatch) + b);
+      const uint32_t at = (uint32_t)((first + kWaves * it) * 2 + b) * 16;
+      if (pg < 0) return Place{0u, 0u, false};
+      return Place{(uint32_t)pg * a.hkv + p.head, at - a.page.div(at) * a.page.d, true};
+    };
+    uint4 kr[2][KS];
+    int ks[2][KS];
+    auto load_k = [&](const Place (&at)[2]) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const char* codes = static_cast<const char*>(a.k) + ((size_t)at[b].block * page + at[b].off) * bytes;
+        const uint8_t* sc = static_cast<const uint8_t*>(a.k_scale) + (size_t)at[b].block * groups * page + at[b].off;
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          const int from = 64 * c + 16 * kg;
+          if constexpr (EXACT) {
+            kr[b][c] = stream_load16(codes + (uint32_t)(col * bytes + from));
+            ks[b][c] = sc[(uint32_t)((4 * c + kg) * page + col)];
+          } else {
+            kr[b][c] = load_codes(codes + (uint32_t)(col * bytes + from), bytes - from);
+            ks[b][c] = from < bytes ? sc[(uint32_t)((4 * c + kg) * page + col)] : 127;
+          }
+        }
+      }
+    };
+    Place at[2];
+    if (n > 0) {
+      fetch_pages(0);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) at[b] = place_of(0, b);
+      load_k(at);
+    }
+    const bool in_row = EXACT || NV * col < d;
+    const int vg = in_row ? NV * col / kGroup : 0;
+    for (int it = 0; it < n; ++it) {
+      const int tile = first + kWaves * it;
+      // values of this tile
+      uint32_t raw[8][VW], vsw[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const char* codes = static_cast<const char*>(a.v) + ((size_t)at[b].block * page + at[b].off) * bytes;
+        const uint8_t* sc = static_cast<const uint8_t*>(a.v_scale) + (size_t)at[b].block * groups * page + at[b].off;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) load_value<NV>(codes + (uint32_t)((4 * g + r) * bytes), col, bytes, in_row, raw[4 * b + r]);
+        vsw[b] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)(vg * page + 4 * g));
+      }
+      // scores
+      float t[8], vs[8], w[8];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const f32x4 s = scores<DP>(kr[b], ks[b], qp);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[4 * b + r] = s[r] * a.c;
+      }
+      // the last tile's end and absent pages: what does not count is removed from the scores and the values
+      const bool cut = (tile + 1) * kTile > p.len || !at[0].there || !at[1].there;
+      uint32_t gone = 0;
+      if (cut) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (tile * kTile + 16 * (j / 4) + 4 * g + j % 4 >= p.len || !at[j / 4].there) {
+            gone |= 1u << j;
+            t[j] = -INFINITY;
+          }
+        }
+      }
+      // keys of the next tile
+      if (it + 1 < n) {
+        if ((it + 1) % kBatch == 0) fetch_pages(it + 1);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) at[b] = place_of(it + 1, b);
+        load_k(at);
+      }
+      softmax_step<NV>(t, m, l, o, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vs[j] = scale_of(vsw[j / 4], j % 4);
+      if (cut) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((gone >> j) & 1u) {
+            vs[j] = 1.f;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) raw[j][i] = 0;
+          }
+      }
+      add_values<DT, NV>(raw, vs, w, o);
+    }
+    finish<DT, DP, false>(a, p, o, 1.f, m, l);
+  } while (span.left > 0);
+}
+
+template <int DT, int DP>
+hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
+  const int units = units_of(a);
+  const dim3 grid(units, a.hkv * a.head_tiles), block(kWaves * kWave);
+  if (a.page.d % 16 == 0 && a.d == DP)
+    hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, true>), grid, block, 0, st, a);
+  else if (a.page.d % 16 == 0)
+    hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, false>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_attention_decode_mx<DT, DP>), grid, block, 0, st, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  return join_pieces<DT>(a, units, st);
+}
+template <int DT>
+hipError_t by_dim(const DecodeAttnArgs& a, hipStream_t st) {
+  if (a.d <= 64) return go<DT, 64>(a, st);
+  if (a.d <= 128) return go<DT, 128>(a, st);
+  return go<DT, 256>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_attention_decode_mx(const spa_heads& q, int n_seqs, int n_q_heads, const spa_kv_cache& c,
+                                      const int32_t* table, int max_pages, const int32_t* lens, float scale, void* out,
+                                      float* lse, float* part_o, float* part_ml, int32_t* part_of, hipStream_t st) {
+  const DecodeAttnArgs a = decode_args(q, n_seqs, n_q_heads, c, table, max_pages, lens, scale, out, lse, part_o, part_ml, part_of);
+  return c.dtype == SPA_F16 ? by_dim<SPA_F16>(a, st) : by_dim<SPA_BF16>(a, st);
+}
+
+}  // namespace spa

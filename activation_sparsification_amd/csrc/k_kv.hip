@@ -1,4 +1,4 @@
-// The paged key-value cache: writing tokens' vectors (quantised on the way for the 8-bit formats) and reading
+// The paged key-value cache: writing tokens' vectors (quantised on the way for the 8-bit and 4-bit formats) and reading
 // the first positions of sequences back as dense rows.
 //
 // Both move every byte once: a vector of head_dim elements is held by a group of LG lanes, 8 elements each, so
@@ -15,12 +15,14 @@ namespace spa {
 namespace {
 
 constexpr int kThreads = 256;
+// 4-byte words of 8 elements as stored.
+template <int FMT> constexpr int kWords = FMT == SPA_KV_NATIVE ? 4 : FMT == SPA_KV_MXFP4 ? 1 : 2;
 
 struct KvArgs {
   const void* src[2];        // write: keys, values
   int64_t row_stride[2], head_stride[2];
   void* pages[2];
-  float* scale[2];
+  void* scale[2];
   void* out[2];              // read: [total][heads][d]
   const int32_t* slots;      // write: [t]
   const int32_t* table;      // read
@@ -67,6 +69,27 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[8], float& scale) {
   return make_uint2(w[0], w[1]);
 }
 
+// Codes of 8 of 32 elements that four lanes hold, and the exponent byte of the 32: from the largest magnitude's own exponent
+// field E and significand, 2^(E - 129), or twice that where the significand is above 1.75 (the magnitude above 7 * 2^(E - 129)).
+// The conversion divides by the scale and rounds once, to nearest even, 6 at the most.
+template <int DT>
+__device__ __forceinline__ uint32_t quantise_mx(const float (&x)[8], uint32_t& scale) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+  a = group_max<4>(a);
+  const bool finite = a < 0x7F800000u, live = finite && __uint_as_float(a) >= 0x1p-100f;
+  constexpr uint32_t kTop = 127 + (DT == SPA_F16 ? 13 : 125);
+  scale = live ? min((a >> 23) - 2 + ((a & 0x7FFFFFu) > 0x600000u), kTop) : finite ? 0u : 255u;
+  const float unit = __uint_as_float(scale << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], unit, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], unit, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], unit, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], unit, 3);
+  return live ? w : 0u;
+}
+
 template <int DT, int FMT, int LG>
 __global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
   constexpr int ROWS = kThreads / LG;
@@ -87,20 +110,37 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
   const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
   const bool ok = slot >= 0 && pg < a.n_pages;                  // the whole group agrees
   const bool live = ok && lane * 8 < a.d;
-  const size_t cell = ((size_t)pg * a.heads + head) * page_size + (slot - pg * page_size);
+  const size_t block = (size_t)pg * a.heads + head;
+  const int off = slot - pg * page_size;
+  const size_t cell = block * page_size + off;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if constexpr (FMT == SPA_KV_NATIVE) {
       if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pages[s]) + cell * a.d + lane * 8) = raw[s];
+    } else if constexpr (FMT == SPA_KV_MXFP4) {
+      float x[8];
+      uint32_t scale;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = elem16<DT>(raw[s], e);
+      const uint32_t codes = quantise_mx<DT>(x, scale);
+      if (live) static_cast<uint32_t*>(a.pages[s])[cell * (a.d / 8) + lane] = codes;
+      if (live && lane % 4 == 0) static_cast<uint8_t*>(a.scale[s])[(block * ((a.d + 31) / 32) + lane / 4) * page_size + off] = (uint8_t)scale;
     } else {
       float x[8], scale;
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = elem16<DT>(raw[s], e);
       const uint2 codes = quantise<FMT, LG>(x, scale);
       if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.pages[s]) + cell * a.d + lane * 8) = codes;
-      if (live && lane == 0) a.scale[s][cell] = scale;
+      if (live && lane == 0) static_cast<float*>(a.scale[s])[cell] = scale;
     }
   }
+}
+
+// Two e2m1 codes (byte SEL of w) times a power of two, rounded once.
+template <int DT, int SEL>
+__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale) {
+  if constexpr (DT == SPA_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
 }
 
 // A wave takes kReadRows consecutive rows of one head.  Lane i finds row i's sequence, page and scales, all rows at
@@ -125,35 +165,47 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
   const int page_size = a.page.d;
   bool ok = row < a.t && seq < a.n_seqs;
   const bool mine = ok;
-  int cell = 0;
+  int cell = 0, off = 0;
   if (ok) {
     const int pos = row - a.cu[seq];
     const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
     const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
     ok = pg >= 0 && pg < a.n_pages;
-    if (ok) cell = (pg * a.heads + head) * page_size + (pos - col * page_size);
+    if (ok) {
+      off = pos - col * page_size;
+      cell = (pg * a.heads + head) * page_size + off;
+    }
   }
   float sc[2] = {0.f, 0.f};
-  if constexpr (FMT != SPA_KV_NATIVE) {
+  if constexpr (FMT == SPA_KV_FP8 || FMT == SPA_KV_INT8) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (ok) sc[s] = a.scale[s][cell];
+      if (ok) sc[s] = static_cast<const float*>(a.scale[s])[cell];
   }
   const uint32_t there = (uint32_t)__ballot(ok), write = (uint32_t)__ballot(mine);
-  constexpr int W = FMT == SPA_KV_NATIVE ? 4 : 2;
-  uint32_t raw[STEPS][2][W];
+  constexpr int W = kWords<FMT>;
+  uint32_t raw[STEPS][2][W], mx[STEPS][2];      // codes; exponent bytes
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int r = i * PER + wl / LG;
     const size_t c = (uint32_t)__shfl(cell, r & (kReadRows - 1), kWave);
+    [[maybe_unused]] size_t first_scale = 0;
+    if constexpr (FMT == SPA_KV_MXFP4) {
+      const int o = __shfl(off, r & (kReadRows - 1), kWave);
+      first_scale = (c - o) * ((a.d + 31) / 32) + (size_t)(lane / 4) * page_size + o;
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int w = 0; w < W; ++w) raw[i][s][w] = 0;
+      mx[i][s] = 0;
       if (r < kReadRows && (there >> r) & 1u && lane * 8 < a.d) {
         if constexpr (FMT == SPA_KV_NATIVE) {
           const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.pages[s]) + c * a.d + lane * 8);
           raw[i][s][0] = v.x; raw[i][s][1] = v.y; raw[i][s][2] = v.z; raw[i][s][3] = v.w;
+        } else if constexpr (FMT == SPA_KV_MXFP4) {
+          raw[i][s][0] = static_cast<const uint32_t*>(a.pages[s])[c * (a.d / 8) + lane];
+          mx[i][s] = static_cast<const uint8_t*>(a.scale[s])[first_scale];
         } else {
           const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.pages[s]) + c * a.d + lane * 8);
           raw[i][s][0] = v.x; raw[i][s][1] = v.y;
@@ -169,6 +221,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
       uint4 v;
       if constexpr (FMT == SPA_KV_NATIVE) {
         v = make_uint4(raw[i][s][0], raw[i][s][1], raw[i][s][2], raw[i][s][3]);
+      } else if constexpr (FMT == SPA_KV_MXFP4) {
+        const float k = __uint_as_float(mx[i][s] << 23);
+        const uint32_t w = raw[i][s][0];
+        v = make_uint4(mx_pair<DT, 0>(w, k), mx_pair<DT, 1>(w, k), mx_pair<DT, 2>(w, k), mx_pair<DT, 3>(w, k));
       } else {
         const float k = __shfl(sc[s], r & (kReadRows - 1), kWave);
         float x[8];
@@ -202,6 +258,7 @@ template <int DT>
 hipError_t by_format(int fmt, bool write, const KvArgs& a, hipStream_t st) {
   if (fmt == SPA_KV_NATIVE) return by_width<DT, SPA_KV_NATIVE>(write, a, st);
   if (fmt == SPA_KV_FP8) return by_width<DT, SPA_KV_FP8>(write, a, st);
+  if (fmt == SPA_KV_MXFP4) return by_width<DT, SPA_KV_MXFP4>(write, a, st);
   return by_width<DT, SPA_KV_INT8>(write, a, st);
 }
 hipError_t dispatch(const spa_kv_cache& c, bool write, KvArgs& a, hipStream_t st) {

@@ -35,11 +35,10 @@ inline bool valid_strides(const spa_heads* h) {
 inline bool dtype16(int dt) { return dt == SPA_F16 || dt == SPA_BF16; }
 inline bool valid_head_dim(int32_t d) { return d >= 1 && d <= kMaxDim; }
 inline bool built_head_dim(int32_t d) { return d % 8 == 0 && d <= kMaxHeadDim; }
-inline int kv_bytes(const spa_kv_cache* c) { return c->format == SPA_KV_NATIVE ? 2 : 1; }
 
 inline spa_status check_cache(const spa_kv_cache* c) {
   if (!c || !valid_dtype(c->dtype)) return SPA_ERR_INVALID;
-  if (c->format < SPA_KV_NATIVE || c->format > SPA_KV_INT8) return SPA_ERR_INVALID;
+  if (c->format < SPA_KV_NATIVE || c->format > SPA_KV_MXFP4) return SPA_ERR_INVALID;
   if (c->n_pages < 1 || c->page_size < 1 || c->n_heads < 1 || c->n_heads > kMaxHeads) return SPA_ERR_INVALID;
   if (!valid_head_dim(c->head_dim)) return SPA_ERR_INVALID;
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return SPA_ERR_INVALID;

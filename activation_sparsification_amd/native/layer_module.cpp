@@ -19,6 +19,7 @@
 #include <initializer_list>
 #include <optional>
 #include <string>
+#include <utility>
 
 #include "spa.h"
 
@@ -240,21 +241,25 @@ Pages pages_of(PyObject* const (&p)[4]) {
   held(k, k.numel(), "KvCache.k");
   given(v, {n, h, s, d}, type, k.device(), "KvCache.v");
   spa_kv_cache c{};
-  c.format = type == at::kFloat8_e4m3fn ? SPA_KV_FP8 : type == at::kChar ? SPA_KV_INT8 : SPA_KV_NATIVE;
+  c.format = type == at::kFloat8_e4m3fn ? SPA_KV_FP8 : type == at::kChar ? SPA_KV_INT8
+             : type == at::kByte ? SPA_KV_MXFP4 : SPA_KV_NATIVE;
+  const bool mx = c.format == SPA_KV_MXFP4;      // two elements to a byte
   const bool scales[2] = {p[2] && p[2] != Py_None, p[3] && p[3] != Py_None};
   if (c.format != SPA_KV_NATIVE) {
-    need(scales[0] && scales[1], "KvCache: 8-bit pages need k_scale and v_scale");
+    need(scales[0] && scales[1], "KvCache: 8-bit and 4-bit pages need k_scale and v_scale");
     const at::Tensor &ks = tensor(p[2], "KvCache.k_scale"), &vs = tensor(p[3], "KvCache.v_scale");
-    given(ks, {n, h, s}, at::kFloat, k.device(), "KvCache.k_scale");
-    given(vs, {n, h, s}, at::kFloat, k.device(), "KvCache.v_scale");
-    c.k_scale = static_cast<float*>(ks.data_ptr());
-    c.v_scale = static_cast<float*>(vs.data_ptr());
+    for (const auto& [x, name] : {std::pair(&ks, "KvCache.k_scale"), std::pair(&vs, "KvCache.v_scale")}) {
+      if (mx) given(*x, {n, h, (d + 15) / 16, s}, at::kByte, k.device(), name);      // d bytes: 2 d elements, 32 to a scale
+      else given(*x, {n, h, s}, at::kFloat, k.device(), name);
+    }
+    c.k_scale = ks.data_ptr();
+    c.v_scale = vs.data_ptr();
   } else {
-    need(dtype_code(type) >= 0, "KvCache: pages are float16, bfloat16, float8_e4m3fn or int8");
-    need(!scales[0] && !scales[1], "KvCache: scales belong to 8-bit pages");
+    need(dtype_code(type) >= 0, "KvCache: pages are float16, bfloat16, float8_e4m3fn, int8 or uint8 (two 4-bit codes)");
+    need(!scales[0] && !scales[1], "KvCache: scales belong to 8-bit and 4-bit pages");
   }
   c.n_pages = size32(n, "n_pages"); c.n_heads = size32(h, "n_heads");
-  c.page_size = size32(s, "page_size"); c.head_dim = size32(d, "head_dim");
+  c.page_size = size32(s, "page_size"); c.head_dim = size32(mx ? 2 * d : d, "head_dim");
   c.k = k.data_ptr();
   c.v = v.data_ptr();
   return Pages{c, type, k.device()};
@@ -293,8 +298,8 @@ void cache_dealloc(KvCache* self) {
 PyMemberDef cache_members[] = {
     {"k", T_OBJECT, offsetof(KvCache, part), READONLY, "keys, or their codes"},
     {"v", T_OBJECT, offsetof(KvCache, part) + sizeof(PyObject*), READONLY, "values, or their codes"},
-    {"k_scale", T_OBJECT, offsetof(KvCache, part) + 2 * sizeof(PyObject*), READONLY, "float32 scales of 8-bit keys, or None"},
-    {"v_scale", T_OBJECT, offsetof(KvCache, part) + 3 * sizeof(PyObject*), READONLY, "float32 scales of 8-bit values, or None"},
+    {"k_scale", T_OBJECT, offsetof(KvCache, part) + 2 * sizeof(PyObject*), READONLY, "scales of 8-bit or 4-bit keys, or None"},
+    {"v_scale", T_OBJECT, offsetof(KvCache, part) + 3 * sizeof(PyObject*), READONLY, "scales of 8-bit or 4-bit values, or None"},
     {nullptr, 0, 0, 0, nullptr}};
 
 template <int32_t spa_kv_cache::*SIZE>
@@ -365,8 +370,8 @@ PyDoc_STRVAR(kv_read_doc,
              "kv_read($module, /, cache, page_table, cu_seqlens, total, k_out=None, v_out=None, dtype=None)\n--\n\n"
              "The first cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as packed rows (k, v), each\n"
              "[total, n_heads, head_dim].\n\n"
-             "page_table [n_seqs, max_pages] and cu_seqlens [n_seqs + 1] are int32.  dtype is needed for 8-bit pages\n"
-             "when no outputs are given.  Positions on absent pages read as zeros.");
+             "page_table [n_seqs, max_pages] and cu_seqlens [n_seqs + 1] are int32.  dtype is needed for 8-bit and 4-bit\n"
+             "pages when no outputs are given.  Positions on absent pages read as zeros.");
 PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     static const char* const names[] = {"cache", "page_table", "cu_seqlens", "total", "k_out", "v_out", "dtype"};
@@ -389,7 +394,7 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObje
     } else if (a.v[4] || a.v[5]) {
       type = tensor(a.v[4] ? a.v[4] : a.v[5], "k_out").scalar_type();
     } else {
-      need(kv.c.format == SPA_KV_NATIVE, "kv_read: 8-bit pages need dtype or outputs");
+      need(kv.c.format == SPA_KV_NATIVE, "kv_read: 8-bit and 4-bit pages need dtype or outputs");
     }
     const spa_kv_cache c = cache_for(kv, type);
     const at::Tensor k = output(a.v[4], {total, c.n_heads, c.head_dim}, type, kv.dev, "k_out");
@@ -588,8 +593,10 @@ PyMODINIT_FUNC PyInit__layer_native() {
       "KvCache(k, v, k_scale=None, v_scale=None)\n--\n\n"
       "A paged cache of one layer: k and v are [n_pages, n_heads, page_size, head_dim].\n\n"
       "float16 or bfloat16 pages hold the vectors as they are; float8_e4m3fn and int8 pages hold codes, with float32\n"
-      "k_scale and v_scale [n_pages, n_heads, page_size].  The cache keeps its tensors; each call works on\n"
-      "the memory and sizes that they have then.";
+      "k_scale and v_scale [n_pages, n_heads, page_size]; uint8 pages [n_pages, n_heads, page_size, head_dim / 2] hold two\n"
+      "e2m1 codes to a byte, with uint8 scales [n_pages, n_heads, ceil(head_dim / 32), page_size], exponent + 127 of a power\n"
+      "of two for every 32 elements.  The cache keeps its tensors; each call works on the memory and sizes that they have\n"
+      "then.";
   g_cache_type.tp_new = PyType_GenericNew;
   g_cache_type.tp_init = reinterpret_cast<initproc>(cache_init);
   g_cache_type.tp_dealloc = reinterpret_cast<destructor>(cache_dealloc);

@@ -404,9 +404,11 @@ size_t spa_workspace_bytes(int32_t entry, int32_t t, int32_t k, int32_t n_out, i
  * One value is rounded to the vectors' 16-bit type on the way: a softmax
  * weight (with an 8-bit cache, times its value's scale) where it meets the
  * values in the matrix product.  The sum that divides is of the unrounded
- * weights.
+ * weights.  Over a 4-bit cache the weight of a float16 call keeps 16 bits
+ * instead (two bfloat16 numbers), and a query element is taken to 2^-24 of
+ * the largest of its 32 (elements 0..31, 32..63, ... of its head).
  * ------------------------------------------------------------------------ */
-enum { SPA_KV_NATIVE = 0, SPA_KV_FP8 = 1, SPA_KV_INT8 = 2 };
+enum { SPA_KV_NATIVE = 0, SPA_KV_FP8 = 1, SPA_KV_INT8 = 2, SPA_KV_MXFP4 = 3 };
 enum { SPA_NORM_NONE = 0, SPA_NORM_RMS = 1, SPA_NORM_LAYER = 2 };
 
 /* Vectors of several heads: head h of row i is the head_dim consecutive
@@ -434,6 +436,21 @@ typedef struct spa_heads {
  *                 is stored as zeros with scale 0, one that holds a NaN or an
  *                 infinity as zeros with scale NaN: all of it reads back as
  *                 NaN.  The value of a code is code * scale.
+ *  SPA_KV_MXFP4   e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign),
+ *                 two to a byte: k and v are [n_pages][n_heads][page_size]
+ *                 [head_dim / 2] bytes, element 2i in the low four bits of
+ *                 byte i.  k_scale and v_scale hold a byte per page, head, 32
+ *                 elements and position, [n_pages][n_heads]
+ *                 [ceil(head_dim / 32)][page_size]: the exponent e of the
+ *                 elements' scale 2^e, plus 127.  With a = max |x| over the
+ *                 32 (the last may be fewer), e is the least with a <= 7 *
+ *                 2^e, and no more than 13 (SPA_F16) or 125 (SPA_BF16), so
+ *                 that 6 * 2^e is a number of the type; code = x / 2^e
+ *                 rounded to the nearest (ties to the even code), 6 at the
+ *                 most, with the sign of x.  a < 2^-100 gives zero codes and
+ *                 byte 0, a NaN or an infinity zero codes and byte 255: the
+ *                 elements read back as NaN.  The value of a code is code *
+ *                 2^e.
  * dtype (SPA_F16 or SPA_BF16) is the type of the vectors that go in and out.
  * head_dim must be a multiple of 8 up to 256 and n_pages * page_size *
  * n_heads below 2^31, else SPA_ERR_UNSUPPORTED; any page_size >= 1. */
@@ -446,14 +463,14 @@ typedef struct spa_kv_cache {
   int32_t head_dim;
   void* k;                  /* [device] */
   void* v;                  /* [device] */
-  float* k_scale;           /* [device], 8-bit formats */
-  float* v_scale;           /* [device], 8-bit formats */
+  void* k_scale;            /* [device], float32 or bytes; NULL for SPA_KV_NATIVE */
+  void* v_scale;            /* [device] */
 } spa_kv_cache;
 
 /*
  * spa_kv_write -- store t tokens' keys and values (rows of n_heads vectors,
- * cache->dtype) at the given slots, quantised on the way for the 8-bit
- * formats.  slots: [device] [t] int32; a slot outside [0, n_pages *
+ * cache->dtype) at the given slots, quantised on the way for the 8-bit and
+ * 4-bit formats.  slots: [device] [t] int32; a slot outside [0, n_pages *
  * page_size) -- -1 for a padding token, say -- is skipped.  Two tokens of a
  * call must not name the same slot.  t >= 0 (0 is a no-op).
  */
