@@ -65,6 +65,10 @@ class _Norm(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -135,6 +139,9 @@ def lib() -> ctypes.CDLL:
                                         vp, sz, vp]
         L.gated_residual_norm.restype = ctypes.c_int
         L.gated_residual_norm.argtypes = [vp, i32, i32, i32, vp, i32, norm, vp, i32, f32, norm, f32, vp, vp, vp]
+        L.qk_norm_rope.restype = ctypes.c_int
+        L.qk_norm_rope.argtypes = [heads, heads, heads, i32, i32, i32, i32, i32, vp, ctypes.POINTER(_Rope), norm, norm, f32,
+                                   heads, heads, vp, cache, vp]
         _lib = L
     return _lib
 
@@ -145,7 +152,7 @@ EXPORTS = ("prepare_weight", "prune_nm", "sparse_linear_decode", "sparse_linear_
            "sparse_ffn_relu2_prefill", "spa_ffn_workspace_bytes", "prepare_weight_fp8",
            "sparse_linear_prefill_fp8", "spa_prefill_layout", "sparse_linear_decode_static",
            "spa_kv_write", "spa_kv_read", "attention_decode", "spa_attention_decode_workspace_bytes",
-           "attention_prefill", "spa_attention_prefill_workspace_bytes", "gated_residual_norm")
+           "attention_prefill", "spa_attention_prefill_workspace_bytes", "gated_residual_norm", "qk_norm_rope")
 
 
 @dataclasses.dataclass(frozen=True)

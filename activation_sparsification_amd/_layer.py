@@ -1,4 +1,4 @@
-"""The cache, attention and norm calls: thin native binding (``_layer_native``) of the C entries in ``libspa.so``.
+"""The cache, attention, norm and rotation calls: thin native binding (``_layer_native``) of the C entries in ``libspa.so``.
 
 Tensors of several heads are ``[rows, heads, head_dim]`` with the last axis dense; the row and head strides are
 free (a slice of a packed projection is passed as it is).  Forward only: a tensor that requires a gradient is refused
@@ -25,6 +25,7 @@ kv_read = _native.kv_read
 attention_decode = _native.attention_decode
 attention_prefill = _native.attention_prefill
 gated_residual_norm = _native.gated_residual_norm
+qk_norm_rope = _native.qk_norm_rope
 
 PAGE_TYPES = {"native": None, "fp8": torch.float8_e4m3fn, "int8": torch.int8, "mxfp4": torch.uint8}
 

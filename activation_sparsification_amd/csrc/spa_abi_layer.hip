@@ -82,6 +82,45 @@ spa_status attention_prefill(const spa_heads* q, const spa_heads* k, const spa_h
                                                   stream_of(stream)));
 }
 
+spa_status qk_norm_rope(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t t,
+                        int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* positions,
+                        const spa_rope* rope, const spa_norm* q_norm, const spa_norm* k_norm, float eps,
+                        const spa_heads* q_out, const spa_heads* k_out, const int32_t* slots, const spa_kv_cache* cache,
+                        void* stream) {
+  if (spa_status s = check_qk_norm_rope(q, k, v, dtype, t, n_q_heads, n_kv_heads, head_dim, positions, rope, q_norm, k_norm,
+                                        eps, q_out, k_out, slots, cache))
+    return s;
+  if (t == 0) return SPA_OK;
+  const spa_norm none{SPA_NORM_NONE, nullptr, nullptr};
+  spa::RopeArgs a{};
+  const spa_heads* src[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    if (!src[i]) continue;
+    a.src[i] = static_cast<const uint16_t*>(src[i]->data);
+    a.row[i] = src[i]->row_stride;
+    a.head[i] = src[i]->head_stride;
+  }
+  const spa_heads* dst[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i) {
+    if (!dst[i]) continue;
+    a.dst[i] = static_cast<uint16_t*>(const_cast<void*>(dst[i]->data));
+    a.drow[i] = dst[i]->row_stride;
+    a.dhead[i] = dst[i]->head_stride;
+  }
+  a.pos = positions;
+  a.norm[0] = q_norm ? *q_norm : none;
+  a.norm[1] = k_norm ? *k_norm : none;
+  a.eps = eps;
+  a.t = t; a.hq = n_q_heads; a.hkv = n_kv_heads; a.d = head_dim;
+  if (rope) {
+    a.freq = rope->inv_freq;
+    a.rot = rope->rotary_dim;
+    a.neighbours = rope->interleaved != 0;
+  }
+  a.slots = slots;
+  return hip_status(spa::launch_qk_norm_rope(dtype, cache, a, stream_of(stream)));
+}
+
 spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t c, const void* residual,
                                int32_t stream_dtype, const spa_norm* post, const void* gate, int32_t gate_rows,
                                float scale, const spa_norm* pre, float eps, void* h, void* y, void* stream) {

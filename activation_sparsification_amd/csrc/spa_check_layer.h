@@ -181,10 +181,51 @@ inline PrefillAttnPlan prefill_attn_plan(int tq, int tk, int n_seqs, int n_q_hea
   return p;
 }
 
-// ---- norms ----
+// ---- norm and rotation of queries and keys ----
+// Vectors that are written: no two of them overlap.
+inline bool apart(const spa_heads* h, int64_t rows, int64_t heads, int64_t d) {
+  if (rows > 1 && h->row_stride < d) return false;
+  if (heads > 1 && h->head_stride < d) return false;
+  return rows <= 1 || heads <= 1 || h->row_stride >= (heads - 1) * h->head_stride + d ||
+         h->head_stride >= (rows - 1) * h->row_stride + d;
+}
 inline bool valid_norm(const spa_norm* n) {
   return !n || (n->kind >= SPA_NORM_NONE && n->kind <= SPA_NORM_LAYER);
 }
+inline spa_status check_qk_norm_rope(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t t,
+                                     int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* positions,
+                                     const spa_rope* rope, const spa_norm* q_norm, const spa_norm* k_norm, float eps,
+                                     const spa_heads* q_out, const spa_heads* k_out, const int32_t* slots,
+                                     const spa_kv_cache* c) {
+  if (!valid_dtype(dtype) || t < 0 || t > kMaxRows || n_q_heads < 1 || n_q_heads > kMaxHeads || n_kv_heads < 1 ||
+      n_kv_heads > kMaxHeads || !valid_head_dim(head_dim) || !(eps >= 0.f && eps <= 1e30f))
+    return SPA_ERR_INVALID;
+  for (const spa_norm* n : {q_norm, k_norm})
+    if (!valid_norm(n) || (n && (!aligned16(n->weight) || !aligned16(n->bias)))) return SPA_ERR_INVALID;
+  const int32_t rot = rope ? rope->rotary_dim : 0;
+  if (rot < 0 || rot > head_dim || rot % 2 || (rot && !rope->inv_freq)) return SPA_ERR_INVALID;
+  if (!c && (v || slots)) return SPA_ERR_INVALID;
+  spa_status s = SPA_OK;
+  if (c) {
+    s = check_cache(c);
+    if (s == SPA_ERR_INVALID) return s;
+    if (c->dtype != dtype || c->n_heads != n_kv_heads || c->head_dim != head_dim) return SPA_ERR_INVALID;
+  }
+  if (dtype == SPA_F32 || !built_head_dim(head_dim) || rot % 8) s = SPA_ERR_UNSUPPORTED;
+  if (t == 0) return s;
+  for (const spa_heads* h : {q, k, q_out})
+    if (!h || !valid_heads(h) || !valid_strides(h)) return SPA_ERR_INVALID;
+  if (rot && !positions) return SPA_ERR_INVALID;
+  if (c ? !v || !valid_heads(v) || !valid_strides(v) || !slots : !k_out) return SPA_ERR_INVALID;
+  if (k_out && (!valid_heads(k_out) || !valid_strides(k_out) || !apart(k_out, t, n_kv_heads, head_dim))) return SPA_ERR_INVALID;
+  if (!apart(q_out, t, n_q_heads, head_dim)) return SPA_ERR_INVALID;
+  if (s != SPA_OK) return s;
+  for (const spa_heads* h : {q, k, q_out, c ? v : q, k_out ? k_out : q})
+    if (!built_heads(h)) return SPA_ERR_UNSUPPORTED;
+  return (int64_t)t * (n_q_heads + 2 * n_kv_heads) <= kMaxVectors ? SPA_OK : SPA_ERR_UNSUPPORTED;
+}
+
+// ---- norms ----
 inline spa_status check_norm(const void* x, int32_t dtype, int32_t t, int32_t c, const void* residual,
                              int32_t stream_dtype, const spa_norm* post, const void* gate, int32_t gate_rows,
                              float scale, const spa_norm* pre, float eps, const void* h, const void* y) {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "spa.h"
+#include "spa_div.h"
 
 namespace spa {
 
@@ -38,6 +39,24 @@ struct NormArgs {
   float scale, eps;
   spa_norm post, pre;
 };
+struct RopeArgs {
+  const uint16_t* src[3];    // queries, keys, values (with a cache)
+  int64_t row[3], head[3];   // strides
+  uint16_t* dst[2];          // queries, keys (or NULL)
+  int64_t drow[2], dhead[2];
+  const int32_t* pos;        // [t]; NULL without rotation
+  const float* freq;         // [rot / 2]
+  spa_norm norm[2];          // of queries and keys
+  float eps;
+  int t, hq, hkv, d, rot, neighbours;
+  const int32_t* slots;      // [t], with a cache
+  void* pages[2];            // launch_qk_norm_rope fills in the cache's
+  void* scale[2];
+  int n_pages;
+  FastDiv page;
+};
+hipError_t launch_qk_norm_rope(int dtype, const spa_kv_cache* cache, RopeArgs a, hipStream_t st);
+
 hipError_t launch_norm(int dtype, int stream_dtype, const NormArgs& a, hipStream_t st);
 
 }  // namespace spa

@@ -567,6 +567,85 @@ PyObject* py_gated_residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n_
   });
 }
 
+// Vectors of several heads that a call writes, of this shape, type and device.
+spa_heads heads_out(const at::Tensor& x, c10::IntArrayRef shape, at::ScalarType type, at::Device dev, const char* name) {
+  const spa_heads h = heads(x, name);
+  if (x.sizes() != shape || x.scalar_type() != type || x.device() != dev)
+    refuse(std::string(name) + ": differs from its input in shape, type or device");
+  return h;
+}
+
+PyDoc_STRVAR(qk_norm_rope_doc,
+             "qk_norm_rope($module, /, q, k, positions=None, inv_freq=None, *, norm='rms', q_weight=None, k_weight=None,"
+             " q_bias=None, k_bias=None, eps=1e-05, interleaved=False, q_out=None, k_out=None, v=None, slots=None,"
+             " cache=None)\n--\n\n"
+             "The norm of each head of q [t, n_q_heads, head_dim] and k [t, n_kv_heads, head_dim] ('none', 'rms' or 'layer',\n"
+             "weights and biases [head_dim]), and the rotation of its first 2 * len(inv_freq) elements by the angles\n"
+             "positions[row] * inv_freq (int32 [t], float32): pairs (i, i + len(inv_freq)), or neighbours with interleaved.\n\n"
+             "q_out may be q and k_out may be k.  With a cache, the new keys and v [t, n_kv_heads, head_dim] are stored at\n"
+             "slots [t] int32 as kv_write would, and the keys are returned only where k_out is given.  Returns (q, k or None).");
+PyObject* py_qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"q", "k", "positions", "inv_freq", "norm", "q_weight", "k_weight", "q_bias", "k_bias",
+                                        "eps", "interleaved", "q_out", "k_out", "v", "slots", "cache"};
+    Args<16> a("qk_norm_rope", names, 2, 4, args, n_args, kw);
+    const at::Tensor &q = tensor(a.v[0], "q"), &k = tensor(a.v[1], "k");
+    const spa_heads qh = heads(q, "q"), kh = heads(k, "k");
+    const at::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const OnDevice on(dev);
+    need(dtype_code(type) >= 0 && k.scalar_type() == type, "qk_norm_rope: q and k are float16 or bfloat16, both the same");
+    need(k.device() == dev, "qk_norm_rope: tensors on several devices");
+    need(k.size(0) == q.size(0) && k.size(2) == q.size(2), "qk_norm_rope: q and k differ in rows or head_dim");
+    const int64_t t = q.size(0), d = q.size(2);
+    need(!a.v[2] == !a.v[3], "qk_norm_rope: positions and inv_freq belong together");
+    spa_rope rope{nullptr, 0, a.v[10] ? truth(a.v[10]) : 0};
+    const int32_t* pos = nullptr;
+    if (a.v[2]) {
+      const at::Tensor &p = tensor(a.v[2], "positions"), &f = tensor(a.v[3], "inv_freq");
+      given(p, {t}, at::kInt, dev, "positions");
+      need(f.dim() == 1, "inv_freq: expected [rotary_dim / 2]");
+      given(f, {f.size(0)}, at::kFloat, dev, "inv_freq");
+      need(2 * f.size(0) <= d, "inv_freq: more pairs than the head has");
+      pos = static_cast<const int32_t*>(p.data_ptr());
+      rope.inv_freq = static_cast<const float*>(f.data_ptr());
+      rope.rotary_dim = (int32_t)(2 * f.size(0));
+    }
+    const spa_norm qn = norm_of(a.v[4], SPA_NORM_RMS, a.v[5], a.v[7], d, type, dev, "q_norm");
+    const spa_norm kn = norm_of(a.v[4], SPA_NORM_RMS, a.v[6], a.v[8], d, type, dev, "k_norm");
+    need(!a.v[13] == !a.v[15] && !a.v[14] == !a.v[15], "qk_norm_rope: v, slots and cache belong together");
+    spa_kv_cache c{};
+    spa_heads vh{};
+    const int32_t* slots = nullptr;
+    if (a.v[15]) {
+      const Pages kv = cache(a.v[15]);
+      const at::Tensor &v = tensor(a.v[13], "v"), &s = tensor(a.v[14], "slots");
+      need(kv.dev == dev, "qk_norm_rope: tensors on several devices");
+      need(k.size(1) == kv.c.n_heads && d == kv.c.head_dim, "qk_norm_rope: the cache has other heads");
+      vh = heads_out(v, k.sizes(), type, dev, "v");
+      given(s, {t}, at::kInt, dev, "slots");
+      slots = static_cast<const int32_t*>(s.data_ptr());
+      c = cache_for(kv, type);
+    }
+    const at::Tensor qo = a.v[11] ? tensor(a.v[11], "q_out") : fresh(q.sizes(), type, dev);
+    const spa_heads qoh = heads_out(qo, q.sizes(), type, dev, "q_out");
+    at::Tensor ko;
+    spa_heads koh{};
+    if (a.v[12] || !a.v[15]) {
+      ko = a.v[12] ? tensor(a.v[12], "k_out") : fresh(k.sizes(), type, dev);
+      koh = heads_out(ko, k.sizes(), type, dev, "k_out");
+    }
+    check(qk_norm_rope(&qh, &kh, a.v[15] ? &vh : nullptr, dtype_code(type), size32(t, "q"), size32(q.size(1), "q"),
+                       size32(k.size(1), "k"), size32(d, "q"), pos, &rope, &qn, &kn, a.v[9] ? (float)number(a.v[9]) : 1e-5f, &qoh,
+                       ko.defined() ? &koh : nullptr, slots, a.v[15] ? &c : nullptr, stream_of(dev)),
+          "qk_norm_rope");
+    if (a.v[15])
+      for (PyObject* part : reinterpret_cast<const KvCache*>(a.v[15])->part)
+        if (part && part != Py_None) written(THPVariable_Unpack(part));
+    return pair(back(a.v[11], qo), back(a.v[12], ko));
+  });
+}
+
 PyObject* py_set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XSETREF(g_error, type);
@@ -579,6 +658,7 @@ PyMethodDef g_methods[] = {FAST(kv_write, py_kv_write),
                            FAST(attention_decode, py_attention_decode),
                            FAST(attention_prefill, py_attention_prefill),
                            FAST(gated_residual_norm, py_gated_residual_norm),
+                           FAST(qk_norm_rope, py_qk_norm_rope),
                            {"_set_error", py_set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

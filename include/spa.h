@@ -577,6 +577,46 @@ spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t 
                                int32_t stream_dtype, const spa_norm* post, const void* gate, int32_t gate_rows,
                                float scale, const spa_norm* pre, float eps, void* h, void* y, void* stream);
 
+/*
+ * qk_norm_rope -- what stands between a projection and its attention: the
+ * norm of each query and key head and the rotation by position, in one pass,
+ * and with a cache the keys and values on their way into it.
+ *   u = N(x) over a head's head_dim elements (N as above, weight and bias
+ *   [head_dim], shared by the heads);
+ *   for i < rotary_dim / 2, with the pair (a, b) = (i, i + rotary_dim / 2),
+ *   or (2i, 2i + 1) with interleaved != 0, and the angle p = position *
+ *   inv_freq[i]:  y_a = u_a cos p - u_b sin p,  y_b = u_a sin p + u_b cos p;
+ *   the elements from rotary_dim on are y = u.
+ * Float32 between input and output.  The angle is formed in float64 and its
+ * whole turns taken off there, so far positions keep their precision: 2^-21
+ * of a radian at any position times frequency below 2^31.
+ *  q, k      t rows of n_q_heads and n_kv_heads vectors of dtype (SPA_F16 or
+ *            SPA_BF16)
+ *  positions [device] [t] int32, any value (NULL without rotation)
+ *  rope      NULL, or rotary_dim 0, for no rotation
+ *  q_norm, k_norm  NULL: SPA_NORM_NONE
+ *  q_out, k_out  where the vectors go (written through `data`; no two vectors
+ *            of one may overlap); may be q and k themselves, and otherwise
+ *            must not overlap any input.  k_out may be NULL with a cache
+ *  v, slots, cache  NULL, or: k's result and v's vectors are stored at the
+ *            slots [t], just as spa_kv_write(k_out, v, ...) would store them
+ *            (cache->dtype is dtype; its heads and head_dim are k's)
+ * t >= 0; rotary_dim even and at most head_dim, else SPA_ERR_INVALID; the
+ * kernels are built for a rotary_dim that is a multiple of 8 and the
+ * head_dim, strides and alignment of spa_heads and spa_kv_cache, else
+ * SPA_ERR_UNSUPPORTED.
+ */
+typedef struct spa_rope {
+  const float* inv_freq;    /* [device] [rotary_dim / 2] */
+  int32_t rotary_dim;
+  int32_t interleaved;
+} spa_rope;
+spa_status qk_norm_rope(const spa_heads* q, const spa_heads* k, const spa_heads* v, int32_t dtype, int32_t t,
+                        int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t* positions,
+                        const spa_rope* rope, const spa_norm* q_norm, const spa_norm* k_norm, float eps,
+                        const spa_heads* q_out, const spa_heads* k_out, const int32_t* slots, const spa_kv_cache* cache,
+                        void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* spa_status_str(spa_status s);
 
