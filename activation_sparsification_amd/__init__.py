@@ -32,8 +32,8 @@ from ._binding import (  # noqa: F401
 )
 # The cache, attention and norm calls are bound natively (_layer): loaded at first use, so that this package can be
 # imported to build them.
-_LAYER = ("KvCache", "attention_decode", "attention_prefill", "gated_residual_norm", "kv_read", "kv_write", "new_kv_cache",
-          "qk_norm_rope")
+_LAYER = ("KvCache", "attention_decode", "attention_prefill", "gated_residual_norm", "kv_plan", "kv_read",
+          "kv_write", "new_kv_cache", "new_page_pool", "qk_norm_rope")
 
 
 def __getattr__(name):

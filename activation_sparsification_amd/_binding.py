@@ -69,6 +69,11 @@ class _Rope(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class _PagePool(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("count", ctypes.c_void_p), ("count_out", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -139,6 +144,8 @@ def lib() -> ctypes.CDLL:
                                         vp, sz, vp]
         L.gated_residual_norm.restype = ctypes.c_int
         L.gated_residual_norm.argtypes = [vp, i32, i32, i32, vp, i32, norm, vp, i32, f32, norm, f32, vp, vp, vp]
+        L.spa_kv_plan.restype = ctypes.c_int
+        L.spa_kv_plan.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.POINTER(_PagePool), i32, vp, vp, vp, vp, vp, vp]
         L.qk_norm_rope.restype = ctypes.c_int
         L.qk_norm_rope.argtypes = [heads, heads, heads, i32, i32, i32, i32, i32, vp, ctypes.POINTER(_Rope), norm, norm, f32,
                                    heads, heads, vp, cache, vp]
@@ -152,7 +159,8 @@ EXPORTS = ("prepare_weight", "prune_nm", "sparse_linear_decode", "sparse_linear_
            "sparse_ffn_relu2_prefill", "spa_ffn_workspace_bytes", "prepare_weight_fp8",
            "sparse_linear_prefill_fp8", "spa_prefill_layout", "sparse_linear_decode_static",
            "spa_kv_write", "spa_kv_read", "attention_decode", "spa_attention_decode_workspace_bytes",
-           "attention_prefill", "spa_attention_prefill_workspace_bytes", "gated_residual_norm", "qk_norm_rope")
+           "attention_prefill", "spa_attention_prefill_workspace_bytes", "gated_residual_norm", "qk_norm_rope",
+           "spa_kv_plan")
 
 
 @dataclasses.dataclass(frozen=True)

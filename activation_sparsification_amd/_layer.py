@@ -22,6 +22,7 @@ _native._set_error(SpaError)
 KvCache = _native.KvCache
 kv_write = _native.kv_write
 kv_read = _native.kv_read
+kv_plan = _native.kv_plan
 attention_decode = _native.attention_decode
 attention_prefill = _native.attention_prefill
 gated_residual_norm = _native.gated_residual_norm
@@ -45,3 +46,9 @@ def new_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, dtyp
     pages = [torch.zeros(shape, dtype=PAGE_TYPES[fmt] or dtype, device=device) for _ in range(2)]
     scales = [None if fmt == "native" else torch.zeros(shape[:3], device=device) for _ in range(2)]
     return KvCache(*pages, *scales)
+
+
+def new_page_pool(n_pages: int, device="cuda"):
+    """Every page of a cache, free: the stack of ``kv_plan`` (page 0 on top) and its count."""
+    pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+    return pages, torch.tensor([n_pages, 0], dtype=torch.int32, device=device)

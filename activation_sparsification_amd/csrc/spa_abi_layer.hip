@@ -33,6 +33,22 @@ spa_status spa_kv_read(const spa_kv_cache* cache, const int32_t* page_table, int
                                         stream_of(stream)));
 }
 
+spa_status spa_kv_plan(const int32_t* lens, const int32_t* fresh, const int32_t* done, int32_t n_seqs, int32_t* page_table,
+                       int32_t max_pages, int32_t page_size, const spa_page_pool* pool, int32_t t, int32_t* slots,
+                       int32_t* positions, int32_t* cu_q, int32_t* cu_k, int32_t* lens_out, void* stream) {
+  if (spa_status s = check_kv_plan(lens, fresh, n_seqs, page_table, max_pages, page_size, pool, t, slots, positions, cu_q, cu_k,
+                                   lens_out))
+    return s;
+  spa::PlanArgs a{};
+  a.lens = lens; a.fresh = fresh; a.done = n_seqs ? done : nullptr;
+  a.table = page_table;
+  a.stack = pool->pages; a.count = pool->count; a.count_out = pool->count_out;
+  a.slots = slots; a.positions = positions; a.cu_q = cu_q; a.cu_k = cu_k; a.lens_out = lens_out;
+  a.n_seqs = n_seqs; a.max_pages = max_pages; a.n_pages = pool->n_pages; a.t = t;
+  a.page = spa::FastDiv((uint32_t)page_size);
+  return hip_status(spa::launch_kv_plan(a, stream_of(stream)));
+}
+
 size_t spa_attention_decode_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (n_seqs < 1 || n_seqs > kMaxSeqs || n_q_heads < 1 || n_q_heads > kMaxHeads || n_kv_heads < 1 ||
       n_q_heads % n_kv_heads || head_dim < 1 || !built_head_dim(head_dim))

@@ -73,6 +73,21 @@ inline spa_status check_kv_read(const spa_kv_cache* c, const int32_t* table, int
   return s;
 }
 
+// ---- page tables and slots ----
+inline spa_status check_kv_plan(const int32_t* lens, const int32_t* fresh, int32_t n_seqs, const int32_t* table,
+                                int32_t max_pages, int32_t page_size, const spa_page_pool* pool, int32_t t, const int32_t* slots,
+                                const int32_t* positions, const int32_t* cu_q, const int32_t* cu_k, const int32_t* lens_out) {
+  if (n_seqs < 0 || n_seqs > kMaxSeqs || max_pages < 0 || page_size < 1 || t < 0 || t > kMaxRows) return SPA_ERR_INVALID;
+  if (!pool || pool->n_pages < 0 || !pool->count || !pool->count_out || (pool->n_pages > 0 && !pool->pages)) return SPA_ERR_INVALID;
+  if (!cu_q || !cu_k || cu_q == cu_k) return SPA_ERR_INVALID;
+  if (n_seqs > 0 && (!lens || !fresh || !lens_out || lens_out == fresh)) return SPA_ERR_INVALID;
+  if (n_seqs > 0 && max_pages > 0 && !table) return SPA_ERR_INVALID;
+  if (t > 0 && (!slots || !positions || slots == positions)) return SPA_ERR_INVALID;
+  // positions of a sequence are numbered in 29 bits, so that a length and a call's new rows add up in 31; slots in 31
+  if ((int64_t)max_pages * page_size > kMaxPositions || (int64_t)pool->n_pages * page_size > INT32_MAX) return SPA_ERR_UNSUPPORTED;
+  return SPA_OK;
+}
+
 inline bool valid_scale(float s) { return s > 0.f && s <= 1e30f; }   // false for NaN
 
 // ---- decode attention ----

@@ -14,6 +14,24 @@ hipError_t launch_kv_write(const spa_heads& k, const spa_heads& v, int t, const 
 hipError_t launch_kv_read(const spa_kv_cache& c, const int32_t* table, int n_seqs, int max_pages, const int32_t* cu,
                           int total, void* k_out, void* v_out, hipStream_t st);
 
+struct PlanArgs {
+  const int32_t* lens;       // [n_seqs]
+  const int32_t* fresh;      // [n_seqs]: new tokens
+  const int32_t* done;       // [n_seqs] or NULL
+  int32_t* table;            // [n_seqs][max_pages]
+  int32_t* stack;            // [n_pages]: the free pages
+  const int32_t* count;      // how many
+  int32_t* count_out;        // [2]: how many are left, and how many there were too few
+  int32_t* slots;            // [t]
+  int32_t* positions;        // [t]
+  int32_t* cu_q;             // [n_seqs + 1]
+  int32_t* cu_k;             // [n_seqs + 1]
+  int32_t* lens_out;         // [n_seqs]
+  int n_seqs, max_pages, n_pages, t;
+  FastDiv page;
+};
+hipError_t launch_kv_plan(PlanArgs a, hipStream_t st);
+
 hipError_t launch_attention_decode(const spa_heads& q, int n_seqs, int n_q_heads, const spa_kv_cache& c,
                                    const int32_t* table, int max_pages, const int32_t* lens, float scale, void* out,
                                    float* lse, float* part_o, float* part_ml, int32_t* part_of, hipStream_t st);

@@ -359,6 +359,69 @@ PyObject* py_kv_write(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   });
 }
 
+PyDoc_STRVAR(kv_plan_doc,
+             "kv_plan($module, /, lens, new, page_table, page_size, free_pages, free_count, t, *, done=None, slots=None,"
+             " positions=None, cu_q=None, cu_k=None, lens_out=None, count_out=None)\n--\n\n"
+             "Page tables, slots and offsets of a step from request lengths, all int32 on the device.\n\n"
+             "lens and new [n_seqs]: cached positions and new tokens of each sequence; done [n_seqs]: sequences that are over\n"
+             "give their pages back first and begin anew.  page_table [n_seqs, max_pages] receives pages from the stack\n"
+             "free_pages [n_pages], of which free_count[0] are free (new_page_pool makes both).  Returns (slots [t],\n"
+             "positions [t], cu_q [n_seqs + 1], cu_k [n_seqs + 1], lens [n_seqs], count [2]): the rows' slots (-1 without a\n"
+             "page and past the last token) and positions, running sums of the new tokens and of the new lengths, the new\n"
+             "lengths, and the pages free now and lacking.  lens_out may be lens and count_out may be free_count.");
+PyObject* py_kv_plan(PyObject*, PyObject* const* args, Py_ssize_t n_args, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    static const char* const names[] = {"lens", "new", "page_table", "page_size", "free_pages", "free_count", "t", "done",
+                                        "slots", "positions", "cu_q", "cu_k", "lens_out", "count_out"};
+    Args<14> a("kv_plan", names, 7, 7, args, n_args, kw);
+    const at::Tensor &lens = tensor(a.v[0], "lens"), &fresh_tokens = tensor(a.v[1], "new"), &table = tensor(a.v[2], "page_table");
+    const at::Tensor &stack = tensor(a.v[4], "free_pages"), &count = tensor(a.v[5], "free_count");
+    const at::Device dev = lens.device();
+    need(lens.is_cuda() && lens.dim() == 1, "lens: expected a device tensor [n_seqs]");
+    const OnDevice on(dev);
+    const int32_t n = size32(lens.size(0), "lens"), page_size = integer(a.v[3], "page_size"), t = integer(a.v[6], "t");
+    need(t >= 0, "t: expected 0 or more");
+    given(lens, {n}, at::kInt, dev, "lens");
+    given(fresh_tokens, {n}, at::kInt, dev, "new");
+    need(table.dim() == 2, "page_table: expected [n_seqs, max_pages]");
+    given(table, {n, table.size(1)}, at::kInt, dev, "page_table");
+    need(stack.dim() == 1, "free_pages: expected [n_pages]");
+    given(stack, {stack.size(0)}, at::kInt, dev, "free_pages");
+    given(count, {2}, at::kInt, dev, "free_count");
+    const int32_t* done = nullptr;
+    if (a.v[7]) {
+      const at::Tensor& d = tensor(a.v[7], "done");
+      given(d, {n}, at::kInt, dev, "done");
+      done = static_cast<const int32_t*>(d.data_ptr());
+    }
+    const at::Tensor out[6] = {output(a.v[8], {t}, at::kInt, dev, "slots"), output(a.v[9], {t}, at::kInt, dev, "positions"),
+                               output(a.v[10], {(int64_t)n + 1}, at::kInt, dev, "cu_q"),
+                               output(a.v[11], {(int64_t)n + 1}, at::kInt, dev, "cu_k"),
+                               output(a.v[12], {n}, at::kInt, dev, "lens_out"), output(a.v[13], {2}, at::kInt, dev, "count_out")};
+    int32_t* to[6];
+    for (int i = 0; i < 6; ++i) to[i] = static_cast<int32_t*>(out[i].data_ptr());
+    const spa_page_pool pool{static_cast<int32_t*>(stack.data_ptr()), static_cast<const int32_t*>(count.data_ptr()), to[5],
+                             size32(stack.size(0), "free_pages")};
+    check(spa_kv_plan(static_cast<const int32_t*>(lens.data_ptr()), static_cast<const int32_t*>(fresh_tokens.data_ptr()), done, n,
+                      static_cast<int32_t*>(table.data_ptr()), size32(table.size(1), "page_table"), page_size, &pool, t, to[0],
+                      to[1], to[2], to[3], to[4], stream_of(dev)),
+          "spa_kv_plan");
+    written(table);
+    written(stack);
+    PyObject* r = PyTuple_New(6);
+    if (!r) return nullptr;
+    for (int i = 0; i < 6; ++i) {
+      PyObject* o = back(a.v[8 + i], out[i]);
+      if (!o) {
+        Py_DECREF(r);
+        return nullptr;
+      }
+      PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+  });
+}
+
 // A page table of n sequences; n < 0 takes it from the table.
 int32_t table_width(const at::Tensor& t, int64_t n, at::Device dev) {
   need(t.dim() == 2, "page_table: expected [n_seqs, max_pages]");
@@ -655,6 +718,7 @@ PyObject* py_set_error(PyObject*, PyObject* type) {
 #define FAST(name, fn) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(fn)), METH_FASTCALL | METH_KEYWORDS, name##_doc}
 PyMethodDef g_methods[] = {FAST(kv_write, py_kv_write),
                            FAST(kv_read, py_kv_read),
+                           FAST(kv_plan, py_kv_plan),
                            FAST(attention_decode, py_attention_decode),
                            FAST(attention_prefill, py_attention_prefill),
                            FAST(gated_residual_norm, py_gated_residual_norm),

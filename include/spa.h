@@ -494,6 +494,51 @@ spa_status spa_kv_read(const spa_kv_cache* cache, const int32_t* page_table, int
                        const int32_t* cu_seqlens, int32_t total, void* k_out, void* v_out, void* stream);
 
 /*
+ * spa_kv_plan -- page tables, slots and offsets of a step, on the device from
+ * the lengths of its requests.  Sequence s has L = lens[s] cached positions
+ * (0 if done[s] != 0) and gets n = fresh[s] new tokens; P(x) = ceil(x /
+ * page_size).
+ *  1. With done (NULL for none), the pages of the sequences that are over --
+ *     the first P(lens[s]) entries of their rows that name a page -- go back
+ *     on the stack, in the order of the sequences and their columns.  Such a
+ *     sequence may get tokens in the same call: it begins anew.
+ *  2. Rows are given out in the order of the sequences: cu_q[s] .. cu_q[s] +
+ *     n - 1 to sequence s, at the positions L .. L + n - 1.  Tokens past row t
+ *     are cut off, as if the last sequences' fresh were less.
+ *  3. Columns P(L) .. P(L + n) - 1 of its row of the page table receive pages
+ *     from the top of the stack, in the same order.  Where the stack is empty
+ *     they receive -1, and so does a column whose stack entry is no page.
+ *  lens, fresh, done  [device] [n_seqs] int32.  Lengths are cut to 0 ..
+ *             max_pages * page_size, negative fresh counts as 0
+ *  page_table [device] [n_seqs][max_pages] int32; other entries stay as they
+ *             are (those behind a length are never read)
+ *  pool       pages: [device] [n_pages], a stack of page numbers; count:
+ *             [device] how many of them are free; count_out: [device] [2] how
+ *             many are free after the call, and how many pages it lacked.
+ *             count_out may be count
+ *  slots      [device] [t]: each row's slot, -1 where its position has no page
+ *             or is past the table, and for rows past the last token
+ *  positions  [device] [t]: each row's position, 0 past the last token
+ *  cu_q, cu_k [device] [n_seqs + 1]: running sums of the new tokens and of
+ *             the lengths after the step (which stop at 2^31 - 1)
+ *  lens_out   [device] [n_seqs]: the lengths after the step, L + n; may be
+ *             lens
+ * Outputs must not overlap other arguments.  A page must stand in one row
+ * only: rows that share pages cannot be given back here.  A pool is one call's
+ * at a time.  n_seqs and t may be 0.  SPA_ERR_UNSUPPORTED for max_pages *
+ * page_size above 2^29 and n_pages * page_size of 2^31 or more.
+ */
+typedef struct spa_page_pool {
+  int32_t* pages;
+  const int32_t* count;
+  int32_t* count_out;
+  int32_t n_pages;
+} spa_page_pool;
+spa_status spa_kv_plan(const int32_t* lens, const int32_t* fresh, const int32_t* done, int32_t n_seqs, int32_t* page_table,
+                       int32_t max_pages, int32_t page_size, const spa_page_pool* pool, int32_t t, int32_t* slots,
+                       int32_t* positions, int32_t* cu_q, int32_t* cu_k, int32_t* lens_out, void* stream);
+
+/*
  * attention_decode -- attention of one new token per sequence over its cache:
  *   out[s][h] = sum_p softmax_p(scale * q[s][h] . k_p) v_p
  * over the positions p < seq_lens[s] of key-value head h / (n_q_heads /
