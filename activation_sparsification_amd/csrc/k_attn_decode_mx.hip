@@ -168,24 +168,24 @@ __device__ __forceinline__ void add_values(const uint32_t (&raw)[8][NV > 8 ? NV 
   }
 }
 
-// The running maximum, sum and outputs take in a tile's scores t; w receives its weights.
+// The running maximum, sum and outputs take in a tile's scores t, of which c times is the exponent; w receives its weights.
 template <int NV>
-__device__ __forceinline__ void softmax_step(const float (&t)[8], float& m, float& l, f32x4 (&o)[NV], float (&w)[8]) {
+__device__ __forceinline__ void softmax_step(const float (&t)[8], float c, float& m, float& l, f32x4 (&o)[NV], float (&w)[8]) {
   float mx = t[0];
 #pragma unroll
   for (int j = 1; j < 8; ++j) mx = fmaxf(mx, t[j]);
   mx = across_groups_max(mx);
   if (__any(mx > m)) {
-    const float now = fmaxf(m, mx), alpha = exp2_hw(m - (now == -INFINITY ? 0.f : now));
+    const float now = fmaxf(m, mx), alpha = exp2_hw((m - (now == -INFINITY ? 0.f : now)) * c);
     m = now;
     l *= alpha;
 #pragma unroll
     for (int i = 0; i < NV; ++i) o[i] *= alpha;
   }
-  const float base = m == -INFINITY ? 0.f : m;                 // nothing seen yet: every weight is 0
+  const float base = m == -INFINITY ? 0.f : -m * c;            // nothing seen yet: every weight is 0
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    w[j] = exp2_hw(t[j] - base);
+    w[j] = exp2_hw(t[j] * c + base);
     l += w[j];
   }
 }
@@ -213,7 +213,7 @@ __device__ __forceinline__ void load_value(const char* row, int col, int bytes, 
 
 // Any page size: a lane finds one position's place and the others get it by lane exchange.
 template <int DT, int DP>
-__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx(DecodeAttnArgs a) {
+__global__ void __launch_bounds__(kWaves * kWave, DP <= 128 ? 2 : 1) k_attention_decode_mx(DecodeAttnArgs a) {
   constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = QueryPieces<DP>::KS;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int col = lane & 15, g = lane >> 4;
@@ -254,10 +254,10 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx(DecodeAt
         }
         const f32x4 s = scores<DP>(kf, ks, qp);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) t[4 * b + r] = (gone >> (16 * b + 4 * g + r)) & 1u ? -INFINITY : s[r] * a.c;
+        for (int r = 0; r < 4; ++r) t[4 * b + r] = (gone >> (16 * b + 4 * g + r)) & 1u ? -INFINITY : s[r];
       }
       float w[8], vs[8];
-      softmax_step<NV>(t, m, l, o, w);
+      softmax_step<NV>(t, a.c, m, l, o, w);
       uint32_t raw[8][VW];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -270,136 +270,127 @@ __global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx(DecodeAt
       }
       add_values<DT, NV>(raw, vs, w, o);
     }
-    finish<DT, DP, false>(a, p, o, 1.f, m, l);
+    finish<DT, DP, false>(a, p, o, 1.f, m * a.c, l);
   } while (span.left > 0);
 }
 
+// A table entry that a whole wave reads, by the scalar unit: nothing writes the table during the call.
+typedef const __attribute__((address_space(4))) int32_t* table_ptr;
+
 // Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave shares.
-// EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  The page numbers of a wave's next 32 tiles are
-// held one to a lane; keys of the next tile are on their way while this tile's softmax and V product run, and values while its
-// scores are formed.
+// EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  Two tiles are on their way while one is worked
+// on, the page numbers of the next one too.  Every load of the loop is issued whatever the tile (past the last one it is read
+// again): a load that only some rounds issue would make the waits drain all of them.
 template <int DT, int DP, bool EXACT>
-__global__ void __launch_bounds__(kWaves * kWave) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
+__global__ void __launch_bounds__(kWaves * kWave, DP <= 128 ? 2 : 1) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
   constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = QueryPieces<DP>::KS;
-  constexpr int kBatch = kWave / 2;                          // tiles whose page numbers are held
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, g = lane >> 4;
   const int kg = DP == 64 ? g & 1 : g;                       // this lane's 32 dimensions of a k step
   const int d = EXACT ? DP : a.d, bytes = d / 2, groups = (d + kGroup - 1) / kGroup, page = (int)a.page.d;
+  const bool in_row = EXACT || NV * col < d;
+  const uint32_t k_at = (uint32_t)(col * bytes + 16 * kg), ks_at = (uint32_t)(kg * page + col);
+  const uint32_t v_at = (uint32_t)(4 * g * bytes), vs_at = (uint32_t)((in_row ? NV * col / kGroup : 0) * page + 4 * g);
   Span span;
   if (!find_span(a, span)) return;
   do {
     const Piece p = next_piece(a, span);
+    const int len = __builtin_amdgcn_readfirstlane(p.len);
+    const int first = __builtin_amdgcn_readfirstlane(p.begin) + wave;
+    const int n = (__builtin_amdgcn_readfirstlane(p.end) - first + kWaves - 1) / kWaves;      // this wave's tiles
+    const table_ptr table = (table_ptr)(a.table + (size_t)__builtin_amdgcn_readfirstlane(p.seq) * a.max_pages);
+    const uint32_t head = (uint32_t)__builtin_amdgcn_readfirstlane(p.head);
+
+    struct Tile {
+      uint4 k[2][KS];
+      int ks[2][KS];
+      uint32_t v[8][VW], vs[2];
+      bool there[2];
+    };
+    // the first position of block b of tile number `it` (or of the last tile), as far as the sequence has it
+    auto block_at = [&](int it, int b) { return (uint32_t)min((first + kWaves * min(it, n - 1)) * kTile + 16 * b, (len - 1) & ~15); };
+    int pages[2];                        // of the tile that is read next
+    auto find_pages = [&](int it) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) pages[b] = table[a.page.div(block_at(it, b))];
+    };
+    auto load = [&](Tile& x, int it) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        // an absent page: the cache's first one stands in
+        x.there[b] = pages[b] >= 0 && pages[b] < a.n_pages;
+        const uint32_t at = block_at(it, b), off = x.there[b] ? at - a.page.div(at) * (uint32_t)page : 0u;
+        const uint32_t block = x.there[b] ? (uint32_t)pages[b] * (uint32_t)a.hkv + head : 0u;
+        const size_t codes = ((size_t)block * (uint32_t)page + off) * (uint32_t)bytes;
+        const size_t scales = (size_t)block * (uint32_t)(groups * page) + off;
+        const char *k = static_cast<const char*>(a.k) + codes, *v = static_cast<const char*>(a.v) + codes;
+        const uint8_t *ks = static_cast<const uint8_t*>(a.k_scale) + scales, *vs = static_cast<const uint8_t*>(a.v_scale) + scales;
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          if constexpr (EXACT) {
+            x.k[b][c] = stream_load16(k + (k_at + 64 * c));
+            x.ks[b][c] = ks[ks_at + (uint32_t)(4 * c * page)];
+          } else {
+            const int from = 64 * c + 16 * kg;
+            x.k[b][c] = load_codes(k + (k_at + 64 * c), bytes - from);
+            x.ks[b][c] = from < bytes ? ks[ks_at + (uint32_t)(4 * c * page)] : 127;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) load_value<NV>(v + (v_at + (uint32_t)(r * bytes)), col, bytes, in_row, x.v[4 * b + r]);
+        x.vs[b] = *reinterpret_cast<const uint32_t*>(vs + vs_at);
+      }
+    };
+
+    Tile x[2];
+    if (n > 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        find_pages(u);
+        load(x[u], u);
+      }
+      find_pages(2);
+    }
     QueryPieces<DP> qp;
     load_query<DT, DP>(a, p, col, g, qp);
     f32x4 o[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
-
-    const int first = p.begin + wave, n = (p.end - first + kWaves - 1) / kWaves;      // this wave's tiles
-    int pages = -1;                      // lane i: the page of block i % 2 of tile i / 2 of the batch, -1 if there is none
-    auto fetch_pages = [&](int it) {
-      const int at = ((first + kWaves * (it + lane / 2)) * 2 + (lane & 1)) * 16;
-      pages = -1;
-      if (at < p.len) {
-        pages = a.table[(size_t)p.seq * a.max_pages + a.page.div((uint32_t)at)];
-        if (pages >= a.n_pages) pages = -1;
-      }
-    };
-    // block b of tile number `it`: its page and head, its first place there, and whether the page is there (else the cache's
-    // first page stands in)
-    struct Place { uint32_t block, off; bool there; };
-    auto place_of = [&](int it, int b) {
-      const int pg = __builtin_amdgcn_readlane(pages, 2 * (it % kBatch) + b);
-      const uint32_t at = (uint32_t)((first + kWaves * it) * 2 + b) * 16;
-      if (pg < 0) return Place{0u, 0u, false};
-      return Place{(uint32_t)pg * a.hkv + p.head, at - a.page.div(at) * a.page.d, true};
-    };
-    uint4 kr[2][KS];
-    int ks[2][KS];
-    auto load_k = [&](const Place (&at)[2]) {
+    for (int base = 0; base < n; base += 2) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const char* codes = static_cast<const char*>(a.k) + ((size_t)at[b].block * page + at[b].off) * bytes;
-        const uint8_t* sc = static_cast<const uint8_t*>(a.k_scale) + (size_t)at[b].block * groups * page + at[b].off;
+      for (int u = 0; u < 2; ++u) {
+        const int it = base + u, tile = first + kWaves * it;
+        if (it < n) {
+          float t[8], vs[8], w[8];
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          const int from = 64 * c + 16 * kg;
-          if constexpr (EXACT) {
-            kr[b][c] = stream_load16(codes + (uint32_t)(col * bytes + from));
-            ks[b][c] = sc[(uint32_t)((4 * c + kg) * page + col)];
-          } else {
-            kr[b][c] = load_codes(codes + (uint32_t)(col * bytes + from), bytes - from);
-            ks[b][c] = from < bytes ? sc[(uint32_t)((4 * c + kg) * page + col)] : 127;
+          for (int b = 0; b < 2; ++b) {
+            const f32x4 s = scores<DP>(x[u].k[b], x[u].ks[b], qp);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[4 * b + r] = s[r];
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vs[j] = scale_of(x[u].vs[j / 4], j % 4);
+          // the last tile's end and absent pages: what does not count is removed from the scores and the values
+          if ((tile + 1) * kTile > len || !x[u].there[0] || !x[u].there[1]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (tile * kTile + 16 * (j / 4) + 4 * g + j % 4 >= len || !x[u].there[j / 4]) {
+                t[j] = -INFINITY;
+                vs[j] = 1.f;
+#pragma unroll
+                for (int i = 0; i < VW; ++i) x[u].v[j][i] = 0;
+              }
+          }
+          softmax_step<NV>(t, a.c, m, l, o, w);
+          add_values<DT, NV>(x[u].v, vs, w, o);
         }
+        load(x[u], it + 2);
+        find_pages(it + 3);
       }
-    };
-    Place at[2];
-    if (n > 0) {
-      fetch_pages(0);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) at[b] = place_of(0, b);
-      load_k(at);
     }
-    const bool in_row = EXACT || NV * col < d;
-    const int vg = in_row ? NV * col / kGroup : 0;
-    for (int it = 0; it < n; ++it) {
-      const int tile = first + kWaves * it;
-      // values of this tile
-      uint32_t raw[8][VW], vsw[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const char* codes = static_cast<const char*>(a.v) + ((size_t)at[b].block * page + at[b].off) * bytes;
-        const uint8_t* sc = static_cast<const uint8_t*>(a.v_scale) + (size_t)at[b].block * groups * page + at[b].off;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) load_value<NV>(codes + (uint32_t)((4 * g + r) * bytes), col, bytes, in_row, raw[4 * b + r]);
-        vsw[b] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)(vg * page + 4 * g));
-      }
-      // scores
-      float t[8], vs[8], w[8];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const f32x4 s = scores<DP>(kr[b], ks[b], qp);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) t[4 * b + r] = s[r] * a.c;
-      }
-      // the last tile's end and absent pages: what does not count is removed from the scores and the values
-      const bool cut = (tile + 1) * kTile > p.len || !at[0].there || !at[1].there;
-      uint32_t gone = 0;
-      if (cut) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (tile * kTile + 16 * (j / 4) + 4 * g + j % 4 >= p.len || !at[j / 4].there) {
-            gone |= 1u << j;
-            t[j] = -INFINITY;
-          }
-        }
-      }
-      // keys of the next tile
-      if (it + 1 < n) {
-        if ((it + 1) % kBatch == 0) fetch_pages(it + 1);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) at[b] = place_of(it + 1, b);
-        load_k(at);
-      }
-      softmax_step<NV>(t, m, l, o, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vs[j] = scale_of(vsw[j / 4], j % 4);
-      if (cut) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((gone >> j) & 1u) {
-            vs[j] = 1.f;
-#pragma unroll
-            for (int i = 0; i < VW; ++i) raw[j][i] = 0;
-          }
-      }
-      add_values<DT, NV>(raw, vs, w, o);
-    }
-    finish<DT, DP, false>(a, p, o, 1.f, m, l);
+    finish<DT, DP, false>(a, p, o, 1.f, m * a.c, l);
   } while (span.left > 0);
 }
 
