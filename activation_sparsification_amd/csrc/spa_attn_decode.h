@@ -56,7 +56,7 @@ struct Piece {
   int seq, head, h0, heads;    // key-value head; first query head and their number
   int len;                     // positions of the sequence
   int begin, end;              // tiles
-  bool whole;                  // the sequence is this piece alone
+  int whole;                   // 1: the sequence is this piece alone
   int slot;                    // where the piece's sums go if not: two slots to a workgroup
 };
 __device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(tiles_of(seq_len(a, s)), 1); }
@@ -136,15 +136,15 @@ __device__ __forceinline__ uint4 stream_load16(const void* p) {
   const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
-// Joins the four waves and writes the piece's result: lane (col, g) holds dimensions NV * (4 g + r) + i of query
+// Joins the waves and writes the piece's result: lane (col, g) holds dimensions NV * (4 g + r) + i of query
 // head col, its maximum and its own positions' sum; with SCALED, `unit` is what
 // one of o stands for.
-template <int DT, int DP, bool SCALED>
+template <int DT, int DP, bool SCALED, int WAVES = kWaves>
 __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, const f32x4 (&o)[DP / 16], float unit, float m,
                                        float l) {
   constexpr int NV = DP / 16;
-  __shared__ float s_o[kWaves][16][DP + 4];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  __shared__ float s_o[WAVES][16][DP + 4];
+  __shared__ float s_m[WAVES][16], s_l[WAVES][16];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int col = lane & 15, g = lane >> 4;
   l += __shfl_xor(l, 16, kWave);
@@ -155,16 +155,16 @@ __device__ __forceinline__ void finish(const DecodeAttnArgs& a, const Piece& p, 
 #pragma unroll
     for (int i = 0; i < NV; ++i) s_o[wave][col][NV * (4 * g + r) + i] = SCALED ? o[i][r] * unit : o[i][r];
   __syncthreads();
-  for (int e = threadIdx.x; e < p.heads * (DP / 2); e += kWaves * kWave) {
+  for (int e = threadIdx.x; e < p.heads * (DP / 2); e += WAVES * kWave) {
     const int h = e / (DP / 2), dim = e % (DP / 2) * 2;
     if (dim >= a.d) continue;
     float mx = s_m[0][h];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+    for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, s_m[w][h]);
     const float base = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f, x0 = 0.f, x1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const float f = exp2_hw(s_m[w][h] - base);
       sum += f * s_l[w][h];
       x0 += f * s_o[w][h][dim];

@@ -1,7 +1,7 @@
 """The 4-bit cache on the GPU: codes and scales bit for bit, reading back, and decode attention within bounds that are summed
 from its roundings (tests/attention_bounds.py).
 
-Beside those bounds a query element is held to 2^-24 of the largest of its 32, so a score is off by up to 2^-24 scale sum
+Beside those bounds a query element is held to 2^-19 of the largest of its 32, so a score is off by up to 2^-19 scale sum
 over the blocks of max |q| sum |k|; QUERY_ERROR below.  The weights of a float16 call keep 16 bits, finer than the bounds ask.
 """
 import math
@@ -160,14 +160,14 @@ def test_read_absent_pages_are_zero(dev):
 # attention
 # ---------------------------------------------------------------------------------------------------------------
 def query_error(q, k, scale):
-    """What holding query elements to 2^-24 of the largest of their 32 can change in a score: q [1, hq, d], k [lk, hkv, d]."""
+    """What holding query elements to 2^-19 of the largest of their 32 can change in a score: q [1, hq, d], k [lk, hkv, d]."""
     hq, hkv = q.shape[1], k.shape[1]
     most = torch.zeros((1, hq), dtype=torch.float64, device=q.device)
     for i in range(0, q.shape[-1], 32):
         a = q[..., i:i + 32].double().abs().amax(-1)
         size = k[..., i:i + 32].abs().sum(-1).amax(0)
         most += a * size.repeat_interleave(hq // hkv)
-    return 2.0 ** -24 * scale * most
+    return 2.0 ** -19 * scale * most
 
 
 def decode_check(dev, dtype, hq, hkv, d, page, lens, seed=0, scale=None, gain=1.0, absent=(), quiet=False, outlier=1.0):
