@@ -28,6 +28,7 @@ struct RopeKernelArgs {
   RopeArgs a;
   FastDiv per;                       // heads of this workgroup's range
   int tokens;                        // of a workgroup
+  int biased[2], to_keys;            // whether there are biases, and whether the keys go anywhere but the cache
 };
 
 // Sum over the LG lanes that hold a vector, on each of them.
@@ -76,6 +77,21 @@ struct Eight {
   }
 };
 
+// A kernel argument in a register of its own.  Where lanes choose between two arguments by the kind of head, the compiler
+// otherwise reads the chosen one from memory for each lane, a trip to memory ahead of every load and store.
+template <typename T>
+__device__ __forceinline__ T held(T v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// One of three by the kind of head: queries, keys, values.
+template <int FMT, typename T>
+__device__ __forceinline__ T of_kind(bool key, bool value, T q, T k, T v) {
+  const T x = key ? k : q;
+  return FMT != kNone && value ? v : x;
+}
+
 template <int DT, int FMT, int LG>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   constexpr int kGroups = kThreads / LG;
@@ -91,35 +107,71 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   const int items = tokens * heads;
   const bool in_head = lane * 8 < a.d, turns = lane * 8 < a.rot;
   const int c0 = a.neighbours || !turns ? 8 * lane : 4 * lane, c1 = a.neighbours || !turns ? c0 + 4 : a.rot / 2 + 4 * lane;
+  const uint16_t* src[3];
+  uint16_t* dst[2];
+  uint32_t row[3], step[3], drow[2], dstep[2];         // between rows and between heads
+  int norm[2], biased[2];
+  void *cells[2], *scales[2];
+  const int to_keys = held(ka.to_keys);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    src[i] = held(a.src[i] + (size_t)first * a.row[i]);
+    row[i] = held((uint32_t)a.row[i]);
+    step[i] = held((uint32_t)a.head[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    dst[i] = held(a.dst[i] + (size_t)first * a.drow[i]);
+    drow[i] = held((uint32_t)a.drow[i]);
+    dstep[i] = held((uint32_t)a.dhead[i]);
+    norm[i] = held(a.norm[i].kind);
+    biased[i] = held(ka.biased[i]);
+    cells[i] = held(a.pages[i]);
+    scales[i] = held(a.scale[i]);
+  }
 
   // item i: one head of one token
-  auto find = [&](int i, int& tok, int& head) {
-    tok = (int)ka.per.div((uint32_t)i);
-    head = h0 + i - tok * heads;
-    return i < items && head < n_heads && in_head;
+  struct Item { int tok, head; bool key, value, there; };
+  auto find = [&](int i) {
+    Item m;
+    m.tok = (int)ka.per.div((uint32_t)i);
+    m.head = h0 + i - m.tok * heads;
+    m.there = i < items && m.head < n_heads;
+    m.value = FMT != kNone && m.head >= a.hq + a.hkv;
+    m.key = m.head >= a.hq && !m.value;
+    m.head -= of_kind<FMT>(m.key, m.value, 0, a.hq, a.hq + a.hkv);
+    return m;
   };
   auto load = [&](int i, Eight& x) {
-    int tok, head;
+    const Item m = find(i);
     x.a = x.b = make_uint2(0, 0);
-    if (!find(i, tok, head)) return;
-    const int part = head < a.hq ? 0 : head < a.hq + a.hkv ? 1 : 2;
-    const int h = head - (part == 0 ? 0 : part == 1 ? a.hq : a.hq + a.hkv);
-    x.load(a.src[part] + (size_t)(first + tok) * a.row[part] + (size_t)h * a.head[part], c0, c1);
+    if (!m.there || !in_head) return;
+    const uint16_t* p = of_kind<FMT>(m.key, m.value, src[0], src[1], src[2]);
+    const uint32_t r = of_kind<FMT>(m.key, m.value, row[0], row[1], row[2]);
+    const uint32_t h = of_kind<FMT>(m.key, m.value, step[0], step[1], step[2]);
+    x.load(p + ((uint64_t)(uint32_t)m.tok * r + (uint64_t)(uint32_t)m.head * h), c0, c1);
   };
 
   Eight x[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load(group + u * kGroups, x[u]);
-  // each lane's weights and biases of queries and keys
-  Eight w[2], b[2];
-  if (in_head)
+  // each lane's weights of queries and keys, and their biases
+  float w[2][8];
+  Eight b[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (a.norm[s].weight) w[s].load(static_cast<const uint16_t*>(a.norm[s].weight), c0, c1);
-      if (a.norm[s].bias) b[s].load(static_cast<const uint16_t*>(a.norm[s].bias), c0, c1);
-      w[s].pair_up(a.neighbours);
-      b[s].pair_up(a.neighbours);
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[s][e] = 1.f;
+    if (!in_head) continue;
+    if (a.norm[s].weight) {
+      Eight raw;
+      raw.load(static_cast<const uint16_t*>(a.norm[s].weight), c0, c1);
+      raw.pair_up(a.neighbours);
+      raw.template to_f32<DT>(w[s]);
     }
+    if (a.norm[s].bias) b[s].load(static_cast<const uint16_t*>(a.norm[s].bias), c0, c1);
+    b[s].pair_up(a.neighbours);
+  }
   const int pairs = a.rot / 2;
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int tok = i / pairs, f = i - tok * pairs;
@@ -135,17 +187,17 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   for (int base = group; base < items; base += kAhead * kGroups) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      int tok, head;
-      const bool live = find(base + u * kGroups, tok, head);
-      if (base + u * kGroups >= items || head >= n_heads) continue;      // the whole group
-      const bool value = head >= a.hq + a.hkv, key = !value && head >= a.hq;
-      if (!value) {
-        x[u].pair_up(a.neighbours);
+      const Item m = find(base + u * kGroups);
+      Eight y = x[u];
+      load(base + (u + kAhead) * kGroups, x[u]);
+      if (!m.there) continue;                                  // the whole group
+      if (!m.value) {
+        y.pair_up(a.neighbours);
         float v[8];
-        x[u].to_f32<DT>(v);
-        const spa_norm& n = key ? a.norm[1] : a.norm[0];
-        if (n.kind != SPA_NORM_NONE) {
-          if (n.kind == SPA_NORM_LAYER) {
+        y.to_f32<DT>(v);
+        const int kind = m.key ? norm[1] : norm[0];
+        if (kind != SPA_NORM_NONE) {
+          if (kind == SPA_NORM_LAYER) {
             float s = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += v[e];             // lanes past the head hold zeros
@@ -157,17 +209,16 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) q += v[e] * v[e];
           const float r = rsqrtf(group_sum<LG>(q) * inv_d + a.eps);
+          if (m.key) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= r;
-          if (n.weight) {
-            float k[8];
-            (key ? w[1] : w[0]).template to_f32<DT>(k);
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[1][e];
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= k[e];
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[0][e];
           }
-          if (n.bias) {
+          if (m.key ? biased[1] : biased[0]) {
             float k[8];
-            (key ? b[1] : b[0]).template to_f32<DT>(k);
+            (m.key ? b[1] : b[0]).template to_f32<DT>(k);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += k[e];
           }
@@ -175,50 +226,47 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
         if (turns) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 cs = s_turn[tok][4 * lane + e];
+            const float2 cs = s_turn[m.tok][4 * lane + e];
             const float p = v[e], o = v[4 + e];
             v[e] = p * cs.x - o * cs.y;
             v[4 + e] = p * cs.y + o * cs.x;
           }
         }
-        x[u].a = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
-        x[u].b = make_uint2(pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
-        x[u].take_apart(a.neighbours);
-        const int part = key, h = head - (key ? a.hq : 0);
-        if (a.dst[part] && live) {
-          uint16_t* to = a.dst[part] + (size_t)(first + tok) * a.drow[part] + (size_t)h * a.dhead[part];
-          *reinterpret_cast<uint2*>(to + c0) = x[u].a;
-          *reinterpret_cast<uint2*>(to + c1) = x[u].b;
+        y.a = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
+        y.b = make_uint2(pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        y.take_apart(a.neighbours);
+        if ((FMT == kNone || !m.key || to_keys) && in_head) {
+          const uint32_t r = m.key ? drow[1] : drow[0], h = m.key ? dstep[1] : dstep[0];
+          uint16_t* to = (m.key ? dst[1] : dst[0]) + ((uint64_t)(uint32_t)m.tok * r + (uint64_t)(uint32_t)m.head * h);
+          *reinterpret_cast<uint2*>(to + c0) = y.a;
+          *reinterpret_cast<uint2*>(to + c1) = y.b;
         }
       }
       if constexpr (FMT != kNone) {
-        if (head < a.hq) continue;
-        const int s = value, h = head - a.hq - (value ? a.hkv : 0);
-        const int slot = s_slot[tok], page_size = (int)a.page.d;
+        if (!m.key && !m.value) continue;
+        void* pages = m.value ? cells[1] : cells[0];
+        const int slot = s_slot[m.tok], page_size = (int)a.page.d;
         const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
         const bool there = slot >= 0 && pg < a.n_pages && in_head;
-        const size_t block = (size_t)pg * a.hkv + h;
+        const size_t block = (size_t)pg * a.hkv + m.head;
         const int off = slot - pg * page_size;
         if constexpr (kCodes) {
           // 8 consecutive elements to a lane, for the scales
           uint2* mine = reinterpret_cast<uint2*>(s_vec + group * LG);
-          if (in_head) mine[c0 / 4] = x[u].a, mine[c1 / 4] = x[u].b;
+          if (in_head) mine[c0 / 4] = y.a, mine[c1 / 4] = y.b;
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
           __builtin_amdgcn_wave_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
           const uint4 raw = in_head ? s_vec[group * LG + lane] : make_uint4(0, 0, 0, 0);
           __builtin_amdgcn_wave_barrier();
-          store_vector<DT, FMT, LG>(a.pages[s], a.scale[s], block, off, page_size, a.d, lane, there, raw);
+          store_vector<DT, FMT, LG>(pages, m.value ? scales[1] : scales[0], block, off, page_size, a.d, lane, there, raw);
         } else if (there) {
-          uint16_t* to = static_cast<uint16_t*>(a.pages[s]) + (block * page_size + off) * a.d;
-          *reinterpret_cast<uint2*>(to + c0) = x[u].a;
-          *reinterpret_cast<uint2*>(to + c1) = x[u].b;
+          uint16_t* to = static_cast<uint16_t*>(pages) + (block * page_size + off) * a.d;
+          *reinterpret_cast<uint2*>(to + c0) = y.a;
+          *reinterpret_cast<uint2*>(to + c1) = y.b;
         }
       }
     }
-    if (base + kAhead * kGroups < items)
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) load(base + (kAhead + u) * kGroups, x[u]);
   }
 }
 
@@ -230,7 +278,8 @@ hipError_t go(const RopeArgs& a, hipStream_t st) {
   const bool few = a.t <= 256;
   const int per = few ? std::min(heads, kGroups) : heads;
   const int tokens = few ? 1 : kTokens;
-  const RopeKernelArgs ka{a, FastDiv((uint32_t)per), tokens};
+  const RopeKernelArgs ka{a, FastDiv((uint32_t)per), tokens, {a.norm[0].bias != nullptr, a.norm[1].bias != nullptr},
+                          a.dst[1] != nullptr};
   const dim3 grid((a.t + tokens - 1) / tokens, (heads + per - 1) / per);
   hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG>), grid, dim3(kThreads), 0, st, ka);
   return hipGetLastError();
