@@ -19,16 +19,13 @@ namespace spa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;           // of a workgroup at the most
+constexpr int kFewTokens = 256;      // up to these a workgroup takes one token and as many heads as it has lane groups
 constexpr int kMaxPairs = 128;       // of a head of 256
 constexpr int kNone = -1;            // no cache
-constexpr int kAhead = 4;            // rows of a lane group in flight
 
 struct RopeKernelArgs {
   RopeArgs a;
-  FastDiv per;                       // heads of this workgroup's range
-  int tokens;                        // of a workgroup
-  int biased[2], to_keys;            // whether there are biases, and whether the keys go anywhere but the cache
+  int heads;                         // of a workgroup
 };
 
 // Sum over the LG lanes that hold a vector, on each of them.
@@ -50,12 +47,37 @@ __device__ __forceinline__ float group_sum(float v) {
 __device__ __forceinline__ uint32_t evens(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t odds(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
+// What lanes choose by the kind of their head, from values: a choice between variables, or kernel arguments, would be one of
+// addresses, and a trip to memory for each lane ahead of every load and store.
+template <typename T>
+__device__ __forceinline__ T pick(bool key, T q, T k) { return key ? k : q; }
+template <typename T>
+__device__ __forceinline__ T pick(bool key, bool value, T q, T k, T v) { return value ? v : key ? k : q; }
+// Pointers are chosen as numbers, and are global memory's where they are used.
+__device__ __forceinline__ uint64_t address(const void* p) { return reinterpret_cast<uint64_t>(p); }
+__device__ __forceinline__ void* global(uint64_t at) { return (void*)reinterpret_cast<__attribute__((address_space(1))) char*>(at); }
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(1))) u32x2 global_u32x2;
+
 // A lane's 8 elements: the first elements of its four pairs, then the second ones.
 struct Eight {
   uint2 a, b;
-  __device__ __forceinline__ void load(const uint16_t* p, int c0, int c1) {
-    a = *reinterpret_cast<const uint2*>(p + c0);
-    b = *reinterpret_cast<const uint2*>(p + c1);
+  // at: the vector's address
+  __device__ __forceinline__ void load(uint64_t at, int c0, int c1) {
+    const u32x2 x = *reinterpret_cast<const global_u32x2*>(at + 2 * c0), y = *reinterpret_cast<const global_u32x2*>(at + 2 * c1);
+    a = make_uint2(x[0], x[1]);
+    b = make_uint2(y[0], y[1]);
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(uint64_t at, int c0, int c1) const {
+    global_u32x2 *x = reinterpret_cast<global_u32x2*>(at + 2 * c0), *y = reinterpret_cast<global_u32x2*>(at + 2 * c1);
+    if constexpr (STREAM) {
+      __builtin_nontemporal_store(u32x2{a.x, a.y}, x);
+      __builtin_nontemporal_store(u32x2{b.x, b.y}, y);
+    } else {
+      *x = u32x2{a.x, a.y};
+      *y = u32x2{b.x, b.y};
+    }
   }
   __device__ __forceinline__ void pair_up(int neighbours) {
     if (!neighbours) return;
@@ -77,101 +99,49 @@ struct Eight {
   }
 };
 
-// A kernel argument in a register of its own.  Where lanes choose between two arguments by the kind of head, the compiler
-// otherwise reads the chosen one from memory for each lane, a trip to memory ahead of every load and store.
-template <typename T>
-__device__ __forceinline__ T held(T v) {
-  asm volatile("" : "+s"(v));
-  return v;
-}
-
-// One of three by the kind of head: queries, keys, values.
-template <int FMT, typename T>
-__device__ __forceinline__ T of_kind(bool key, bool value, T q, T k, T v) {
-  const T x = key ? k : q;
-  return FMT != kNone && value ? v : x;
-}
-
-template <int DT, int FMT, int LG>
+// A lane group takes one head of TOK tokens at a time, then the next head that is the workgroup's groups further on: kind,
+// weights and addresses are found once for the TOK rows, whose loads are all in flight, and the next head's replace them as they
+// are worked on.
+template <int DT, int FMT, int LG, int TOK>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   constexpr int kGroups = kThreads / LG;
+  // many rows are written past the caches: 8191 tokens take 32.7 us so and 38.2 with plain stores
+  constexpr bool kStream = TOK > 1;
   const RopeArgs& a = ka.a;
-  __shared__ float2 s_turn[kTokens][kMaxPairs];
-  __shared__ int s_slot[kTokens];
+  __shared__ float2 s_turn[TOK][kMaxPairs];
+  __shared__ int s_slot[TOK];
   constexpr bool kCodes = FMT != kNone && FMT != SPA_KV_NATIVE;
   __shared__ uint4 s_vec[kCodes ? kThreads : 1];
   const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
-  const int first = blockIdx.x * ka.tokens, tokens = min(ka.tokens, a.t - first);
-  const int heads = (int)ka.per.d, h0 = blockIdx.y * heads;
+  const int first = blockIdx.x * TOK, tokens = min(TOK, a.t - first);
   const int n_heads = a.hq + a.hkv * (FMT == kNone ? 1 : 2);   // queries, keys and, with a cache, values
-  const int items = tokens * heads;
+  const int end = min((int)(blockIdx.y + 1) * ka.heads, n_heads);
   const bool in_head = lane * 8 < a.d, turns = lane * 8 < a.rot;
   const int c0 = a.neighbours || !turns ? 8 * lane : 4 * lane, c1 = a.neighbours || !turns ? c0 + 4 : a.rot / 2 + 4 * lane;
-  const uint16_t* src[3];
-  uint16_t* dst[2];
-  uint32_t row[3], step[3], drow[2], dstep[2];         // between rows and between heads
-  int norm[2], biased[2];
-  void *cells[2], *scales[2];
-  const int to_keys = held(ka.to_keys);
+  // bytes between rows and between heads
+  const uint64_t q_from = address(a.src[0]), k_from = address(a.src[1]), v_from = address(a.src[2]);
+  const uint32_t q_row = 2 * (uint32_t)a.row[0], k_row = 2 * (uint32_t)a.row[1], v_row = 2 * (uint32_t)a.row[2];
+  const uint32_t q_step = 2 * (uint32_t)a.head[0], k_step = 2 * (uint32_t)a.head[1], v_step = 2 * (uint32_t)a.head[2];
+  const uint32_t k_first = (uint32_t)a.hq, v_first = (uint32_t)(a.hq + a.hkv);
+  auto is_value = [&](int head) { return FMT != kNone && head >= (int)v_first; };
+  auto is_key = [&](int head) { return head >= (int)k_first && !is_value(head); };
+  auto load = [&](int head, Eight (&x)[TOK]) {
+    const bool key = is_key(head), value = is_value(head);
+    const uint32_t h = (uint32_t)head - pick(key, value, 0u, k_first, v_first);
+    const uint32_t r = pick(key, value, q_row, k_row, v_row), st = pick(key, value, q_step, k_step, v_step);
+    uint64_t at = pick(key, value, q_from, k_from, v_from);
+    at += (uint64_t)(uint32_t)first * r + (uint64_t)h * st;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    src[i] = held(a.src[i] + (size_t)first * a.row[i]);
-    row[i] = held((uint32_t)a.row[i]);
-    step[i] = held((uint32_t)a.head[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    dst[i] = held(a.dst[i] + (size_t)first * a.drow[i]);
-    drow[i] = held((uint32_t)a.drow[i]);
-    dstep[i] = held((uint32_t)a.dhead[i]);
-    norm[i] = held(a.norm[i].kind);
-    biased[i] = held(ka.biased[i]);
-    cells[i] = held(a.pages[i]);
-    scales[i] = held(a.scale[i]);
-  }
-
-  // item i: one head of one token
-  struct Item { int tok, head; bool key, value, there; };
-  auto find = [&](int i) {
-    Item m;
-    m.tok = (int)ka.per.div((uint32_t)i);
-    m.head = h0 + i - m.tok * heads;
-    m.there = i < items && m.head < n_heads;
-    m.value = FMT != kNone && m.head >= a.hq + a.hkv;
-    m.key = m.head >= a.hq && !m.value;
-    m.head -= of_kind<FMT>(m.key, m.value, 0, a.hq, a.hq + a.hkv);
-    return m;
-  };
-  auto load = [&](int i, Eight& x) {
-    const Item m = find(i);
-    x.a = x.b = make_uint2(0, 0);
-    if (!m.there || !in_head) return;
-    const uint16_t* p = of_kind<FMT>(m.key, m.value, src[0], src[1], src[2]);
-    const uint32_t r = of_kind<FMT>(m.key, m.value, row[0], row[1], row[2]);
-    const uint32_t h = of_kind<FMT>(m.key, m.value, step[0], step[1], step[2]);
-    x.load(p + ((uint64_t)(uint32_t)m.tok * r + (uint64_t)(uint32_t)m.head * h), c0, c1);
-  };
-
-  Eight x[kAhead];
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(group + u * kGroups, x[u]);
-  // each lane's weights of queries and keys, and their biases
-  float w[2][8];
-  Eight b[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[s][e] = 1.f;
-    if (!in_head) continue;
-    if (a.norm[s].weight) {
-      Eight raw;
-      raw.load(static_cast<const uint16_t*>(a.norm[s].weight), c0, c1);
-      raw.pair_up(a.neighbours);
-      raw.template to_f32<DT>(w[s]);
+    for (int u = 0; u < TOK; ++u) {
+      x[u].a = x[u].b = make_uint2(0, 0);
+      if (head < end && u < tokens && in_head) x[u].load(at, c0, c1);
+      at += r;
     }
-    if (a.norm[s].bias) b[s].load(static_cast<const uint16_t*>(a.norm[s].bias), c0, c1);
-    b[s].pair_up(a.neighbours);
-  }
+  };
+
+  int head = blockIdx.y * ka.heads + group;
+  Eight x[TOK];
+  load(head, x);
   const int pairs = a.rot / 2;
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int tok = i / pairs, f = i - tok * pairs;
@@ -183,24 +153,54 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   if (FMT != kNone && (int)threadIdx.x < tokens) s_slot[threadIdx.x] = a.slots[first + threadIdx.x];
   __syncthreads();
 
+  const int q_kind = a.norm[0].kind, k_kind = a.norm[1].kind;
+  const uint64_t q_weight = address(a.norm[0].weight), k_weight = address(a.norm[1].weight);
+  const uint64_t q_bias = address(a.norm[0].bias), k_bias = address(a.norm[1].bias);
+  const uint64_t q_to = address(a.dst[0]), k_to = address(a.dst[1]);
+  const uint32_t q_row_to = 2 * (uint32_t)a.drow[0], k_row_to = 2 * (uint32_t)a.drow[1];
+  const uint32_t q_step_to = 2 * (uint32_t)a.dhead[0], k_step_to = 2 * (uint32_t)a.dhead[1];
+  const uint64_t k_cells = address(a.pages[0]), v_cells = address(a.pages[1]);
+  const uint64_t k_scale = address(a.scale[0]), v_scale = address(a.scale[1]);
   const float inv_d = 1.f / (float)a.d;
-  for (int base = group; base < items; base += kAhead * kGroups) {
+  for (; head < end; head += kGroups) {
+    const bool key = is_key(head), value = is_value(head);
+    const uint32_t h = (uint32_t)head - pick(key, value, 0u, k_first, v_first);
+    const int norm = pick(key, value, q_kind, k_kind, (int)SPA_NORM_NONE);
+    const uint64_t weight = pick(key, q_weight, k_weight), bias = pick(key, q_bias, k_bias);
+    Eight w, b;                                        // the kind's weights and biases
+    w.a = w.b = b.a = b.b = make_uint2(0, 0);
+    if (in_head && norm != SPA_NORM_NONE) {
+      if (weight) w.load(weight, c0, c1);
+      if (bias) b.load(bias, c0, c1);
+    }
+    const uint32_t r_to = pick(key, q_row_to, k_row_to);
+    uint64_t to = pick(key, q_to, k_to);
+    const bool out = !value && to != 0 && in_head;
+    to += (uint64_t)(uint32_t)first * r_to + (uint64_t)h * pick(key, q_step_to, k_step_to);
+    Eight y[TOK];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const Item m = find(base + u * kGroups);
-      Eight y = x[u];
-      load(base + (u + kAhead) * kGroups, x[u]);
-      if (!m.there) continue;                                  // the whole group
-      if (!m.value) {
-        y.pair_up(a.neighbours);
+    for (int u = 0; u < TOK; ++u) y[u] = x[u];
+    load(head + kGroups, x);
+    float wf[8], bf[8];
+    w.pair_up(a.neighbours);
+    b.pair_up(a.neighbours);
+    w.to_f32<DT>(wf);
+    b.to_f32<DT>(bf);
+    if (!weight)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wf[e] = 1.f;
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) {
+      if (u >= tokens) break;                          // the whole workgroup
+      if (!value) {
+        y[u].pair_up(a.neighbours);
         float v[8];
-        y.to_f32<DT>(v);
-        const int kind = m.key ? norm[1] : norm[0];
-        if (kind != SPA_NORM_NONE) {
-          if (kind == SPA_NORM_LAYER) {
+        y[u].template to_f32<DT>(v);
+        if (norm != SPA_NORM_NONE) {
+          if (norm == SPA_NORM_LAYER) {
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += v[e];             // lanes past the head hold zeros
+            for (int e = 0; e < 8; ++e) s += v[e];     // lanes past the head hold zeros
             const float mean = group_sum<LG>(s) * inv_d;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] -= in_head ? mean : 0.f;
@@ -209,61 +209,47 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) q += v[e] * v[e];
           const float r = rsqrtf(group_sum<LG>(q) * inv_d + a.eps);
-          if (m.key) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[1][e];
-          } else {
+          for (int e = 0; e < 8; ++e) v[e] = v[e] * r * wf[e];
+          if (bias)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[0][e];
-          }
-          if (m.key ? biased[1] : biased[0]) {
-            float k[8];
-            (m.key ? b[1] : b[0]).template to_f32<DT>(k);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += k[e];
-          }
+            for (int e = 0; e < 8; ++e) v[e] += bf[e];
         }
         if (turns) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 cs = s_turn[m.tok][4 * lane + e];
+            const float2 cs = s_turn[u][4 * lane + e];
             const float p = v[e], o = v[4 + e];
             v[e] = p * cs.x - o * cs.y;
             v[4 + e] = p * cs.y + o * cs.x;
           }
         }
-        y.a = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
-        y.b = make_uint2(pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
-        y.take_apart(a.neighbours);
-        if ((FMT == kNone || !m.key || to_keys) && in_head) {
-          const uint32_t r = m.key ? drow[1] : drow[0], h = m.key ? dstep[1] : dstep[0];
-          uint16_t* to = (m.key ? dst[1] : dst[0]) + ((uint64_t)(uint32_t)m.tok * r + (uint64_t)(uint32_t)m.head * h);
-          *reinterpret_cast<uint2*>(to + c0) = y.a;
-          *reinterpret_cast<uint2*>(to + c1) = y.b;
-        }
+        y[u].a = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
+        y[u].b = make_uint2(pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        y[u].take_apart(a.neighbours);
+        if (out) y[u].template store<kStream>(to, c0, c1);
+        to += r_to;
       }
       if constexpr (FMT != kNone) {
-        if (!m.key && !m.value) continue;
-        void* pages = m.value ? cells[1] : cells[0];
-        const int slot = s_slot[m.tok], page_size = (int)a.page.d;
+        if (!key && !value) continue;
+        const uint64_t cells = pick(value, k_cells, v_cells);
+        const int slot = s_slot[u], page_size = (int)a.page.d;
         const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
         const bool there = slot >= 0 && pg < a.n_pages && in_head;
-        const size_t block = (size_t)pg * a.hkv + m.head;
+        const size_t block = (size_t)pg * (uint32_t)a.hkv + h;
         const int off = slot - pg * page_size;
         if constexpr (kCodes) {
           // 8 consecutive elements to a lane, for the scales
           uint2* mine = reinterpret_cast<uint2*>(s_vec + group * LG);
-          if (in_head) mine[c0 / 4] = y.a, mine[c1 / 4] = y.b;
+          if (in_head) mine[c0 / 4] = y[u].a, mine[c1 / 4] = y[u].b;
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
           __builtin_amdgcn_wave_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
           const uint4 raw = in_head ? s_vec[group * LG + lane] : make_uint4(0, 0, 0, 0);
           __builtin_amdgcn_wave_barrier();
-          store_vector<DT, FMT, LG>(pages, m.value ? scales[1] : scales[0], block, off, page_size, a.d, lane, there, raw);
+          store_vector<DT, FMT, LG>(global(cells), global(pick(value, k_scale, v_scale)), block, off, page_size, a.d, lane, there, raw);
         } else if (there) {
-          uint16_t* to = static_cast<uint16_t*>(pages) + (block * page_size + off) * a.d;
-          *reinterpret_cast<uint2*>(to + c0) = y.a;
-          *reinterpret_cast<uint2*>(to + c1) = y.b;
+          y[u].template store<kStream>(cells + 2 * (block * page_size + off) * (uint32_t)a.d, c0, c1);
         }
       }
     }
@@ -274,14 +260,14 @@ template <int DT, int FMT, int LG>
 hipError_t go(const RopeArgs& a, hipStream_t st) {
   constexpr int kGroups = kThreads / LG;
   const int heads = a.hq + a.hkv * (FMT == kNone ? 1 : 2);
-  // few tokens: every group takes one head; many: a workgroup takes all heads of up to kTokens tokens
-  const bool few = a.t <= 256;
-  const int per = few ? std::min(heads, kGroups) : heads;
-  const int tokens = few ? 1 : kTokens;
-  const RopeKernelArgs ka{a, FastDiv((uint32_t)per), tokens, {a.norm[0].bias != nullptr, a.norm[1].bias != nullptr},
-                          a.dst[1] != nullptr};
-  const dim3 grid((a.t + tokens - 1) / tokens, (heads + per - 1) / per);
-  hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG>), grid, dim3(kThreads), 0, st, ka);
+  RopeKernelArgs ka{a, heads};
+  if (a.t <= kFewTokens) {
+    ka.heads = std::min(heads, kGroups);
+    const dim3 grid(a.t, (heads + ka.heads - 1) / ka.heads);
+    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 1>), grid, dim3(kThreads), 0, st, ka);
+  } else {
+    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 4>), dim3((a.t + 3) / 4), dim3(kThreads), 0, st, ka);
+  }
   return hipGetLastError();
 }
 template <int DT, int FMT>
