@@ -6,6 +6,8 @@
 // handles consecutive tokens of one head, keys and values together: consecutive tokens are consecutive positions of
 // a page, so the codes and the 4-byte scales of a workgroup are runs.  8191 tokens by 8 heads of 128 into int8 pages:
 // 11.5 us, 4.5 TB/s; twelve ragged sequences read back from them: 83 us, 4.7 TB/s (a large copy moves 4.9).
+#include <algorithm>
+
 #include "spa_common.h"
 #include "spa_attn.h"
 #include "spa_kv.h"
@@ -58,16 +60,22 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvArgs a) {
   }
 }
 
-// Two e2m1 codes (byte SEL of w) times a power of two, rounded once.
-template <int DT, int SEL>
-__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale) {
-  if constexpr (DT == SPA_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
-  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
-}
-
 // A wave takes kReadRows consecutive rows of one head.  Lane i finds row i's sequence, page and scales, all rows at
 // once, and the groups get them by lane exchange; then every load of the wave's rows is in flight together.
 constexpr int kReadRows = 16;
+// A row's sequence: the number of offsets after the first that are at or below it.  `first`: of the wave's rows.
+__device__ __forceinline__ int sequence_of(const KvArgs& a, int first, int row) {
+  const int wl = threadIdx.x % kWave;
+  int seq = 0;
+  for (int base = 0; base < a.n_seqs; base += kWave) {
+    const int end = base + wl < a.n_seqs ? a.cu[base + wl + 1] : INT32_MAX;
+    const int low = __popcll(__ballot(end <= first)), high = __popcll(__ballot(end <= first + kReadRows - 1));
+    seq += low;
+    for (int i = low; i < high; ++i) seq += __shfl(end, i, kWave) <= row;      // sequences that end within the rows
+  }
+  return seq;
+}
+
 template <int DT, int FMT, int LG>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
   constexpr int PER = kWave / LG, STEPS = (kReadRows + PER - 1) / PER;      // rows side by side, and one after the other
@@ -76,58 +84,39 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
   const int first = (blockIdx.x / a.heads * (kThreads / kWave) + threadIdx.x / kWave) * kReadRows;
   if (first >= a.t) return;                                     // the whole wave
   const int row = first + wl % kReadRows;
-  // a row's sequence: the number of offsets after the first that are at or below it
-  int seq = 0;
-  for (int base = 0; base < a.n_seqs; base += kWave) {
-    const int end = base + wl < a.n_seqs ? a.cu[base + wl + 1] : INT32_MAX;
-    const int low = __popcll(__ballot(end <= first)), high = __popcll(__ballot(end <= first + kReadRows - 1));
-    seq += low;
-    for (int i = low; i < high; ++i) seq += __shfl(end, i, kWave) <= row;      // sequences that end within the rows
-  }
+  const int seq = sequence_of(a, first, row);
   const int page_size = a.page.d;
   bool ok = row < a.t && seq < a.n_seqs;
   const bool mine = ok;
-  int cell = 0, off = 0;
+  int cell = 0;
   if (ok) {
     const int pos = row - a.cu[seq];
     const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
     const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
     ok = pg >= 0 && pg < a.n_pages;
-    if (ok) {
-      off = pos - col * page_size;
-      cell = (pg * a.heads + head) * page_size + off;
-    }
+    if (ok) cell = (pg * a.heads + head) * page_size + (pos - col * page_size);
   }
   float sc[2] = {0.f, 0.f};
-  if constexpr (FMT == SPA_KV_FP8 || FMT == SPA_KV_INT8) {
+  if constexpr (FMT != SPA_KV_NATIVE) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (ok) sc[s] = static_cast<const float*>(a.scale[s])[cell];
   }
   const uint32_t there = (uint32_t)__ballot(ok), write = (uint32_t)__ballot(mine);
   constexpr int W = kWords<FMT>;
-  uint32_t raw[STEPS][2][W], mx[STEPS][2];      // codes; exponent bytes
+  uint32_t raw[STEPS][2][W];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int r = i * PER + wl / LG;
     const size_t c = (uint32_t)__shfl(cell, r & (kReadRows - 1), kWave);
-    [[maybe_unused]] size_t first_scale = 0;
-    if constexpr (FMT == SPA_KV_MXFP4) {
-      const int o = __shfl(off, r & (kReadRows - 1), kWave);
-      first_scale = (c - o) * ((a.d + 31) / 32) + (size_t)(lane / 4) * page_size + o;
-    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int w = 0; w < W; ++w) raw[i][s][w] = 0;
-      mx[i][s] = 0;
       if (r < kReadRows && (there >> r) & 1u && lane * 8 < a.d) {
         if constexpr (FMT == SPA_KV_NATIVE) {
           const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.pages[s]) + c * a.d + lane * 8);
           raw[i][s][0] = v.x; raw[i][s][1] = v.y; raw[i][s][2] = v.z; raw[i][s][3] = v.w;
-        } else if constexpr (FMT == SPA_KV_MXFP4) {
-          raw[i][s][0] = static_cast<const uint32_t*>(a.pages[s])[c * (a.d / 8) + lane];
-          mx[i][s] = static_cast<const uint8_t*>(a.scale[s])[first_scale];
         } else {
           const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.pages[s]) + c * a.d + lane * 8);
           raw[i][s][0] = v.x; raw[i][s][1] = v.y;
@@ -143,10 +132,6 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
       uint4 v;
       if constexpr (FMT == SPA_KV_NATIVE) {
         v = make_uint4(raw[i][s][0], raw[i][s][1], raw[i][s][2], raw[i][s][3]);
-      } else if constexpr (FMT == SPA_KV_MXFP4) {
-        const float k = __uint_as_float(mx[i][s] << 23);
-        const uint32_t w = raw[i][s][0];
-        v = make_uint4(mx_pair<DT, 0>(w, k), mx_pair<DT, 1>(w, k), mx_pair<DT, 2>(w, k), mx_pair<DT, 3>(w, k));
       } else {
         const float k = __shfl(sc[s], r & (kReadRows - 1), kWave);
         float x[8];
@@ -161,12 +146,114 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvArgs a) {
   }
 }
 
+// Two e2m1 codes (byte SEL of w) times a power of two, rounded once.
+template <int DT, int SEL>
+__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale) {
+  if constexpr (DT == SPA_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
+}
+
+// The 4-bit format's rows are a quarter of what is written for them, and 32 to 128 bytes long: a wave finds its rows' places
+// once for all heads of a workgroup (every 4th is its own), and the next head's codes are on their way while one is unpacked.
+// Many rows are written past the caches.  12 ragged sequences of up to 8191 positions by 8 heads of 128: 68 us, 4.8 TB/s.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <int DT, int LG, bool STREAM>
+__global__ void __launch_bounds__(kThreads) k_kv_read_mx(KvArgs a, int heads) {
+  constexpr int PER = kWave / LG, STEPS = (kReadRows + PER - 1) / PER, kWaves = kThreads / kWave;
+  const int wl = threadIdx.x % kWave, lane = wl % LG;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int first = blockIdx.x * kReadRows;
+  const int end = min((int)(blockIdx.y + 1) * heads, a.heads);
+  const int row = first + wl % kReadRows, page_size = (int)a.page.d;
+  const int seq = sequence_of(a, first, row);
+  bool ok = row < a.t && seq < a.n_seqs;
+  const uint32_t write = (uint32_t)__ballot(ok);
+  int block = 0, off = 0;                              // the page's first head; the place in the page
+  if (ok) {
+    const int pos = row - a.cu[seq];
+    const int col = pos >= 0 ? (int)a.page.div((uint32_t)pos) : a.max_pages;
+    const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
+    ok = pg >= 0 && pg < a.n_pages;
+    if (ok) block = pg * a.heads, off = pos - col * page_size;
+  }
+  const uint32_t there = (uint32_t)__ballot(ok);
+  const int words = a.d / 8, groups = (a.d + 31) / 32;
+  const bool in_row = lane < words;
+  size_t code[STEPS], scale[STEPS];                    // of the row's head 0
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = (i * PER + wl / LG) & (kReadRows - 1);
+    const size_t b = (uint32_t)__shfl(block, r, kWave);
+    const int o = __shfl(off, r, kWave);
+    code[i] = (b * page_size + o) * words + lane;
+    scale[i] = (b * groups + lane / 4) * page_size + o;
+  }
+  const size_t code_step = (size_t)page_size * words, scale_step = (size_t)page_size * groups;
+  uint32_t raw[STEPS][2], mx[STEPS][2];
+  auto load = [&](int head) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = i * PER + wl / LG;
+      const bool live = head < end && r < kReadRows && (there >> r) & 1u && in_row;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        raw[i][s] = mx[i][s] = 0;
+        if (live) {
+          raw[i][s] = static_cast<const uint32_t*>(a.pages[s])[code[i] + (size_t)head * code_step];
+          mx[i][s] = static_cast<const uint8_t*>(a.scale[s])[scale[i] + (size_t)head * scale_step];
+        }
+      }
+    }
+  };
+  int head = blockIdx.y * heads + wave;
+  load(head);
+  for (; head < end; head += kWaves) {
+    uint32_t w[STEPS][2], e[STEPS][2];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) w[i][s] = raw[i][s], e[i][s] = mx[i][s];
+    load(head + kWaves);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = i * PER + wl / LG;
+      if (!(r < kReadRows && (write >> r) & 1u && in_row)) continue;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const float k = __uint_as_float(e[i][s] << 23);
+        const u32x4 v = {mx_pair<DT, 0>(w[i][s], k), mx_pair<DT, 1>(w[i][s], k), mx_pair<DT, 2>(w[i][s], k), mx_pair<DT, 3>(w[i][s], k)};
+        u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out[s]) + ((size_t)(first + r) * a.heads + head) * a.d + lane * 8);
+        if constexpr (STREAM) __builtin_nontemporal_store(v, to);
+        else *to = v;
+      }
+    }
+  }
+}
+// Up to these bytes of output they are written through the caches, for the call that reads them next.
+constexpr int64_t kCachedOutput = int64_t(32) << 20;
+template <int DT, int LG>
+hipError_t read_mx(const KvArgs& a, hipStream_t st) {
+  const int chunks = (a.t + kReadRows - 1) / kReadRows;
+  // a workgroup takes as many heads, in fours, as leave two workgroups for each compute unit
+  const int splits = std::min(std::max(512 / chunks, 1), (a.heads + 3) / 4);
+  const int heads = ((a.heads + splits - 1) / splits + 3) / 4 * 4;
+  const dim3 grid(chunks, (a.heads + heads - 1) / heads);
+  if ((int64_t)a.t * a.heads * a.d * 4 > kCachedOutput)
+    hipLaunchKernelGGL((k_kv_read_mx<DT, LG, true>), grid, dim3(kThreads), 0, st, a, heads);
+  else
+    hipLaunchKernelGGL((k_kv_read_mx<DT, LG, false>), grid, dim3(kThreads), 0, st, a, heads);
+  return hipGetLastError();
+}
+
 template <int DT, int FMT, int LG>
 hipError_t go(bool write, const KvArgs& a, hipStream_t st) {
+  if constexpr (FMT == SPA_KV_MXFP4) {
+    if (!write) return read_mx<DT, LG>(a, st);
+  }
   const int rows = write ? kThreads / LG : kThreads / kWave * kReadRows;      // of a workgroup
   const int64_t blocks = ((int64_t)a.t + rows - 1) / rows * a.heads;
   if (write) hipLaunchKernelGGL((k_kv_write<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
-  else hipLaunchKernelGGL((k_kv_read<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
+  else if constexpr (FMT != SPA_KV_MXFP4) hipLaunchKernelGGL((k_kv_read<DT, FMT, LG>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 template <int DT, int FMT>
