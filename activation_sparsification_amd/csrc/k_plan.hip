@@ -4,7 +4,7 @@
 //   the page of column c of s is stack[count - 1 - (pages of the sequences before + c - P(L_s))] whoever asks for it.
 //
 // Little work on the end of a chain of dependent loads: bound by latency.  Every workgroup therefore sums up the lengths for
-// itself (a thread holds four sequences) and no workgroup waits for another; it writes its 2048 rows from what it found.
+// itself and no workgroup waits for another; it writes its rows (512, or 2048) from what it found.
 // Offsets, lengths and the count are one workgroup's work: the same one for a call of one, an extra one for larger calls,
 // and a launch of its own where they replace the values that the others read.
 #include "spa_attn.h"
@@ -14,8 +14,7 @@ namespace spa {
 
 namespace {
 
-constexpr int kThreads = 512, kPer = 4;                // sequences, and rows, of a thread
-constexpr int kRows = kThreads * kPer;                 // of a workgroup
+constexpr int kThreads = 512;
 constexpr uint32_t kMost = 0x7FFFFFFFu;
 
 struct Add {
@@ -31,22 +30,29 @@ template <int CTRL, int ROW_MASK, typename Op>
 __device__ __forceinline__ uint32_t scan_step(uint32_t v, Op op) {
   return op(v, (uint32_t)__builtin_amdgcn_update_dpp(Op::kNothing, (int)v, CTRL, ROW_MASK, 0xF, false));
 }
-// What `op` makes of the threads before this one and, in `all`, of the whole workgroup.
+// What `op` makes of the lanes up to and with this one.
 template <typename Op>
-__device__ __forceinline__ uint32_t scan_before(uint32_t v, Op op, uint32_t (&s_wave)[kThreads / kWave], uint32_t& all) {
+__device__ __forceinline__ uint32_t wave_scan_of(uint32_t v, Op op) {
   v = scan_step<0x111, 0xF>(v, op);    // within rows of 16
   v = scan_step<0x112, 0xF>(v, op);
   v = scan_step<0x114, 0xF>(v, op);
   v = scan_step<0x118, 0xF>(v, op);
   v = scan_step<0x142, 0xA>(v, op);    // the rows before
-  v = scan_step<0x143, 0xC>(v, op);
+  return scan_step<0x143, 0xC>(v, op);
+}
+// What `op` makes of the threads before this one and, in `all`, of the whole workgroup of W waves.  The first half leaves each
+// wave's result in s_wave; a barrier comes between.
+template <int W>
+__device__ __forceinline__ void scan_offer(uint32_t v, uint32_t (&s_wave)[W]) {
+  if ((threadIdx.x & (kWave - 1)) == kWave - 1) s_wave[threadIdx.x / kWave] = v;
+}
+template <int W, typename Op>
+__device__ __forceinline__ uint32_t scan_take(uint32_t v, Op op, const uint32_t (&s_wave)[W], uint32_t& all) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  if (lane == kWave - 1) s_wave[wave] = v;
-  __syncthreads();
   uint32_t before = (uint32_t)Op::kNothing;
   all = (uint32_t)Op::kNothing;
 #pragma unroll
-  for (int w = 0; w < kThreads / kWave; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w == wave) before = all;
     all = op(all, s_wave[w]);
   }
@@ -55,49 +61,60 @@ __device__ __forceinline__ uint32_t scan_before(uint32_t v, Op op, uint32_t (&s_
 }
 
 // A sequence as its rows see it: the row's position less its number; its number; the new pages before column 0, so that column
-// c's is number pages + c; the columns that it had.
-struct Home { int shift, seq, pages, old; };
+// c's is number pages + c; the columns that it had, and the page of the last of them.
+struct Home { int shift, seq, pages, old, page; };
 
 __device__ __forceinline__ int pages_of(const PlanArgs& a, int length) {
   return (int)a.page.div((uint32_t)(length + (int)a.page.d - 1));
 }
 
-// rows: this workgroup writes rows; commit: and, or, the offsets, lengths and count.
+// rows: this workgroup writes the rows from `first`, PER to a thread; commit: and, or, the offsets, lengths and count.  A thread
+// holds PER sequences at a time.
+template <int THREADS, int PER>
 __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, int first) {
-  __shared__ uint32_t s_wave[3][kThreads / kWave];
+  constexpr int kRows = THREADS * PER, W = THREADS / kWave;
+  __shared__ uint32_t s_wave[4][W];
   __shared__ Home s_home[kRows + 1];                   // at a sequence's first row; the last: of the sequence that began before
   __shared__ int s_begins[kRows];
   const int tid = threadIdx.x, end = rows ? min(first + kRows, a.t) : 0;
   const int cap = a.max_pages * (int)a.page.d;
-  const int avail = min(max(a.count[0], 0), a.n_pages);
+  const int count = a.count[0];
   if (rows)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s_begins[i * kThreads + tid] = -1;
+    for (int i = 0; i < PER; ++i) s_begins[i * THREADS + tid] = -1;
   uint32_t done_rows = 0, done_pages = 0, done_keys = 0;       // of the sequences so far
-  if (rows && tid == 0) s_home[kRows].seq = -1;
-  for (int base = 0; base < a.n_seqs; base += kThreads * kPer) {
-    int have[kPer], fresh[kPer];
+  const Add fit{(uint32_t)a.t}, most{kMost};
+  for (int base = 0; base < a.n_seqs; base += kRows) {
+    int have[PER], fresh[PER], page[PER];
     uint32_t sum = 0;
-    const Add fit{(uint32_t)a.t};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int s = base + tid * kPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = base + tid * PER + i;
       have[i] = fresh[i] = 0;
       if (s < a.n_seqs) {
-        have[i] = a.done && a.done[s] ? 0 : min(max(a.lens[s], 0), cap);
-        fresh[i] = min(max(a.fresh[s], 0), a.t);
+        const int length = a.lens[s], tokens = a.fresh[s], over = a.done ? a.done[s] : 0;
+        have[i] = over ? 0 : min(max(length, 0), cap);
+        fresh[i] = min(max(tokens, 0), a.t);
       }
       sum = fit(sum, (uint32_t)fresh[i]);
     }
-    uint32_t all_rows, all_pages, all_keys = 0;
-    // (a third buffer in turn would do for the barriers; three are simpler: each is written again only after the others' barriers)
-    uint32_t row = fit(done_rows, scan_before(sum, fit, s_wave[0], all_rows));
-    uint32_t want = 0, keys = 0;
-    const Add most{kMost};
-    int start[kPer], need[kPer];
-    uint32_t at = row;
+    // a page that is not full takes the first of the new rows
+    if (rows)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+      for (int i = 0; i < PER; ++i) {
+        const int s = base + tid * PER + i, old = pages_of(a, have[i]);
+        page[i] = -1;
+        if (s < a.n_seqs && fresh[i] > 0 && old * (int)a.page.d > have[i]) page[i] = a.table[(size_t)s * a.max_pages + old - 1];
+      }
+    sum = wave_scan_of(sum, fit);
+    scan_offer<W>(sum, s_wave[0]);
+    __syncthreads();
+    uint32_t all_rows, all_pages, all_keys;
+    uint32_t at = fit(done_rows, scan_take<W>(sum, fit, s_wave[0], all_rows));
+    uint32_t want = 0, keys = 0;
+    int start[PER], need[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
       start[i] = (int)at;
       const uint32_t to = fit(at, (uint32_t)fresh[i]);
       fresh[i] = (int)(to - at);                       // the rows end at t: what is past them is cut off
@@ -106,15 +123,20 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
       want += (uint32_t)need[i];
       keys = most(keys, (uint32_t)(have[i] + fresh[i]));
     }
-    uint32_t page = done_pages + scan_before(want, most, s_wave[1], all_pages);
-    uint32_t key = commit ? most(done_keys, scan_before(keys, most, s_wave[2], all_keys)) : 0;
+    want = wave_scan_of(want, most);
+    keys = wave_scan_of(keys, most);
+    scan_offer<W>(want, s_wave[1]);
+    scan_offer<W>(keys, s_wave[2]);
+    __syncthreads();
+    uint32_t pages = done_pages + scan_take<W>(want, most, s_wave[1], all_pages);
+    uint32_t key = most(done_keys, scan_take<W>(keys, most, s_wave[2], all_keys));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int s = base + tid * kPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = base + tid * PER + i;
       const int old = pages_of(a, have[i]);
       if (rows && fresh[i] > 0 && start[i] < end && start[i] + fresh[i] > first) {
         const int local = start[i] < first ? kRows : start[i] - first;
-        s_home[local] = Home{have[i] - start[i], s, (int)page - old, old};
+        s_home[local] = Home{have[i] - start[i], s, (int)pages - old, old, page[i]};
         if (start[i] >= first) s_begins[local] = local;
       }
       if (commit && s < a.n_seqs) {
@@ -123,30 +145,34 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
         a.cu_k[s + 1] = (int)key;
         a.lens_out[s] = have[i] + fresh[i];
       }
-      page += (uint32_t)need[i];
+      pages += (uint32_t)need[i];
     }
     done_rows = fit(done_rows, all_rows);
     done_pages += all_pages;
     done_keys = most(done_keys, all_keys);
-    __syncthreads();                                   // the scans' buffers and, after the last, the homes
+    __syncthreads();                                   // the homes are there; the scans' buffers may be written again
     if (!commit && (int)done_rows >= end) break;       // every row has its sequence
   }
+  const int avail = min(max(count, 0), a.n_pages);
   if (commit && tid == 0) {
     a.cu_q[0] = a.cu_k[0] = 0;
     a.count_out[0] = max(avail - (int)min(done_pages, kMost), 0);
     a.count_out[1] = max((int)min(done_pages, kMost) - avail, 0);
   }
   if (!rows) return;
-  __syncthreads();
-  int begins[kPer];
+  if (a.n_seqs == 0) __syncthreads();                  // nothing has waited for s_begins yet
+  int begins[PER];
   int best = -1;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) best = begins[i] = max(best, s_begins[tid * kPer + i]);
+  for (int i = 0; i < PER; ++i) best = begins[i] = max(best, s_begins[tid * PER + i]);
+  const uint32_t upto = wave_scan_of((uint32_t)best, Max{});
+  scan_offer<W>(upto, s_wave[3]);
+  __syncthreads();
   uint32_t all;
-  const int before = (int)scan_before((uint32_t)best, Max{}, s_wave[0], all);
+  const int before = (int)scan_take<W>(upto, Max{}, s_wave[3], all);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = first + tid * kPer + i;
+  for (int i = 0; i < PER; ++i) {
+    const int r = first + tid * PER + i;
     if (r >= end) break;
     const int at = max(before, begins[i]);
     int slot = -1, pos = 0;
@@ -155,10 +181,8 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
       pos = r + h.shift;
       if (pos < cap) {
         const int col = (int)a.page.div((uint32_t)pos), off = pos - col * (int)a.page.d;
-        int pg;
-        if (col < h.old) {
-          pg = a.table[(size_t)h.seq * a.max_pages + col];
-        } else {
+        int pg = h.page;
+        if (col >= h.old) {
           const int from = avail - 1 - (h.pages + col);
           pg = from >= 0 ? a.stack[from] : -1;
           if (pg >= a.n_pages) pg = -1;
@@ -173,17 +197,18 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
 }
 
 // mode: 0 rows and the rest in one workgroup; 1 rows, the last workgroup the rest; 2 rows alone; 3 the rest alone
-__global__ void __launch_bounds__(kThreads) k_kv_plan(PlanArgs a, int mode) {
+template <int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) k_kv_plan(PlanArgs a, int mode) {
   const bool last = blockIdx.x + 1 == gridDim.x;
   const bool rows = mode == 0 || mode == 2 || (mode == 1 && !last);
-  plan(a, rows, mode == 0 || mode == 3 || (mode == 1 && last), (int)blockIdx.x * kRows);
+  plan<THREADS, PER>(a, rows, mode == 0 || mode == 3 || (mode == 1 && last), (int)blockIdx.x * THREADS * PER);
 }
 
 // The pages of sequences that are over go back on the stack, in the order of the sequences and their columns.  One workgroup:
 // it takes 512 sequences at a time, lists those that are over, counts their pages a wave to each, and copies them.
 __global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
-  constexpr int kLook = 8;                             // entries of a lane in flight
-  __shared__ uint32_t s_wave[2][kThreads / kWave];
+  constexpr int kLook = 8, kWaves = kThreads / kWave;  // entries of a lane in flight
+  __shared__ uint32_t s_wave[2][kWaves];
   __shared__ int2 s_list[kThreads];                    // sequence, columns
   __shared__ int s_count[kThreads];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -193,7 +218,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
     const int s = base + tid;
     const int cols = s < a.n_seqs && a.done[s] ? pages_of(a, min(max(a.lens[s], 0), cap)) : 0;
     uint32_t listed, total;
-    const uint32_t place = scan_before(cols > 0 ? 1u : 0u, Add{kMost}, s_wave[0], listed);
+    const uint32_t mine = wave_scan_of(cols > 0 ? 1u : 0u, Add{kMost});
+    scan_offer<kWaves>(mine, s_wave[0]);
+    __syncthreads();
+    const uint32_t place = scan_take<kWaves>(mine, Add{kMost}, s_wave[0], listed);
     if (cols > 0) s_list[place] = make_int2(s, cols);
     s_count[tid] = 0;
     __syncthreads();
@@ -207,17 +235,20 @@ __global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
         for (int u = 0; u < kLook; ++u) each(pg[u], pg[u] >= 0 && pg[u] < a.n_pages);
       }
     };
-    for (int i = wave; i < (int)listed; i += kThreads / kWave) {
+    for (int i = wave; i < (int)listed; i += kWaves) {
       int n = 0;
       walk(s_list[i], [&](int, bool ok) { n += __popcll(__ballot(ok)); });
       if (lane == 0) s_count[i] = n;
     }
     __syncthreads();
-    const uint32_t before = scan_before((uint32_t)s_count[tid], Add{kMost}, s_wave[1], total);
+    const uint32_t upto = wave_scan_of((uint32_t)s_count[tid], Add{kMost});
+    scan_offer<kWaves>(upto, s_wave[1]);
+    __syncthreads();
+    const uint32_t before = scan_take<kWaves>(upto, Add{kMost}, s_wave[1], total);
     __syncthreads();
     s_count[tid] = (int)before;
     __syncthreads();
-    for (int i = wave; i < (int)listed; i += kThreads / kWave) {
+    for (int i = wave; i < (int)listed; i += kWaves) {
       int64_t to = (int64_t)count + s_count[i];
       walk(s_list[i], [&](int pg, bool ok) {
         const uint64_t there = __ballot(ok);
@@ -232,6 +263,20 @@ __global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
   if (tid == 0) a.count_out[0] = count;
 }
 
+
+template <int THREADS, int PER>
+hipError_t go(const PlanArgs& a, bool replaces, hipStream_t st) {
+  const int blocks = (a.t + THREADS * PER - 1) / (THREADS * PER);
+  auto run = [&](int grid, int mode) {
+    hipLaunchKernelGGL((k_kv_plan<THREADS, PER>), dim3(grid), dim3(THREADS), 0, st, a, mode);
+    return hipGetLastError();
+  };
+  if (blocks <= 1) return run(1, 0);
+  if (!replaces) return run(blocks + 1, 1);
+  const hipError_t e = run(blocks, 2);
+  return e ? e : run(1, 3);
+}
+
 }  // namespace
 
 hipError_t launch_kv_plan(PlanArgs a, hipStream_t st) {
@@ -242,17 +287,11 @@ hipError_t launch_kv_plan(PlanArgs a, hipStream_t st) {
     a.count = a.count_out;
     replaces = true;
   }
-  const int blocks = (a.t + kRows - 1) / kRows;
-  if (blocks <= 1) {
-    hipLaunchKernelGGL(k_kv_plan, dim3(1), dim3(kThreads), 0, st, a, 0);
-  } else if (!replaces) {
-    hipLaunchKernelGGL(k_kv_plan, dim3(blocks + 1), dim3(kThreads), 0, st, a, 1);
-  } else {
-    hipLaunchKernelGGL(k_kv_plan, dim3(blocks), dim3(kThreads), 0, st, a, 2);
-    if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL(k_kv_plan, dim3(1), dim3(kThreads), 0, st, a, 3);
-  }
-  return hipGetLastError();
+  // As few rows to a workgroup as there are threads, if they also hold all sequences at once; one wave waits for nobody: 64
+  // sequences take 2.5 us so, 5.4 with 512 threads of four.  More sequences: fewer workgroups that each sum them up.
+  if (a.t <= kWave && a.n_seqs <= kWave) return go<kWave, 1>(a, replaces, st);
+  if (a.n_seqs <= kThreads) return go<kThreads, 1>(a, replaces, st);
+  return go<kThreads, 4>(a, replaces, st);
 }
 
 }  // namespace spa
