@@ -59,21 +59,26 @@ struct Piece {
   int whole;                   // 1: the sequence is this piece alone
   int slot;                    // where the piece's sums go if not: two slots to a workgroup
 };
-__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) { return max(tiles_of(seq_len(a, s)), 1); }
+// START: what beginning a sequence costs a workgroup, in tiles; every sequence's share has so many ahead of its own.
+template <int START>
+__device__ __forceinline__ int seq_share(const DecodeAttnArgs& a, int s) {
+  return max(tiles_of(seq_len(a, s)), 1) + START;
+}
 
+template <int START = 0>
 __device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
   const int lane = threadIdx.x & (kWave - 1);
   s.lens = lane < a.n_seqs ? seq_len(a, lane) : 0;
-  const int c0 = lane < a.n_seqs ? max(tiles_of(s.lens), 1) : 0;
+  const int c0 = lane < a.n_seqs ? max(tiles_of(s.lens), 1) + START : 0;
   const int incl0 = wave_scan(c0);
   long long total = __builtin_amdgcn_readlane(incl0, kWave - 1);
   for (int base = kWave; base < a.n_seqs; base += kWave) {
-    long long c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
+    long long c = base + lane < a.n_seqs ? seq_share<START>(a, base + lane) : 0;
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) c += __shfl_xor(c, off, kWave);
     total += c;
   }
-  const int per = (int)max((total + a.target - 1) / a.target, (long long)kMinTiles);
+  const int per = (int)max((total + a.target - 1) / a.target, (long long)(kMinTiles + START));
   const long long start = (long long)blockIdx.x * per;
   if (start >= total) return false;
   long long before = 0;
@@ -83,7 +88,7 @@ __device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
     before += __builtin_amdgcn_readlane(incl, kWave - 1);
     base += kWave;
     if (base >= a.n_seqs) return false;
-    c = base + lane < a.n_seqs ? seq_share(a, base + lane) : 0;
+    c = base + lane < a.n_seqs ? seq_share<START>(a, base + lane) : 0;
     incl = wave_scan(c);
   }
   const int at = __ffsll((unsigned long long)past) - 1;
@@ -95,29 +100,36 @@ __device__ __forceinline__ bool find_span(const DecodeAttnArgs& a, Span& s) {
   return true;
 }
 
-__device__ __forceinline__ Piece next_piece(const DecodeAttnArgs& a, Span& s) {
-  Piece p;
+// The next piece of a workgroup's share; false if the share ends in a sequence's START, whose tiles are the next workgroup's.
+template <int START>
+__device__ __forceinline__ bool next_piece(const DecodeAttnArgs& a, Span& s, Piece& p) {
   p.seq = s.seq;
   const int ht = blockIdx.y / a.hkv;
   p.head = blockIdx.y % a.hkv;
   p.heads = min(a.group - 16 * ht, 16);
   p.h0 = p.head * a.group + 16 * ht;
   p.len = s.seq < kWave ? __builtin_amdgcn_readlane(s.lens, s.seq) : seq_len(a, s.seq);
-  const int tiles = tiles_of(p.len), share = max(tiles, 1);
-  const int take = min(share - s.local, s.left);
-  p.begin = s.local;
-  p.end = min(s.local + take, tiles);
-  p.whole = take == share;
+  const int tiles = tiles_of(p.len), share = max(tiles, 1) + START;
+  const int take = min(share - s.local, s.left), upto = s.local + take;
+  const bool some = upto > START, begins = some && s.local <= START;
+  p.begin = max(s.local - START, 0);
+  p.end = min(upto - START, tiles);
+  p.whole = begins && upto == share;
   // a piece that starts inside its sequence is its workgroup's first, one that ends inside its last
   p.slot = 2 * blockIdx.x + (s.local == 0 && !s.fresh);
-  if (s.local == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    const int more = share - take;                              // tiles in the workgroups after this one
+  if (begins && blockIdx.y == 0 && threadIdx.x == 0) {
+    const int more = share - upto;                              // tiles in the workgroups after this one
     a.part_of[p.seq] = make_int2(p.slot, 1 + (more + s.per - 1) / s.per);
   }
   s.left -= take;
   ++s.seq;
   s.local = 0;
   s.fresh = false;
+  return some;
+}
+__device__ __forceinline__ Piece next_piece(const DecodeAttnArgs& a, Span& s) {
+  Piece p;
+  next_piece<0>(a, s, p);
   return p;
 }
 
@@ -263,9 +275,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_decode_join(DecodeAt
 }
 
 // Workgroups of a head: no more than the table has room for.
-inline int units_of(const DecodeAttnArgs& a) {
+inline int units_of(const DecodeAttnArgs& a, int start = 0) {
   const int64_t room = ((int64_t)a.max_pages * a.page.d + kTile - 1) / kTile;
-  return (int)std::min<int64_t>(a.target, (std::max<int64_t>(room, 1) * a.n_seqs + kMinTiles - 1) / kMinTiles);
+  const int64_t least = kMinTiles + start;
+  return (int)std::min<int64_t>(a.target, ((std::max<int64_t>(room, 1) + start) * a.n_seqs + least - 1) / least);
 }
 template <int DT>
 hipError_t join_pieces(const DecodeAttnArgs& a, int units, hipStream_t st) {

@@ -5,6 +5,7 @@ Beside those bounds a query element is held to 2^-19 of the largest of its 32, s
 over the blocks of max |q| sum |k|; QUERY_ERROR below.  The weights of a float16 call keep 16 bits, finer than the bounds ask.
 """
 import math
+import random
 
 import pytest
 import torch
@@ -220,6 +221,16 @@ def test_decode_long(dev, dtype, page):
     decode_check(dev, dtype, 4, 1, 128, page, [70001, 3, 9000])
     decode_check(dev, dtype, 2, 2, 64, page, [30000, 30001])
     decode_check(dev, dtype, 2, 1, 256, page, [20000])
+
+
+@pytest.mark.parametrize("n,longest,d,hkv", [(3, 9000, 128, 8), (40, 1500, 128, 8), (130, 700, 64, 8), (9, 6000, 256, 4), (70, 3000, 96, 2)])
+def test_decode_shares(dev, n, longest, d, hkv):
+    # ragged batches whose tiles are shared by many workgroups: shares that begin and end anywhere in a sequence, also right
+    # behind its beginning, empty sequences and ones of a position between them
+    r = random.Random(n)
+    for seed in range(3):
+        lens = [r.choice([0, 1, 32, 33, r.randint(1, longest), r.randint(1, longest)]) for _ in range(n)]
+        decode_check(dev, (BF16, F16)[seed % 2], 2 * hkv, hkv, d, 16, lens, seed=seed, quiet=seed > 0)
 
 
 def test_decode_many_sequences(dev):
