@@ -181,8 +181,8 @@ at::Tensor output(PyObject* o, Shape shape, at::ScalarType type, at::Device dev,
   given(t, shape, type, dev, name);
   return t;
 }
-// Several one-dimensional outputs, given or new.  The new ones are parts of one allocation: for small calls allocating is most of
-// the host's time (six tensors 4 us, one 0.8).
+// Several one-dimensional outputs, given or new.  The new ones are parts of one allocation: a plan of four tensors takes the
+// host 4.4 us so, 3.2 with all of them given; six allocations alone took 4.
 template <int N>
 void outputs(PyObject* const* given_ones, const int64_t (&sizes)[N], const char* const (&names)[N], at::ScalarType type,
              at::Device dev, at::Tensor (&out)[N]) {
@@ -192,7 +192,7 @@ void outputs(PyObject* const* given_ones, const int64_t (&sizes)[N], const char*
   const at::Tensor all = total ? fresh({total}, type, dev) : at::Tensor();
   int64_t at = 0;
   for (int i = 0; i < N; ++i) {
-    if (given_ones[i]) {
+    if (given_ones[i] || !sizes[i]) {
       out[i] = output(given_ones[i], {sizes[i]}, type, dev, names[i]);
       continue;
     }

@@ -266,3 +266,20 @@ def test_writes_are_known_to_autograd(dev):
     lens = torch.zeros(2, dtype=I32, device=dev)
     spa.kv_plan(lens, lens + 3, table, 4, *pool, 6, lens_out=lens, count_out=pool[1])
     assert all(a > b for a, b in zip((table._version, pool[0]._version, pool[1]._version), before)) and lens._version > 0
+
+
+def test_some_outputs_given(dev):
+    # new outputs beside given ones, also where all that is new has no elements
+    pool, count = spa.new_page_pool(4, dev)
+    lens, new, table = ints([2], dev), ints([0], dev), ints([[1, -1]], dev)
+    given = dict(cu_q=ints([9, 9], dev), cu_k=ints([9, 9], dev), lens_out=ints([9], dev), count_out=ints([9, 9], dev))
+    got = dict(zip(NAMES, spa.kv_plan(lens, new, table, 4, pool, count, 0, **given)))
+    assert got["slots"].shape == got["positions"].shape == (0,) and got["cu_k"].tolist() == [0, 2] and got["lens"].tolist() == [2]
+    with torch.inference_mode():
+        got = dict(zip(NAMES, spa.kv_plan(lens, new + 1, table, 4, pool, count, 2, cu_q=given["cu_q"])))
+        got["slots"] += 1
+    assert got["slots"].tolist() == [7, 0] and got["positions"].tolist() == [2, 0] and given["cu_q"].tolist() == [0, 1]
+    got = dict(zip(NAMES, spa.kv_plan(lens, new, table, 4, pool, count, 3)))
+    version = got["positions"]._version
+    got["slots"].add_(1)
+    assert got["positions"]._version == version and got["positions"].tolist() == [0, 0, 0] and got["slots"].tolist() == [0, 0, 0]
