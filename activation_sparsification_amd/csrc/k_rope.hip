@@ -19,7 +19,12 @@ namespace spa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewTokens = 256;      // up to these a workgroup takes one token and as many heads as it has lane groups
+// Up to kFewTokens a workgroup takes one token and as many heads as it has lane groups, above them kTokens tokens and all heads.
+// 32 + 8 heads of 128, one token to a workgroup and two: 5.1 and 6.0 us for 300 tokens, 6.8 and 7.1 for 600 (into the cache), 7.5
+// and 7.2 for 1000, 14.1 and 10.6 for 2000 (into the cache).  Four and eight tokens: 9.1 and 13.4 us for 1000, 14.8 (two: 15.7)
+// and 17.9 for 4000, 31.3 (30.7) and 31.7 for 8191.
+constexpr int kFewTokens = 768;
+constexpr int kTokens = 2;
 constexpr int kMaxPairs = 128;       // of a head of 256
 constexpr int kNone = -1;            // no cache
 
@@ -105,7 +110,7 @@ struct Eight {
 template <int DT, int FMT, int LG, int TOK>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   constexpr int kGroups = kThreads / LG;
-  // many rows are written past the caches: 8191 tokens take 32.7 us so and 38.2 with plain stores
+  // many rows are written past the caches: 8191 tokens took 32.7 us so and 38.2 with plain stores, four tokens to a workgroup
   constexpr bool kStream = TOK > 1;
   const RopeArgs& a = ka.a;
   __shared__ float2 s_turn[TOK][kMaxPairs];
@@ -266,7 +271,7 @@ hipError_t go(const RopeArgs& a, hipStream_t st) {
     const dim3 grid(a.t, (heads + ka.heads - 1) / ka.heads);
     hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 1>), grid, dim3(kThreads), 0, st, ka);
   } else {
-    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 4>), dim3((a.t + 3) / 4), dim3(kThreads), 0, st, ka);
+    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, kTokens>), dim3((a.t + kTokens - 1) / kTokens), dim3(kThreads), 0, st, ka);
   }
   return hipGetLastError();
 }

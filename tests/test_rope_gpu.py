@@ -193,6 +193,32 @@ def test_cache_as_written_apart(dev, fmt, dtype, t, hq, hkv, d, rot, page, neigh
         assert torch.equal(want.view(torch.uint8), one.view(torch.uint8)) and torch.equal(want.view(torch.uint8), two.view(torch.uint8))
 
 
+@pytest.mark.parametrize("t", [768, 769, 1000, 2051])
+@pytest.mark.parametrize("hq,hkv,d,rot,neighbours", [(5, 3, 128, 64, False), (3, 1, 48, 48, True), (2, 2, 256, 256, False)])
+def test_few_and_many_tokens_agree(dev, t, hq, hkv, d, rot, neighbours):
+    # a row's outputs and cached vectors do not depend on how many rows the call has
+    q, k, v, w, b = inputs(dev, t + d, t, hq, hkv, d, BF16)
+    g = gen(dev, t)
+    pos = torch.randint(0, 2 ** 31 - 1, (t,), generator=g, device=dev).to(I32)
+    freq = frequencies(rot, dev)
+    slots = torch.randperm(t + 64, generator=g, device=dev)[:t].to(I32)
+    slots[torch.rand(t, generator=g, device=dev) < 0.1] = -1
+    n_pages = -(-(t + 64) // 16)
+    args = dict(q_weight=w[0], k_weight=w[1], q_bias=b[0], k_bias=b[1], norm="layer", interleaved=neighbours)
+    for fmt in FORMATS:
+        one, other = (spa.new_kv_cache(n_pages, 16, hkv, d, BF16, fmt, dev) for _ in range(2))
+        qo, ko = spa.qk_norm_rope(q, k, pos, freq, v=v, slots=slots, cache=one, k_out=torch.empty(k.shape, dtype=BF16, device=dev), **args)
+        for at in range(0, t, 500):
+            s = slice(at, at + 500)
+            qs, ks = spa.qk_norm_rope(q[s], k[s], pos[s], freq, v=v[s], slots=slots[s], cache=other,
+                                      k_out=torch.empty(k[s].shape, dtype=BF16, device=dev), **args)
+            assert torch.equal(qo[s], qs) and torch.equal(ko[s], ks)
+        for x, y in ((one.k, other.k), (one.v, other.v), (one.k_scale, other.k_scale), (one.v_scale, other.v_scale)):
+            assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    check(qo, reference(q, pos, freq, "layer", w[0], b[0], 1e-5, neighbours), BF16)
+    check(ko, reference(k, pos, freq, "layer", w[1], b[1], 1e-5, neighbours), BF16)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_nonfinite_heads_stay_by_themselves(dev, fmt):
     q, k, v, w, _ = inputs(dev, 1, 40, 4, 2, 128, BF16)
