@@ -36,7 +36,7 @@ spa_status spa_kv_read(const spa_kv_cache* cache, const int32_t* page_table, int
 spa_status spa_kv_plan(const int32_t* lens, const int32_t* fresh, const int32_t* done, int32_t n_seqs, int32_t* page_table,
                        int32_t max_pages, int32_t page_size, const spa_page_pool* pool, int32_t t, int32_t* slots,
                        int32_t* positions, int32_t* cu_q, int32_t* cu_k, int32_t* lens_out, void* stream) {
-  if (spa_status s = check_kv_plan(lens, fresh, n_seqs, page_table, max_pages, page_size, pool, t, slots, positions, cu_q, cu_k,
+  if (spa_status s = check_kv_plan(lens, fresh, done, n_seqs, page_table, max_pages, page_size, pool, t, slots, positions, cu_q, cu_k,
                                    lens_out))
     return s;
   spa::PlanArgs a{};

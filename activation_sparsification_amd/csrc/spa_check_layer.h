@@ -74,7 +74,15 @@ inline spa_status check_kv_read(const spa_kv_cache* c, const int32_t* table, int
 }
 
 // ---- page tables and slots ----
-inline spa_status check_kv_plan(const int32_t* lens, const int32_t* fresh, int32_t n_seqs, const int32_t* table,
+struct Ints {
+  const int32_t* at;
+  int64_t n;
+};
+inline bool overlap(const Ints& a, const Ints& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n * 4 && y < x + (uintptr_t)a.n * 4;
+}
+inline spa_status check_kv_plan(const int32_t* lens, const int32_t* fresh, const int32_t* done, int32_t n_seqs, const int32_t* table,
                                 int32_t max_pages, int32_t page_size, const spa_page_pool* pool, int32_t t, const int32_t* slots,
                                 const int32_t* positions, const int32_t* cu_q, const int32_t* cu_k, const int32_t* lens_out) {
   if (n_seqs < 0 || n_seqs > kMaxSeqs || max_pages < 0 || page_size < 1 || t < 0 || t > kMaxRows) return SPA_ERR_INVALID;
@@ -85,6 +93,18 @@ inline spa_status check_kv_plan(const int32_t* lens, const int32_t* fresh, int32
   if (t > 0 && (!slots || !positions || slots == positions)) return SPA_ERR_INVALID;
   // positions of a sequence are numbered in 29 bits, so that a length and a call's new rows add up in 31; slots in 31
   if ((int64_t)max_pages * page_size > kMaxPositions || (int64_t)pool->n_pages * page_size > INT32_MAX) return SPA_ERR_UNSUPPORTED;
+  // what is written lies apart from everything else, but for the lengths and the count in place
+  const Ints out[] = {{lens_out, n_seqs}, {pool->count_out, 2}, {slots, t}, {positions, t}, {cu_q, (int64_t)n_seqs + 1},
+                      {cu_k, (int64_t)n_seqs + 1}, {table, (int64_t)n_seqs * max_pages}, {pool->pages, pool->n_pages}};
+  const Ints in[] = {{lens_out == lens ? nullptr : lens, lens_out == lens ? 0 : n_seqs},
+                     {pool->count_out == pool->count ? nullptr : pool->count, pool->count_out == pool->count ? 0 : 1},
+                     {fresh, n_seqs}, {done, done ? n_seqs : 0}};
+  for (const Ints& o : out) {
+    for (const Ints& i : in)
+      if (overlap(o, i)) return SPA_ERR_INVALID;
+    for (const Ints* p = out; p != &o; ++p)
+      if (overlap(o, *p)) return SPA_ERR_INVALID;
+  }
   return SPA_OK;
 }
 
@@ -204,6 +224,10 @@ inline bool apart(const spa_heads* h, int64_t rows, int64_t heads, int64_t d) {
   return rows <= 1 || heads <= 1 || h->row_stride >= (heads - 1) * h->head_stride + d ||
          h->head_stride >= (rows - 1) * h->row_stride + d;
 }
+// Written where it was read, each vector is its own; written elsewhere, it lies anywhere.
+inline bool in_place(const spa_heads* to, const spa_heads* from, int64_t rows, int64_t heads) {
+  return to->data != from->data || ((rows <= 1 || to->row_stride == from->row_stride) && (heads <= 1 || to->head_stride == from->head_stride));
+}
 inline bool valid_norm(const spa_norm* n) {
   return !n || (n->kind >= SPA_NORM_NONE && n->kind <= SPA_NORM_LAYER);
 }
@@ -234,6 +258,11 @@ inline spa_status check_qk_norm_rope(const spa_heads* q, const spa_heads* k, con
   if (c ? !v || !valid_heads(v) || !valid_strides(v) || !slots : !k_out) return SPA_ERR_INVALID;
   if (k_out && (!valid_heads(k_out) || !valid_strides(k_out) || !apart(k_out, t, n_kv_heads, head_dim))) return SPA_ERR_INVALID;
   if (!apart(q_out, t, n_q_heads, head_dim)) return SPA_ERR_INVALID;
+  // in place means vector by vector
+  if (k_out && k_out->data == q_out->data) return SPA_ERR_INVALID;
+  if (q_out->data == k->data || (k_out && k_out->data == q->data)) return SPA_ERR_INVALID;
+  if (!in_place(q_out, q, t, n_q_heads) || (k_out && !in_place(k_out, k, t, n_kv_heads))) return SPA_ERR_INVALID;
+  if (c && (q_out->data == v->data || (k_out && k_out->data == v->data))) return SPA_ERR_INVALID;
   if (s != SPA_OK) return s;
   for (const spa_heads* h : {q, k, q_out, c ? v : q, k_out ? k_out : q})
     if (!built_heads(h)) return SPA_ERR_UNSUPPORTED;

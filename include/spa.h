@@ -523,10 +523,11 @@ spa_status spa_kv_read(const spa_kv_cache* cache, const int32_t* page_table, int
  *             the lengths after the step (which stop at 2^31 - 1)
  *  lens_out   [device] [n_seqs]: the lengths after the step, L + n; may be
  *             lens
- * Outputs must not overlap other arguments.  A page must stand in one row
- * only: rows that share pages cannot be given back here.  A pool is one call's
- * at a time.  n_seqs and t may be 0.  SPA_ERR_UNSUPPORTED for max_pages *
- * page_size above 2^29 and n_pages * page_size of 2^31 or more.
+ * Outputs, page_table and pages must not overlap each other or any input, but
+ * for the two above: SPA_ERR_INVALID.  A page must stand in one row only: rows
+ * that share pages cannot be given back here.  A pool is one call's at a time.
+ * n_seqs and t may be 0.  SPA_ERR_UNSUPPORTED for max_pages * page_size above
+ * 2^29 and n_pages * page_size of 2^31 or more.
  */
 typedef struct spa_page_pool {
   int32_t* pages;
@@ -640,9 +641,10 @@ spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t 
  *  positions [device] [t] int32, any value (NULL without rotation)
  *  rope      NULL, or rotary_dim 0, for no rotation
  *  q_norm, k_norm  NULL: SPA_NORM_NONE
- *  q_out, k_out  where the vectors go (written through `data`; no two vectors
- *            of one may overlap); may be q and k themselves, and otherwise
- *            must not overlap any input.  k_out may be NULL with a cache
+ *  q_out, k_out  where the vectors go (written through `data`; no two of them
+ *            may overlap); may be q and k themselves, vector by vector, and
+ *            otherwise must not overlap any input.  k_out may be NULL with a
+ *            cache
  *  v, slots, cache  NULL, or: k's result and v's vectors are stored at the
  *            slots [t], just as spa_kv_write(k_out, v, ...) would store them
  *            (cache->dtype is dtype; its heads and head_dim are k's)
