@@ -25,6 +25,7 @@ constexpr int kGroup = 32;           // elements of one scale
 // What beginning a sequence costs a workgroup, in tiles: its query, the first loads' way, the join of the waves.  64 ragged
 // sequences of up to 8191 positions: 57.7 us without it, 54.8 with 6, 52.5 with 10 to 16; 40 of up to 1500: 23.5, 19.1, 18.6.
 constexpr int kStart = 12;
+constexpr int kUnits = 256;          // compute units
 constexpr int kPieces = 4;           // of a query element, 5 bits each, at the least
 
 template <int CTRL>
@@ -356,6 +357,11 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
   const bool in_row = EXACT || NV * col < d;
   const uint32_t k_at = (uint32_t)(col * bytes + 16 * kg), ks_at = (uint32_t)(kg * page + col);
   const uint32_t v_at = (uint32_t)(4 * g * bytes), vs_at = (uint32_t)((in_row ? NV * col / kGroup : 0) * page + 4 * g);
+  // Of the workgroups on a unit the one that came first is served first, and the later ones end after it, alone: 66 and 79 us of a
+  // call of 82.  The n-th to come (from 0) therefore goes first for n / (n + 1) of a piece, and they end together (two sequences of
+  // 200003 81.3 -> 78.2 us, 64 ragged ones of up to 8191 53.3 -> 51.9, two of 100000 by 20 heads 118.4 -> 113.0; one workgroup
+  // to a unit: the same).
+  const int nth = (int)(blockIdx.x + gridDim.x * blockIdx.y) / kUnits;
   Span span;
   if (!find_span<kStart>(a, span)) return;
 
@@ -450,6 +456,10 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
       find_pages(from, place);
     }
     for (int base = 0; base < steps; base += 2) {
+      if (DP < 256 && nth) {
+        if (base * (nth + 1) < steps * nth) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int it = base + u, tile = now.first + kWaves * it;
