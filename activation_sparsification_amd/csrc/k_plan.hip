@@ -5,8 +5,8 @@
 //
 // Little work on the end of a chain of dependent loads: bound by latency.  Every workgroup therefore sums up the lengths for
 // itself and no workgroup waits for another; it writes its rows (512, or 2048) from what it found.
-// Offsets, lengths and the count are one workgroup's work: the same one for a call of one, an extra one for larger calls,
-// and a launch of its own where they replace the values that the others read.
+// Offsets, lengths and the count are one workgroup's work: the same one for a call of one, an extra one for larger calls, and
+// a launch ahead of the rows where they replace what is read or pages come back first; the rows are then found from them.
 #include "spa_attn.h"
 #include "spa_layer.h"
 
@@ -69,16 +69,16 @@ __device__ __forceinline__ int pages_of(const PlanArgs& a, int length) {
 }
 
 // rows: this workgroup writes the rows from `first`, PER to a thread; commit: and, or, the offsets, lengths and count.  A thread
-// holds PER sequences at a time.
-template <int THREADS, int PER>
-__device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, int first) {
+// holds PER sequences at a time.  count: the free pages.  AFTER: offsets, lengths and count are written already, and the state
+// before is found from them: L + n and the running sums of n give L, count and all new pages what was free.
+template <int THREADS, int PER, bool AFTER>
+__device__ __forceinline__ void plan(const PlanArgs& a, int count, bool rows, bool commit, int first) {
   constexpr int kRows = THREADS * PER, W = THREADS / kWave;
   __shared__ uint32_t s_wave[4][W];
   __shared__ Home s_home[kRows + 1];                   // at a sequence's first row; the last: of the sequence that began before
   __shared__ int s_begins[kRows];
   const int tid = threadIdx.x, end = rows ? min(first + kRows, a.t) : 0;
   const int cap = a.max_pages * (int)a.page.d;
-  const int count = a.count[0];
   if (rows)
 #pragma unroll
     for (int i = 0; i < PER; ++i) s_begins[i * THREADS + tid] = -1;
@@ -92,9 +92,14 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
       const int s = base + tid * PER + i;
       have[i] = fresh[i] = 0;
       if (s < a.n_seqs) {
-        const int length = a.lens[s], tokens = a.fresh[s], over = a.done ? a.done[s] : 0;
-        have[i] = over ? 0 : min(max(length, 0), cap);
-        fresh[i] = min(max(tokens, 0), a.t);
+        if constexpr (AFTER) {
+          fresh[i] = a.cu_q[s + 1] - a.cu_q[s];
+          have[i] = a.lens_out[s] - fresh[i];
+        } else {
+          const int length = a.lens[s], tokens = a.fresh[s], over = a.done ? a.done[s] : 0;
+          have[i] = over ? 0 : min(max(length, 0), cap);
+          fresh[i] = min(max(tokens, 0), a.t);
+        }
       }
       sum = fit(sum, (uint32_t)fresh[i]);
     }
@@ -151,9 +156,9 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
     done_pages += all_pages;
     done_keys = most(done_keys, all_keys);
     __syncthreads();                                   // the homes are there; the scans' buffers may be written again
-    if (!commit && (int)done_rows >= end) break;       // every row has its sequence
+    if (!AFTER && !commit && (int)done_rows >= end) break;     // every row has its sequence
   }
-  const int avail = min(max(count, 0), a.n_pages);
+  const int avail = AFTER ? count + (int)done_pages : min(max(count, 0), a.n_pages);
   if (commit && tid == 0) {
     a.cu_q[0] = a.cu_k[0] = 0;
     a.count_out[0] = max(avail - (int)min(done_pages, kMost), 0);
@@ -196,17 +201,10 @@ __device__ __forceinline__ void plan(const PlanArgs& a, bool rows, bool commit, 
   }
 }
 
-// mode: 0 rows and the rest in one workgroup; 1 rows, the last workgroup the rest; 2 rows alone; 3 the rest alone
-template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS) k_kv_plan(PlanArgs a, int mode) {
-  const bool last = blockIdx.x + 1 == gridDim.x;
-  const bool rows = mode == 0 || mode == 2 || (mode == 1 && !last);
-  plan<THREADS, PER>(a, rows, mode == 0 || mode == 3 || (mode == 1 && last), (int)blockIdx.x * THREADS * PER);
-}
-
 // The pages of sequences that are over go back on the stack, in the order of the sequences and their columns.  One workgroup:
-// it takes 512 sequences at a time, lists those that are over, counts their pages a wave to each, and copies them.
-__global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
+// it takes 512 sequences at a time, lists those that are over, counts their pages a wave to each, and copies them.  Returns what
+// is free then.
+__device__ __forceinline__ int release(const PlanArgs& a) {
   constexpr int kLook = 8, kWaves = kThreads / kWave;  // entries of a lane in flight
   __shared__ uint32_t s_wave[2][kWaves];
   __shared__ int2 s_list[kThreads];                    // sequence, columns
@@ -260,38 +258,55 @@ __global__ void __launch_bounds__(kThreads) k_kv_release(PlanArgs a) {
     count = (int)min((int64_t)count + total, (int64_t)a.n_pages);
     __syncthreads();
   }
-  if (tid == 0) a.count_out[0] = count;
+  return count;
 }
 
+// mode: 0 rows and the rest in one workgroup; 1 rows, the last workgroup the rest; 2 the rest alone; 3 rows after it
+template <int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) k_kv_plan(PlanArgs a, int mode) {
+  const int first = (int)blockIdx.x * THREADS * PER;
+  if (mode == 3) {
+    plan<THREADS, PER, true>(a, a.count_out[0] - a.count_out[1], true, false, first);
+  } else {
+    const bool rest = mode != 1 || blockIdx.x + 1 == gridDim.x;
+    plan<THREADS, PER, false>(a, a.count[0], mode == 0 || !rest, rest, first);
+  }
+}
+// Where sequences are over: mode 0 or 2 of the above behind their pages' return, in one workgroup.  64 sequences of which some are
+// over: 6.1 us a call, 8.9 with a launch for the return; 211 with prompts of 45000 rows among them 11.2, 13.3.
+template <int PER>
+__global__ void __launch_bounds__(kThreads) k_kv_plan_done(PlanArgs a, int mode) {
+  const int count = release(a);
+  __syncthreads();                                     // what is on the stack now may be taken
+  plan<kThreads, PER, false>(a, count, mode == 0, true, 0);
+}
 
 template <int THREADS, int PER>
-hipError_t go(const PlanArgs& a, bool replaces, hipStream_t st) {
+hipError_t go(const PlanArgs& a, hipStream_t st) {
   const int blocks = (a.t + THREADS * PER - 1) / (THREADS * PER);
   auto run = [&](int grid, int mode) {
     hipLaunchKernelGGL((k_kv_plan<THREADS, PER>), dim3(grid), dim3(THREADS), 0, st, a, mode);
     return hipGetLastError();
   };
-  if (blocks <= 1) return run(1, 0);
-  if (!replaces) return run(blocks + 1, 1);
-  const hipError_t e = run(blocks, 2);
-  return e ? e : run(1, 3);
+  if (a.done) {
+    hipLaunchKernelGGL((k_kv_plan_done<PER>), dim3(1), dim3(kThreads), 0, st, a, blocks <= 1 ? 0 : 2);
+    if (hipError_t e = hipGetLastError()) return e;
+  } else {
+    if (blocks <= 1) return run(1, 0);
+    if (a.lens_out != a.lens && a.count_out != a.count) return run(blocks + 1, 1);
+    if (hipError_t e = run(1, 2)) return e;
+  }
+  return blocks <= 1 ? hipSuccess : run(blocks, 3);
 }
 
 }  // namespace
 
 hipError_t launch_kv_plan(PlanArgs a, hipStream_t st) {
-  bool replaces = a.lens_out == a.lens || a.count_out == a.count;
-  if (a.done) {
-    hipLaunchKernelGGL(k_kv_release, dim3(1), dim3(kThreads), 0, st, a);
-    if (hipError_t e = hipGetLastError()) return e;
-    a.count = a.count_out;
-    replaces = true;
-  }
   // As few rows to a workgroup as there are threads, if they also hold all sequences at once; one wave waits for nobody: 64
   // sequences take 2.5 us so, 5.4 with 512 threads of four.  More sequences: fewer workgroups that each sum them up.
-  if (a.t <= kWave && a.n_seqs <= kWave) return go<kWave, 1>(a, replaces, st);
-  if (a.n_seqs <= kThreads) return go<kThreads, 1>(a, replaces, st);
-  return go<kThreads, 4>(a, replaces, st);
+  if (a.t <= kWave && a.n_seqs <= kWave && !a.done) return go<kWave, 1>(a, st);
+  if (a.n_seqs <= kThreads) return go<kThreads, 1>(a, st);
+  return go<kThreads, 4>(a, st);
 }
 
 }  // namespace spa

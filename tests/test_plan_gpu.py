@@ -283,3 +283,32 @@ def test_some_outputs_given(dev):
     version = got["positions"]._version
     got["slots"].add_(1)
     assert got["positions"]._version == version and got["positions"].tolist() == [0, 0, 0] and got["slots"].tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("n,longest,most_new,t,page", [(1, 70, 5, 3, 16), (64, 300, 1, 64, 16), (65, 300, 1, 70, 16), (90, 200, 8, 512, 4), (90, 200, 12, 513, 4),
+                                                       (211, 800, 60, 5000, 32), (513, 100, 3, 1500, 16), (600, 90, 7, 2049, 8), (2500, 40, 4, 9000, 16)])
+def test_requests_that_end_and_begin(dev, inplace, n, longest, most_new, t, page):
+    # over or not, with tokens in the same call or not; enough pages and too few; rows to spare and too few of them
+    rng = random.Random(n + t)
+    for few in (False, True):
+        lens, new = [rng.randint(0, longest) for _ in range(n)], [rng.choice([0, 1, rng.randint(0, most_new)]) for _ in range(n)]
+        done = [int(rng.random() < 0.3) for _ in range(n)]
+        width = -(-(longest + most_new) // page)
+        held = sum(-(-x // page) for x in lens)
+        table, stack, count = state(rng, lens, page, width, held + (n // 8 if few else n * 3))
+        run(dev, lens, new, table, page, stack, count, t // 2 if few else t, done, inplace)
+
+
+def test_replaced_in_part(dev):
+    # only the lengths, or only the count, in place, in calls of several workgroups
+    rng = random.Random(5)
+    for name, done in (("lens_out", None), ("count_out", None), ("lens_out", [0, 1, 0]), ("count_out", [1, 0, 0])):
+        lens, new, page = [700, 20, 333], [900, 40, 800], 16
+        table, stack, count = state(rng, lens, page, 120, 200)
+        want = P.plan(lens, new, table, page, stack, count, 1800, done)
+        args = [ints(lens, dev), ints(new, dev), ints(table, dev), page, ints(stack, dev), ints([count, 0], dev), 1800]
+        given = {name: args[0] if name == "lens_out" else args[5]}
+        got = dict(zip(NAMES, spa.kv_plan(*args, done=None if done is None else ints(done, dev), **given)))
+        for key, x in want.items():
+            assert {**got, "table": args[2], "stack": args[4]}[key].tolist() == x, (name, key)
