@@ -25,6 +25,10 @@ constexpr int kGroup = 32;           // elements of one scale
 // What beginning a sequence costs a workgroup, in tiles: its query, the first loads' way, the join of the waves.  64 ragged
 // sequences of up to 8191 positions: 57.7 us without it, 54.8 with 6, 52.5 with 10 to 16; 40 of up to 1500: 23.5, 19.1, 18.6.
 constexpr int kStart = 12;
+// Tables of up to so many tiles to a sequence: a workgroup takes a sequence whole, and there is no join.  With 8 heads of 128, one
+// sequence of 500 takes 7.5 us so and 10.5 divided, of 1000 11.2 and 11.2, of 2000 17.4 and 11.2; 16 ragged ones of up to 1000 11.7 and
+// 13.9, 128 of up to 500 by 20 heads 41.6 and 59.1.
+constexpr int kWholeTiles = 32;
 constexpr int kUnits = 256;          // compute units
 constexpr int kPieces = 4;           // of a query element, 5 bits each, at the least
 
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
   // call of 82.  The n-th to come (from 0) therefore goes first for n / (n + 1) of a piece, and they end together (two sequences of
   // 200003 81.3 -> 78.2 us, 64 ragged ones of up to 8191 53.3 -> 51.9, two of 100000 by 20 heads 118.4 -> 113.0; one workgroup
   // to a unit: the same).
-  const int nth = (int)(blockIdx.x + gridDim.x * blockIdx.y) / kUnits;
+  const int nth = a.whole ? 0 : (int)(blockIdx.x + gridDim.x * blockIdx.y) / kUnits;
   Span span;
   if (!find_span<kStart>(a, span)) return;
 
@@ -510,15 +514,16 @@ void launch_blocks(const DecodeAttnArgs& a, dim3 grid, hipStream_t st) {
   else hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, false, PACK>), grid, block, 0, st, a);
 }
 template <int DT, int DP>
-hipError_t go(const DecodeAttnArgs& a, hipStream_t st) {
-  const int units = units_of(a, kStart);
+hipError_t go(DecodeAttnArgs a, hipStream_t st) {
+  a.whole = a.page.d % 16 == 0 && (int64_t)a.max_pages * a.page.d <= kWholeTiles * kTile;
+  const int units = a.whole ? a.n_seqs : units_of(a, kStart);
   const dim3 grid(units, a.hkv * a.head_tiles);
   if (a.page.d % 16) hipLaunchKernelGGL((k_attention_decode_mx<DT, DP>), grid, dim3(kWaves * kWave), 0, st, a);
   else if (a.group <= 4) launch_blocks<DT, DP, 4>(a, grid, st);
   else if (a.group <= 8) launch_blocks<DT, DP, 2>(a, grid, st);
   else launch_blocks<DT, DP, 1>(a, grid, st);
   if (hipError_t e = hipGetLastError()) return e;
-  return join_pieces<DT>(a, units, st);
+  return a.whole ? hipSuccess : join_pieces<DT>(a, units, st);
 }
 template <int DT>
 hipError_t by_dim(const DecodeAttnArgs& a, hipStream_t st) {

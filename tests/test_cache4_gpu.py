@@ -171,7 +171,7 @@ def query_error(q, k, scale):
     return 2.0 ** -19 * scale * most
 
 
-def decode_check(dev, dtype, hq, hkv, d, page, lens, seed=0, scale=None, gain=1.0, absent=(), quiet=False, outlier=1.0):
+def decode_check(dev, dtype, hq, hkv, d, page, lens, seed=0, scale=None, gain=1.0, absent=(), quiet=False, outlier=1.0, room=0):
     if not quiet:
         print(f"[decode] {NAMES[dtype]} heads {hq}/{hkv}x{d} page {page} lens {lens[:8]}", flush=True)
     g = gen(dev, seed + d + page)
@@ -179,6 +179,9 @@ def decode_check(dev, dtype, hq, hkv, d, page, lens, seed=0, scale=None, gain=1.
     cache = spa.new_kv_cache(n_pages, page, hkv, d, dtype, "mxfp4", dev)
     held = M.fill(cache, g, dtype, gain)
     table = table_for(dev, g, lens, page, n_pages)
+    wider = -(-room // page) - table.shape[1]
+    if wider > 0:                       # a table of `room` positions to a sequence, as for sequences that go on
+        table = torch.nn.functional.pad(table, (0, wider), value=2 ** 31 - 1).contiguous()
     full = table.clone()
     for s, column in absent:
         table[s, column] = -1 if column % 2 else n_pages
@@ -231,6 +234,16 @@ def test_decode_shares(dev, n, longest, d, hkv):
     for seed in range(3):
         lens = [r.choice([0, 1, 32, 33, r.randint(1, longest), r.randint(1, longest)]) for _ in range(n)]
         decode_check(dev, (BF16, F16)[seed % 2], 2 * hkv, hkv, d, 16, lens, seed=seed, quiet=seed > 0)
+
+
+@pytest.mark.parametrize("room", [1, 1024, 1040, 9000])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (3, 3, 64), (12, 2, 256), (20, 1, 96)])
+def test_decode_tables(dev, room, hq, hkv, d):
+    # what a sequence is divided into depends on the table's width too: whole ones, few pieces, shares that end in a beginning
+    for page in (16, 32, 20):
+        decode_check(dev, F16, hq, hkv, d, page, [1], room=room, quiet=True)
+        decode_check(dev, BF16, hq, hkv, d, page, [1000, 0, 1, 32, 33, 500, 1008], seed=1, room=room)
+        decode_check(dev, F16, hq, hkv, d, page, [(61 * i) % 170 for i in range(90)], seed=2, room=room, quiet=True)
 
 
 def test_decode_many_sequences(dev):
