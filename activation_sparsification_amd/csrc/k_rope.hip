@@ -25,12 +25,12 @@ constexpr int kThreads = 256;
 // and 17.9 for 4000, 31.3 (30.7) and 31.7 for 8191.
 constexpr int kFewTokens = 768;
 constexpr int kTokens = 2;
-constexpr int kMaxPairs = 128;       // of a head of 256
 constexpr int kNone = -1;            // no cache
 
 struct RopeKernelArgs {
   RopeArgs a;
   int heads;                         // of a workgroup
+  int rows;                          // that many times TOK tokens to a workgroup, side by side
 };
 
 // Sum over the LG lanes that hold a vector, on each of them.
@@ -104,21 +104,28 @@ struct Eight {
   }
 };
 
+// SIDE: the heads fill no more than half of the groups, and several rows of TOK tokens stand side by side (33229 tokens of 8 + 1
+// heads of 64 into the cache 30.1 -> 23.1 us).
 // A lane group takes one head of TOK tokens at a time, then the next head that is the workgroup's groups further on: kind,
 // weights and addresses are found once for the TOK rows, whose loads are all in flight, and the next head's replace them as they
 // are worked on.
-template <int DT, int FMT, int LG, int TOK>
+template <int DT, int FMT, int LG, int TOK, bool SIDE>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
   constexpr int kGroups = kThreads / LG;
   // many rows are written past the caches: 8191 tokens took 32.7 us so and 38.2 with plain stores, four tokens to a workgroup
   constexpr bool kStream = TOK > 1;
   const RopeArgs& a = ka.a;
-  __shared__ float2 s_turn[TOK][kMaxPairs];
-  __shared__ int s_slot[TOK];
+  // a token has two heads at the least, a head 4 LG pairs at the most
+  constexpr int kMost = SIDE ? TOK * kGroups / 2 : TOK;
+  __shared__ float2 s_turn[kMost][4 * LG];
+  __shared__ int s_slot[kMost];
   constexpr bool kCodes = FMT != kNone && FMT != SPA_KV_NATIVE;
   __shared__ uint4 s_vec[kCodes ? kThreads : 1];
   const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
-  const int first = blockIdx.x * TOK, tokens = min(TOK, a.t - first);
+  const int all = SIDE ? ka.rows * TOK : TOK;
+  const int block_first = blockIdx.x * all, block_tokens = min(all, a.t - block_first);
+  const int row = SIDE ? group / ka.heads * TOK : 0;    // this group's first token in the workgroup
+  const int first = block_first + row, tokens = min(TOK, block_tokens - row);
   const int n_heads = a.hq + a.hkv * (FMT == kNone ? 1 : 2);   // queries, keys and, with a cache, values
   const int end = min((int)(blockIdx.y + 1) * ka.heads, n_heads);
   const bool in_head = lane * 8 < a.d, turns = lane * 8 < a.rot;
@@ -144,18 +151,19 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
     }
   };
 
-  int head = blockIdx.y * ka.heads + group;
+  // groups past the last row take no head
+  int head = SIDE ? row < all ? group % ka.heads : end : (int)blockIdx.y * ka.heads + group;
   Eight x[TOK];
   load(head, x);
   const int pairs = a.rot / 2;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < block_tokens * pairs; i += kThreads) {
     const int tok = i / pairs, f = i - tok * pairs;
-    const double turn = (double)a.pos[first + tok] * ((double)a.freq[f] * 0.15915494309189535);
+    const double turn = (double)a.pos[block_first + tok] * ((double)a.freq[f] * 0.15915494309189535);
     float sn, cs;
     sincospif((float)(2.0 * (turn - rint(turn))), &sn, &cs);
     s_turn[tok][f] = make_float2(cs, sn);
   }
-  if (FMT != kNone && (int)threadIdx.x < tokens) s_slot[threadIdx.x] = a.slots[first + threadIdx.x];
+  if (FMT != kNone && (int)threadIdx.x < block_tokens) s_slot[threadIdx.x] = a.slots[block_first + threadIdx.x];
   __syncthreads();
 
   const int q_kind = a.norm[0].kind, k_kind = a.norm[1].kind;
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
       for (int e = 0; e < 8; ++e) wf[e] = 1.f;
 #pragma unroll
     for (int u = 0; u < TOK; ++u) {
-      if (u >= tokens) break;                          // the whole workgroup
+      if (u >= tokens) break;
       if (!value) {
         y[u].pair_up(a.neighbours);
         float v[8];
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
         if (turns) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 cs = s_turn[u][4 * lane + e];
+            const float2 cs = s_turn[row + u][4 * lane + e];
             const float p = v[e], o = v[4 + e];
             v[e] = p * cs.x - o * cs.y;
             v[4 + e] = p * cs.y + o * cs.x;
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(RopeKernelArgs ka) {
       if constexpr (FMT != kNone) {
         if (!key && !value) continue;
         const uint64_t cells = pick(value, k_cells, v_cells);
-        const int slot = s_slot[u], page_size = (int)a.page.d;
+        const int slot = s_slot[row + u], page_size = (int)a.page.d;
         const int pg = slot >= 0 ? (int)a.page.div((uint32_t)slot) : a.n_pages;
         const bool there = slot >= 0 && pg < a.n_pages && in_head;
         const size_t block = (size_t)pg * (uint32_t)a.hkv + h;
@@ -265,13 +273,17 @@ template <int DT, int FMT, int LG>
 hipError_t go(const RopeArgs& a, hipStream_t st) {
   constexpr int kGroups = kThreads / LG;
   const int heads = a.hq + a.hkv * (FMT == kNone ? 1 : 2);
-  RopeKernelArgs ka{a, heads};
+  RopeKernelArgs ka{a, heads, 1};
   if (a.t <= kFewTokens) {
     ka.heads = std::min(heads, kGroups);
     const dim3 grid(a.t, (heads + ka.heads - 1) / ka.heads);
-    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 1>), grid, dim3(kThreads), 0, st, ka);
+    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, 1, false>), grid, dim3(kThreads), 0, st, ka);
   } else {
-    hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, kTokens>), dim3((a.t + kTokens - 1) / kTokens), dim3(kThreads), 0, st, ka);
+    ka.rows = std::max(kGroups / heads, 1);
+    const int tokens = ka.rows * kTokens;
+    const dim3 grid((a.t + tokens - 1) / tokens);
+    if (ka.rows > 1) hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, kTokens, true>), grid, dim3(kThreads), 0, st, ka);
+    else hipLaunchKernelGGL((k_qk_norm_rope<DT, FMT, LG, kTokens, false>), grid, dim3(kThreads), 0, st, ka);
   }
   return hipGetLastError();
 }
