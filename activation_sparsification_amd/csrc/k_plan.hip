@@ -205,7 +205,7 @@ __device__ __forceinline__ void plan(const PlanArgs& a, int count, bool rows, bo
 // it takes 512 sequences at a time, lists those that are over, counts their pages a wave to each, and copies them.  Returns what
 // is free then.
 __device__ __forceinline__ int release(const PlanArgs& a) {
-  constexpr int kLook = 8, kWaves = kThreads / kWave;  // entries of a lane in flight
+  constexpr int kLook = 8, kWaves = kThreads / kWave;
   __shared__ uint32_t s_wave[2][kWaves];
   __shared__ int2 s_list[kThreads];                    // sequence, columns
   __shared__ int s_count[kThreads];
@@ -223,21 +223,62 @@ __device__ __forceinline__ int release(const PlanArgs& a) {
     if (cols > 0) s_list[place] = make_int2(s, cols);
     s_count[tid] = 0;
     __syncthreads();
-    auto walk = [&](int2 e, auto each) {               // each(entry's page, whether it is one)
-      const int32_t* row = a.table + (size_t)e.x * a.max_pages;
-      for (int c = lane; c - lane < e.y; c += kLook * kWave) {
-        int pg[kLook];
+    // A wave's entries, every kWaves-th of the list, 64 columns at a time and kLook of these in flight, whosoever they are:
+    // each(the entry's place in the list, a lane's page, whether it is one, whether the entry's columns end).  69 sequences of one
+    // page that are over, of 345: 14.1 us a call, 21.3 with one entry at a time.
+    auto walk = [&](auto each) {
+      const int n_listed = __builtin_amdgcn_readfirstlane((int)listed);
+      int at = __builtin_amdgcn_readfirstlane(wave), col = 0, seq = 0, cols = 0;
+      auto open = [&] {
+        if (at >= n_listed) return;
+        seq = __builtin_amdgcn_readfirstlane(s_list[at].x);
+        cols = __builtin_amdgcn_readfirstlane(s_list[at].y);
+      };
+      open();
+      while (at < n_listed) {
+        if (cols - col > kWave) {                      // a longer one: all in flight are its
+          int pg[kLook];
+          const int32_t* row = a.table + (size_t)seq * a.max_pages + col + lane;
 #pragma unroll
-        for (int u = 0; u < kLook; ++u) pg[u] = c + u * kWave < e.y ? row[c + u * kWave] : -1;
+          for (int u = 0; u < kLook; ++u) pg[u] = col + u * kWave + lane < cols ? row[u * kWave] : -1;
 #pragma unroll
-        for (int u = 0; u < kLook; ++u) each(pg[u], pg[u] >= 0 && pg[u] < a.n_pages);
+          for (int u = 0; u < kLook; ++u)
+            if (col + u * kWave < cols) each(at, pg[u], pg[u] >= 0 && pg[u] < a.n_pages, col + (u + 1) * kWave >= cols);
+          col += kWave * kLook;
+          if (col >= cols) {
+            at += kWaves;
+            col = 0;
+            open();
+          }
+          continue;
+        }
+        int pg[kLook], of[kLook];
+        bool ends[kLook];
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+          of[u] = at;
+          pg[u] = -1;
+          if (at < n_listed && col + lane < cols) pg[u] = a.table[(size_t)seq * a.max_pages + col + lane];
+          col += kWave;
+          ends[u] = at < n_listed && col >= cols;
+          if (ends[u]) {
+            at += kWaves;
+            col = 0;
+            open();
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kLook; ++u)
+          if (of[u] < n_listed) each(of[u], pg[u], pg[u] >= 0 && pg[u] < a.n_pages, ends[u]);
       }
     };
-    for (int i = wave; i < (int)listed; i += kWaves) {
-      int n = 0;
-      walk(s_list[i], [&](int, bool ok) { n += __popcll(__ballot(ok)); });
-      if (lane == 0) s_count[i] = n;
-    }
+    int n = 0;
+    walk([&](int entry, int, bool ok, bool ends) {
+      n += __popcll(__ballot(ok));
+      if (!ends) return;
+      if (lane == 0) s_count[entry] = n;
+      n = 0;
+    });
     __syncthreads();
     const uint32_t upto = wave_scan_of((uint32_t)s_count[tid], Add{kMost});
     scan_offer<kWaves>(upto, s_wave[1]);
@@ -246,15 +287,14 @@ __device__ __forceinline__ int release(const PlanArgs& a) {
     __syncthreads();
     s_count[tid] = (int)before;
     __syncthreads();
-    for (int i = wave; i < (int)listed; i += kWaves) {
-      int64_t to = (int64_t)count + s_count[i];
-      walk(s_list[i], [&](int pg, bool ok) {
-        const uint64_t there = __ballot(ok);
-        const int64_t mine = to + __popcll(there & ((1ull << lane) - 1));
-        if (ok && mine < a.n_pages) a.stack[mine] = pg;      // a stack holds every page once: it cannot be fuller
-        to += __popcll(there);
-      });
-    }
+    int64_t to = -1;                                   // where the entry's next page goes
+    walk([&](int entry, int pg, bool ok, bool ends) {
+      if (to < 0) to = (int64_t)count + s_count[entry];
+      const uint64_t there = __ballot(ok);
+      const int64_t mine = to + __popcll(there & ((1ull << lane) - 1));
+      if (ok && mine < a.n_pages) a.stack[mine] = pg;        // a stack holds every page once: it cannot be fuller
+      to = ends ? -1 : to + __popcll(there);
+    });
     count = (int)min((int64_t)count + total, (int64_t)a.n_pages);
     __syncthreads();
   }
