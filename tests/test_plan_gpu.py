@@ -312,3 +312,12 @@ def test_replaced_in_part(dev):
         got = dict(zip(NAMES, spa.kv_plan(*args, done=None if done is None else ints(done, dev), **given)))
         for key, x in want.items():
             assert {**got, "table": args[2], "stack": args[4]}[key].tolist() == x, (name, key)
+
+
+def test_lengths_of_ended_requests(dev):
+    # columns that fill a wave's loads, or all that it has in flight, and one more or fewer
+    rng = random.Random(11)
+    lens = [1, 63, 64, 65, 128, 129, 511, 512, 513, 575, 576, 577, 1024, 1088, 0, 2] * 2
+    for gone in (range(32), range(0, 32, 3), [8], [13, 30]):
+        table, stack, count = state(rng, lens, 1, 1100, sum(lens) + 40)
+        run(dev, lens, [1] * 32, table, 1, stack, count, 32, [int(i in gone) for i in range(32)])
