@@ -5,7 +5,10 @@ attention, pruned output projection, gated residual norm, pruned squared-ReLU FF
 different lengths run packed, a second piece of each prompt attends to its cached beginning, and single tokens run
 over the paged cache.  The result of the last token is compared with running every sequence whole.
 
-    python examples/decoder_layer.py --format fp8
+With --rotate queries and keys are normed and turned by their positions on the way to the attention and into the cache;
+with --pool pages come from a stack of free ones, and slots, positions and offsets are made on the GPU.
+
+    python examples/decoder_layer.py --format mxfp4 --rotate --pool
 """
 from __future__ import annotations
 
@@ -22,13 +25,13 @@ import activation_sparsification_amd as spa  # noqa: E402
 class Layer:
     """Weights of one decoder layer and its part of the cache."""
 
-    def __init__(self, g, hidden, ffn, heads, kv_heads, head_dim, n_pages, page, fmt, dtype, dev):
+    def __init__(self, g, hidden, ffn, heads, kv_heads, head_dim, n_pages, page, fmt, dtype, dev, rotate=False):
         def weight(n_out, k):
             w = torch.randn((n_out, k), generator=g, device=dev) * k ** -0.5
             return spa.prepare_weight(w.to(dtype), alpha=0.5)
 
-        def vector(mean, std):
-            return (mean + std * torch.randn(hidden, generator=g, device=dev)).to(dtype)
+        def vector(mean, std, size=hidden):
+            return (mean + std * torch.randn(size, generator=g, device=dev)).to(dtype)
 
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.qkv = weight((heads + 2 * kv_heads) * head_dim, hidden)
@@ -36,6 +39,7 @@ class Layer:
         self.post = [vector(1.0, 0.1) for _ in range(2)]
         self.pre = [vector(1.0, 0.1) for _ in range(2)]
         self.gate = [vector(0.5, 0.1) for _ in range(2)]
+        self.qk = [vector(1.0, 0.1, head_dim) for _ in range(2)] if rotate else None
         self.cache = spa.new_kv_cache(n_pages, page, kv_heads, head_dim, dtype, fmt, dev)
 
 
@@ -43,23 +47,32 @@ class Decoder:
     """Layers, the page tables of a batch of sequences and their lengths."""
 
     def __init__(self, n_seqs, longest, layers=2, hidden=512, ffn=1024, heads=8, kv_heads=2, head_dim=64, page=16,
-                 fmt="native", dtype=torch.bfloat16, dev="cuda", seed=0):
+                 fmt="native", dtype=torch.bfloat16, dev="cuda", seed=0, rotate=False, pool=False):
         g = torch.Generator(device=dev)
         g.manual_seed(seed)
         width = -(-longest // page)
-        self.layers = [Layer(g, hidden, ffn, heads, kv_heads, head_dim, n_seqs * width, page, fmt, dtype, dev)
+        self.layers = [Layer(g, hidden, ffn, heads, kv_heads, head_dim, n_seqs * width, page, fmt, dtype, dev, rotate)
                        for _ in range(layers)]
         # pages in no order, as an allocator hands them out
         self.table = torch.randperm(n_seqs * width, generator=g, device=dev).to(torch.int32).view(n_seqs, width)
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
         self.page, self.hidden, self.dev = page, hidden, dev
+        self.freq = 10000.0 ** (-torch.arange(0, head_dim, 2, device=dev) / head_dim) if rotate else None
+        self.pool = spa.new_page_pool(n_seqs * width, dev) if pool else None
+        if pool:
+            self.table.fill_(-1)
         self.cfg = spa.PruneConfig(8, 16, score="weight", shift="token_mean")
         self.cfg_act = spa.PruneConfig(8, 16, score="weight", shift="token_mean", act="relu2")
 
     def _slots(self, seq, pos):
         return (self.table[seq, pos // self.page].long() * self.page + pos % self.page).to(torch.int32)
 
-    def _run(self, x, slots, attend, linear):
+    def _plan(self, new, t):
+        """Pages for ``new[s]`` more tokens of each sequence: slots, positions, cu_q, cu_k; the lengths move on."""
+        pages, count = self.pool
+        return spa.kv_plan(self.lens, new, self.table, self.page, pages, count, t, lens_out=self.lens, count_out=count)[:4]
+
+    def _run(self, x, pos, slots, attend, linear):
         """Rows x [t, hidden] through every layer; ``attend(layer, q, k, v)`` is the attention of this kind of call."""
         h, y = spa.gated_residual_norm(x, None, pre="rms", pre_weight=self.layers[0].pre[0])
         h = h.float()                                           # the residual stream is kept in float32
@@ -67,7 +80,11 @@ class Decoder:
             qkv, _, _ = linear(y, layer.qkv, self.cfg)
             qkv = qkv.view(x.shape[0], -1, layer.head_dim)
             q, k, v = qkv.split([layer.heads, layer.kv_heads, layer.kv_heads], dim=1)
-            spa.kv_write(k, v, slots, layer.cache)
+            if self.freq is None:
+                spa.kv_write(k, v, slots, layer.cache)
+            else:
+                q, k = spa.qk_norm_rope(q, k, pos, self.freq, q_weight=layer.qk[0], k_weight=layer.qk[1], q_out=q, k_out=k, v=v,
+                                        slots=slots, cache=layer.cache)
             a = attend(layer, q, k, v)
             o, _, _ = linear(a.view(x.shape[0], -1), layer.out, self.cfg)
             h, y = spa.gated_residual_norm(o, h, post="rms", post_weight=layer.post[0], gate=layer.gate[0], scale=0.5,
@@ -82,40 +99,46 @@ class Decoder:
     def prompt(self, x, new):
         """The next ``new[s]`` tokens of each sequence, packed in x; what is cached already is attended to."""
         new = torch.tensor(new, dtype=torch.int32, device=self.dev)
-        cu_q = torch.nn.functional.pad(new.cumsum(0), (1, 0)).to(torch.int32)
-        have = self.lens + new
-        cu_k = torch.nn.functional.pad(have.cumsum(0), (1, 0)).to(torch.int32)
-        seq = torch.repeat_interleave(torch.arange(len(new), device=self.dev), new.long())
-        pos = torch.arange(x.shape[0], device=self.dev) - cu_q[:-1].long()[seq] + self.lens.long()[seq]
-        total, fresh = int(cu_k[-1]), not bool(self.lens.any())
+        fresh = not bool(self.lens.any())
+        if self.pool:
+            slots, pos, cu_q, cu_k = self._plan(new, x.shape[0])
+        else:
+            slots, pos, cu_q, cu_k = self._offsets(new, x.shape[0])
+        total = int(cu_k[-1])
 
         def attend(layer, q, k, v):
             if not fresh:                                       # the cached beginning and the new piece, as dense rows
                 k, v = spa.kv_read(layer.cache, self.table, cu_k, total, dtype=q.dtype)
             return spa.attention_prefill(q, k, v, cu_q, cu_q if fresh else cu_k)[0]
 
-        y = self._run(x, self._slots(seq, pos), attend, spa.sparse_linear_prefill)
+        return self._run(x, pos, slots, attend, spa.sparse_linear_prefill)
+
+    def _offsets(self, new, t):
+        """What ``_plan`` gives, in torch operations over a table that is filled from the start."""
+        cu_q = torch.nn.functional.pad(new.cumsum(0), (1, 0)).to(torch.int32)
+        have = self.lens + new
+        cu_k = torch.nn.functional.pad(have.cumsum(0), (1, 0)).to(torch.int32)
+        seq = torch.repeat_interleave(torch.arange(len(new), device=self.dev), new.long())
+        pos = torch.arange(t, device=self.dev) - cu_q[:-1].long()[seq] + self.lens.long()[seq]
         self.lens = have
-        return y
+        return self._slots(seq, pos), pos.to(torch.int32), cu_q, cu_k
 
     def step(self, x):
         """One new token of each sequence, x [n_seqs, hidden] (up to 32 sequences)."""
-        slots = self._slots(torch.arange(x.shape[0], device=self.dev), self.lens.long())
-        lens = self.lens + 1
+        new = torch.ones(x.shape[0], dtype=torch.int32, device=self.dev)
+        slots, pos = (self._plan if self.pool else self._offsets)(new, x.shape[0])[:2]
 
         def attend(layer, q, k, v):
-            return spa.attention_decode(q, layer.cache, self.table, lens)[0]
+            return spa.attention_decode(q, layer.cache, self.table, self.lens)[0]
 
-        y = self._run(x, slots, attend, spa.sparse_linear_decode)
-        self.lens = lens
-        return y
+        return self._run(x, pos, slots, attend, spa.sparse_linear_decode)
 
 
-def compare(fmt="native", lens=(70, 33, 129), pieces=20, steps=3, seed=0):
+def compare(fmt="native", lens=(70, 33, 129), pieces=20, steps=3, seed=0, rotate=False, pool=False):
     """The last token's outputs after prompts, second pieces and single tokens, and after whole prompts: their relative
     difference in the 2-norm, one number per sequence."""
     longest = max(lens) + pieces + steps
-    args = dict(n_seqs=len(lens), longest=longest, fmt=fmt, seed=seed)
+    args = dict(n_seqs=len(lens), longest=longest, fmt=fmt, seed=seed, rotate=rotate, pool=pool)
     a, b = Decoder(**args), Decoder(**args)
     g = torch.Generator(device="cuda")
     g.manual_seed(seed + 1)
@@ -132,10 +155,12 @@ def compare(fmt="native", lens=(70, 33, 129), pieces=20, steps=3, seed=0):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("--format", choices=["native", "fp8", "int8"], default="native", help="how the cache holds vectors")
+    ap.add_argument("--format", choices=["native", "fp8", "int8", "mxfp4"], default="native", help="how the cache holds vectors")
     ap.add_argument("--steps", type=int, default=3, help="single tokens after the prompts")
+    ap.add_argument("--rotate", action="store_true", help="norm and turn queries and keys")
+    ap.add_argument("--pool", action="store_true", help="pages from a pool, planned on the GPU")
     args = ap.parse_args()
-    got = compare(args.format, steps=args.steps)
+    got = compare(args.format, steps=args.steps, rotate=args.rotate, pool=args.pool)
     print(f"cache {args.format}: last token against whole prompts, relative difference "
           + ", ".join(f"{x:.2e}" for x in got))
 
