@@ -13,6 +13,9 @@
 //         code has two significant bits), pairs of positions brought together by byte permutes.  Softmax weights are
 //         rounded to bfloat16, for a float16 call taken as two bfloat16 numbers in two products (16 bits; bfloat16 keeps
 //         the scales' range).
+//
+// 64 ragged sequences of up to 8191 positions by 8 heads of 128: 51 us with the join, 4.8 TB/s; two of 200003 79 us, 5.5 TB/s (a
+// stream that is only read reaches 7.2); one of 61 5.7 us.
 #include "spa_attn_decode.h"
 
 namespace spa {
