@@ -321,6 +321,10 @@ __global__ void __launch_bounds__(kWaves * kWave, DP <= 128 ? 2 : 1) k_attention
   }
 }
 
+// A cached row: of the kernel's DP dimensions; of whole 16-byte lanes (a multiple of 32 dimensions; 12 + 2 heads of 192 28.0 -> 25.0 us, eight
+// short sequences by 16 + 4 of 96 9.7 -> 8.5); of 4-byte words.
+constexpr int kFull = 0, kLines = 1, kWordsOnly = 2;
+
 // A table entry that a whole wave reads, by the scalar unit: nothing writes the table during the call.
 typedef const __attribute__((address_space(4))) int32_t* table_ptr;
 
@@ -348,11 +352,11 @@ template <int DP, int PACK> constexpr int kBlockWaves = DP == 256 && PACK > 1 ? 
 template <int DP, int PACK> constexpr int kSimdWaves = (DP == 64 ? 3 : DP == 128 ? 2 : 1) * kBlockWaves<DP, PACK> / 4;
 
 // Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave shares.
-// EXACT: head_dim is DP; else pieces past it are not read and count as zeros.  Two tiles are on their way while one is worked
+// ROW: other than kFull, pieces past head_dim are not read and count as zeros.  Two tiles are on their way while one is worked
 // on, and the page numbers of the next one; at the end of a piece they are the next piece's.  Every load of the loop is issued
 // whatever the tile (past the last one it is read again): a load that only some rounds issue would make the waits drain all
 // of them.
-template <int DT, int DP, bool EXACT, int PACK>
+template <int DT, int DP, int ROW, int PACK>
 __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<DP, PACK>)) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
   constexpr int kWaves = kBlockWaves<DP, PACK>;
   constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = Query<DP, PACK>::KS;
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, g = lane >> 4;
   const int kg = DP == 64 ? g & 1 : g;                       // this lane's 32 dimensions of a k step
-  const int d = EXACT ? DP : a.d, bytes = d / 2, groups = (d + kGroup - 1) / kGroup, page = (int)a.page.d;
-  const bool in_row = EXACT || NV * col < d;
+  const int d = ROW == kFull ? DP : a.d, bytes = d / 2, groups = (d + kGroup - 1) / kGroup, page = (int)a.page.d;
+  const bool in_row = ROW == kFull || NV * col < d;
   const uint32_t k_at = (uint32_t)(col * bytes + 16 * kg), ks_at = (uint32_t)(kg * page + col);
   const uint32_t v_at = (uint32_t)(4 * g * bytes), vs_at = (uint32_t)((in_row ? NV * col / kGroup : 0) * page + 4 * g);
   // Of the workgroups on a unit the one that came first is served first, and the later ones end after it, alone: 66 and 79 us of a
@@ -401,12 +405,17 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
       const uint8_t *ks = static_cast<const uint8_t*>(a.k_scale) + scales, *vs = static_cast<const uint8_t*>(a.v_scale) + scales;
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
-        if constexpr (EXACT) {
+        if constexpr (ROW == kFull) {
           x.k[b][c] = stream_load16(k + (k_at + 64 * c));
           x.ks[b][c] = ks[ks_at + (uint32_t)(4 * c * page)];
         } else {
           const int from = 64 * c + 16 * kg;
-          x.k[b][c] = load_codes(k + (k_at + 64 * c), bytes - from);
+          if constexpr (ROW == kLines) {
+            x.k[b][c] = make_uint4(0, 0, 0, 0);
+            if (from < bytes) x.k[b][c] = stream_load16(k + (k_at + 64 * c));
+          } else {
+            x.k[b][c] = load_codes(k + (k_at + 64 * c), bytes - from);
+          }
           x.ks[b][c] = from < bytes ? ks[ks_at + (uint32_t)(4 * c * page)] : 127;
         }
       }
@@ -513,8 +522,9 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
 template <int DT, int DP, int PACK>
 void launch_blocks(const DecodeAttnArgs& a, dim3 grid, hipStream_t st) {
   const dim3 block(kBlockWaves<DP, PACK> * kWave);
-  if (a.d == DP) hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, true, PACK>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, false, PACK>), grid, block, 0, st, a);
+  if (a.d == DP) hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, kFull, PACK>), grid, block, 0, st, a);
+  else if (a.d % 32 == 0) hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, kLines, PACK>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_attention_decode_mx_blocks<DT, DP, kWordsOnly, PACK>), grid, block, 0, st, a);
 }
 template <int DT, int DP>
 hipError_t go(DecodeAttnArgs a, hipStream_t st) {

@@ -444,3 +444,22 @@ def test_calls_on_two_streams(dev):
     torch.cuda.synchronize()
     for w, all_of in zip(want, got):
         assert all(torch.equal(w, x) for x in all_of)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 96), (20, 1, 64), (2, 2, 256)])
+def test_nonfinite_queries_stay_by_themselves(dev, hq, hkv, d):
+    # a head's query pieces stand beside the other heads' in the matrix product
+    g = gen(dev, 12)
+    lens = [700, 40, 33, 1]
+    for page in (16, 20):
+        cache = spa.new_kv_cache(200, page, hkv, d, BF16, "mxfp4", dev)
+        M.fill(cache, g, BF16)
+        table = table_for(dev, g, lens, page, 200)
+        ln = torch.tensor(lens, dtype=I32, device=dev)
+        q = torch.randn((4, hq, d), generator=g, device=dev).to(BF16)
+        want = spa.attention_decode(q, cache, table, ln)[0]
+        q[0, hq - 1, 3], q[1, 0, d - 1], q[3, 1, d // 2] = math.nan, math.inf, -math.inf
+        got = spa.attention_decode(q, cache, table, ln)[0]
+        hit = torch.zeros((4, hq), dtype=torch.bool, device=dev)
+        hit[0, hq - 1] = hit[1, 0] = hit[3, 1] = True
+        assert torch.equal(got[~hit], want[~hit]) and torch.isnan(got[hit]).all()
