@@ -321,8 +321,7 @@ __global__ void __launch_bounds__(kWaves * kWave, DP <= 128 ? 2 : 1) k_attention
   }
 }
 
-// A cached row: of the kernel's DP dimensions; of whole 16-byte lanes (a multiple of 32 dimensions; 12 + 2 heads of 192 28.0 -> 25.0 us, eight
-// short sequences by 16 + 4 of 96 9.7 -> 8.5); of 4-byte words.
+// A cached row: of the kernel's DP dimensions; of whole 16-byte lanes (a multiple of 32 dimensions); of 4-byte words.
 constexpr int kFull = 0, kLines = 1, kWordsOnly = 2;
 
 // A table entry that a whole wave reads, by the scalar unit: nothing writes the table during the call.
@@ -347,17 +346,19 @@ __device__ __forceinline__ Walk walk_of(const DecodeAttnArgs& a, const Piece& p,
 }
 
 // Waves of a workgroup, and of a SIMD as the registers allow: the workgroups of a compute unit (three, two or one, by the head's
-// dimensions) fill it.
+// dimensions) fill it.  The division counts two for 128 dimensions also where the registers leave room for three: they serve
+// calls of more workgroups (128 sequences of up to 500 by 20 heads 41.5 -> 34.1 us).
 template <int DP, int PACK> constexpr int kBlockWaves = DP == 256 && PACK > 1 ? 8 : 4;
-template <int DP, int PACK> constexpr int kSimdWaves = (DP == 64 ? 3 : DP == 128 ? 2 : 1) * kBlockWaves<DP, PACK> / 4;
+template <int DP, int ROW, int PACK>
+constexpr int kSimdWaves = (DP == 64 || (DP == 128 && ROW == kFull && PACK == 4) ? 3 : DP == 128 ? 2 : 1) * kBlockWaves<DP, PACK> / 4;
 
 // Pages of whole 16-position blocks: a block's rows are consecutive, so a tile has two bases that the whole wave shares.
-// ROW: other than kFull, pieces past head_dim are not read and count as zeros.  Two tiles are on their way while one is worked
+// ROW: other than kFull, what lies past head_dim meets zeros of the query or is not written.  Two tiles are on their way while one is worked
 // on, and the page numbers of the next one; at the end of a piece they are the next piece's.  Every load of the loop is issued
 // whatever the tile (past the last one it is read again): a load that only some rounds issue would make the waits drain all
 // of them.
 template <int DT, int DP, int ROW, int PACK>
-__global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<DP, PACK>)) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
+__global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<DP, ROW, PACK>)) k_attention_decode_mx_blocks(DecodeAttnArgs a) {
   constexpr int kWaves = kBlockWaves<DP, PACK>;
   constexpr int NV = DP / 16, VW = NV > 8 ? NV / 8 : 1, KS = Query<DP, PACK>::KS;
   const int lane = threadIdx.x & (kWave - 1);
@@ -367,7 +368,13 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
   const int d = ROW == kFull ? DP : a.d, bytes = d / 2, groups = (d + kGroup - 1) / kGroup, page = (int)a.page.d;
   const bool in_row = ROW == kFull || NV * col < d;
   const uint32_t k_at = (uint32_t)(col * bytes + 16 * kg), ks_at = (uint32_t)(kg * page + col);
-  const uint32_t v_at = (uint32_t)(4 * g * bytes), vs_at = (uint32_t)((in_row ? NV * col / kGroup : 0) * page + 4 * g);
+  const uint32_t vs_at = (uint32_t)((in_row ? NV * col / kGroup : 0) * page + 4 * g);
+  uint32_t v_at[VW];                   // this lane's dimensions; past the row's end they are not written, whatever was read
+#pragma unroll
+  for (int i = 0; i < VW; ++i) {
+    const int at = NV / 2 * col + 4 * i;
+    v_at[i] = (uint32_t)(4 * g * bytes + (ROW == kFull ? at : min(at, bytes - (NV == 4 ? 2 : 4))));
+  }
   // Of the workgroups on a unit the one that came first is served first, and the later ones end after it, alone: 66 and 79 us of a
   // call of 82.  The n-th to come (from 0) therefore goes first for n / (n + 1) of a piece, and they end together (two sequences of
   // 200003 81.3 -> 78.2 us, 64 ragged ones of up to 8191 53.3 -> 51.9, two of 100000 by 20 heads 118.4 -> 113.0; one workgroup
@@ -409,18 +416,34 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
           x.k[b][c] = stream_load16(k + (k_at + 64 * c));
           x.ks[b][c] = ks[ks_at + (uint32_t)(4 * c * page)];
         } else {
+          // past the row's end the query is 0, and any codes will do: 32 ragged sequences of up to 8000 by 16 + 4 heads of 96 take
+          // 21.7 us so, 26.7 with lanes that read nothing
           const int from = 64 * c + 16 * kg;
+          const uint32_t row = (uint32_t)(col * bytes);
           if constexpr (ROW == kLines) {
-            x.k[b][c] = make_uint4(0, 0, 0, 0);
-            if (from < bytes) x.k[b][c] = stream_load16(k + (k_at + 64 * c));
+            x.k[b][c] = stream_load16(k + (row + (uint32_t)min(from, bytes - 16)));
           } else {
-            x.k[b][c] = load_codes(k + (k_at + 64 * c), bytes - from);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(k + (row + (uint32_t)min(from + 4 * i, bytes - 4)));
+            x.k[b][c] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          x.ks[b][c] = from < bytes ? ks[ks_at + (uint32_t)(4 * c * page)] : 127;
+          x.ks[b][c] = ks[(uint32_t)(min(4 * c + kg, groups - 1) * page + col)];
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) load_value<NV>(v + (v_at + (uint32_t)(r * bytes)), col, bytes, in_row, x.v[4 * b + r]);
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (ROW == kFull) {
+          load_value<NV>(v + ((uint32_t)(4 * g * bytes) + (uint32_t)(r * bytes)), col, bytes, true, x.v[4 * b + r]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            const char* from = v + (v_at[i] + (uint32_t)(r * bytes));
+            if constexpr (NV == 4) x.v[4 * b + r][i] = *reinterpret_cast<const uint16_t*>(from);
+            else x.v[4 * b + r][i] = *reinterpret_cast<const uint32_t*>(from);
+          }
+        }
+      }
       x.vs[b] = *reinterpret_cast<const uint32_t*>(vs + vs_at);
     }
   };
@@ -483,7 +506,10 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
           float t[8], vs[8], w[8];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const f32x4 s = scores<DP, PACK>(x[u].k[b], x[u].ks[b], qp);
+            int unit[KS];
+#pragma unroll
+            for (int c = 0; c < KS; ++c) unit[c] = ROW != kFull && 64 * c + 16 * kg >= bytes ? 127 : x[u].ks[b][c];
+            const f32x4 s = scores<DP, PACK>(x[u].k[b], ROW == kFull ? x[u].ks[b] : unit, qp);
 #pragma unroll
             for (int r = 0; r < 4; ++r) t[4 * b + r] = s[r];
           }
