@@ -10,12 +10,13 @@
 //         aligns the products of 16 elements to the largest and drops what is 2^-14 of it, which a plain split of the
 //         queries into e4m3 numbers loses bits to.  Four pieces hold an element to 2^-19 of the largest.
 //   O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: values are unpacked, with their scales, by v_cvt_scalef32_pk_bf16_fp4 (exact: a
-//         code has two significant bits), pairs of positions brought together by byte permutes.  Softmax weights are
-//         rounded to bfloat16, for a float16 call taken as two bfloat16 numbers in two products (16 bits; bfloat16 keeps
-//         the scales' range).
+//         code has two significant bits), pairs of positions brought together by byte permutes.  A softmax weight is taken as
+//         two bfloat16 numbers in two products (16 bits, and bfloat16 has the scales' range).  One, its 8 bits, would be off by
+//         more than the rounding of a bfloat16 output where values cancel, and save 2 to 8 % (64 ragged sequences of up to
+//         8191 52.4 -> 50.6 us, 32 of up to 8000 by 16 + 4 heads of 96 23.7 -> 21.9).
 //
-// 64 ragged sequences of up to 8191 positions by 8 heads of 128: 51 us with the join, 4.8 TB/s; two of 200003 79 us, 5.5 TB/s (a
-// stream that is only read reaches 7.2); one of 61 5.7 us.
+// 64 ragged sequences of up to 8191 positions by 8 heads of 128: 52 us with the join, 4.7 TB/s; two of 200003 79 us, 5.5 TB/s (a
+// stream that is only read reaches 7.2); one of 61 6 us.
 #include "spa_attn_decode.h"
 
 namespace spa {
@@ -175,20 +176,21 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
 }
 
-// Adds this lane's 8 positions to o.  raw: their value rows' codes, NV dimensions each; w: their softmax weights.
-template <int DT, int NV>
+// Adds this lane's 8 positions to o.  raw: their value rows' codes, NV dimensions each; w: their softmax weights, each cut into
+// a bfloat16 number and what that leaves.
+template <int NV>
 __device__ __forceinline__ void add_values(const uint32_t (&raw)[8][NV > 8 ? NV / 8 : 1], const float (&vs)[8], const float (&w)[8],
                                            f32x4 (&o)[NV]) {
-  uint4 pf[DT == SPA_F16 ? 2 : 1];
+  uint4 pf[2];
   {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       hi[j] = pack2<SPA_BF16>(w[2 * j], w[2 * j + 1]);
-      if constexpr (DT == SPA_F16) lo[j] = pack2<SPA_BF16>(w[2 * j] - bf16_to_f32(hi[j] & 0xFFFFu), w[2 * j + 1] - bf16_to_f32(hi[j] >> 16));
+      lo[j] = pack2<SPA_BF16>(w[2 * j] - bf16_to_f32(hi[j] & 0xFFFFu), w[2 * j + 1] - bf16_to_f32(hi[j] >> 16));
     }
     pf[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (DT == SPA_F16) pf[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    pf[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 #pragma unroll
   for (int i = 0; i < NV / 2; ++i) {
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kWaves * kWave, DP <= 128 ? 2 : 1) k_attention
         load_value<NV>(static_cast<const char*>(a.v) + (vb * page + vo) * bytes, col, bytes, live, raw[j]);
         vs[j] = live ? scale_of(v_scale[(vb * groups + NV * col / kGroup) * page + vo], 0) : 1.f;
       }
-      add_values<DT, NV>(raw, vs, w, o);
+      add_values<NV>(raw, vs, w, o);
     }
     finish<DT, DP, false>(a, p, o, 1.f, m * a.c, l);
     if (span.left <= 0) break;
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__((kBlockWaves<DP, PACK> * kWave), (kSimdWaves<D
               }
           }
           softmax_step<NV>(t, a.c, m, l, o, w);
-          add_values<DT, NV>(x[u].v, vs, w, o);
+          add_values<NV>(x[u].v, vs, w, o);
         }
         Walk from;
         int place = source(it + 2, from);

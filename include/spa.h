@@ -404,9 +404,9 @@ size_t spa_workspace_bytes(int32_t entry, int32_t t, int32_t k, int32_t n_out, i
  * One value is rounded to the vectors' 16-bit type on the way: a softmax
  * weight (with an 8-bit cache, times its value's scale) where it meets the
  * values in the matrix product.  The sum that divides is of the unrounded
- * weights.  Over a 4-bit cache the weight of a float16 call keeps 16 bits
- * instead (two bfloat16 numbers), and a query element is taken to 2^-19 of
- * the largest of its 32 (elements 0..31, 32..63, ... of its head).
+ * weights.  Over a 4-bit cache the weight keeps 16 bits instead (two
+ * bfloat16 numbers), and a query element is taken to 2^-19 of the largest of
+ * its 32 (elements 0..31, 32..63, ... of its head).
  * ------------------------------------------------------------------------ */
 enum { SPA_KV_NATIVE = 0, SPA_KV_FP8 = 1, SPA_KV_INT8 = 2, SPA_KV_MXFP4 = 3 };
 enum { SPA_NORM_NONE = 0, SPA_NORM_RMS = 1, SPA_NORM_LAYER = 2 };
