@@ -224,10 +224,57 @@ inline bool apart(const spa_heads* h, int64_t rows, int64_t heads, int64_t d) {
   return rows <= 1 || heads <= 1 || h->row_stride >= (heads - 1) * h->head_stride + d ||
          h->head_stride >= (rows - 1) * h->row_stride + d;
 }
-// Written where it was read, each vector is its own; written elsewhere, it lies anywhere.
-inline bool in_place(const spa_heads* to, const spa_heads* from, int64_t rows, int64_t heads) {
-  return to->data != from->data || ((rows <= 1 || to->row_stride == from->row_stride) && (heads <= 1 || to->head_stride == from->head_stride));
+// Memory that a call reads or writes: rows x heads vectors of `bytes`, `row` and `head` bytes apart (0 where there is one).
+struct Vectors {
+  uintptr_t at, end;           // the first vector's address and where the last one ends
+  int64_t rows, heads, row, head, bytes;
+};
+// A stride of 0 gives the same vectors again.
+inline Vectors vectors(const spa_heads* h, int64_t rows, int64_t heads, int64_t d) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(h->data);
+  const int64_t row = rows > 1 ? 2 * h->row_stride : 0, head = heads > 1 ? 2 * h->head_stride : 0;
+  return Vectors{at, at + (uintptr_t)((rows - 1) * row + (heads - 1) * head + 2 * d), row ? rows : 1, head ? heads : 1, row, head, 2 * d};
 }
+inline Vectors block(const void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return Vectors{at, at + (uintptr_t)bytes, 1, 1, 0, 0, bytes};
+}
+constexpr Vectors kNoVectors{0, 0, 1, 1, 0, 0, 0};
+inline bool same(const Vectors& a, const Vectors& b) {
+  return a.at == b.at && a.rows == b.rows && a.heads == b.heads && a.row == b.row && a.head == b.head;
+}
+inline bool ranges_meet(const Vectors& a, const Vectors& b) { return a.at < b.end && b.at < a.end; }
+// Whether a vector of a and one of b share a byte, where their ranges meet.  Views of one packed projection have their rows side
+// by side; others are gone through head by head.  Where both have several rows at different strides, they count as sharing.
+inline bool vectors_meet(const Vectors& a, const Vectors& b) {
+  if (!a.bytes || !b.bytes) return false;
+  const int64_t a_row = (a.heads - 1) * a.head + a.bytes, b_row = (b.heads - 1) * b.head + b.bytes;
+  if (a.rows > 1 && b.rows > 1 && a.row != b.row) return true;
+  const int64_t row = a.rows > 1 ? a.row : b.row, from = (int64_t)(a.at - b.at);
+  if (row) {
+    const int64_t past = from % row, on = past > 0 ? row - past : -past;      // b's row begins so far behind one of a's
+    if (a_row <= on && on + b_row <= row) return false;
+  }
+  // x: from a head of b to one of a in the same row.  Rows r apart are at x + r row, r from 1 - b.rows to a.rows - 1.
+  auto meet = [&](int64_t x) {
+    if (!row) return -a.bytes < x && x < b.bytes;
+    const int64_t over = -a.bytes - x;                // r row has to be more than this
+    int64_t r = over / row - (over % row < 0) + 1;
+    if (r < 1 - b.rows) r = 1 - b.rows;
+    return r < a.rows && x + r * row < b.bytes;
+  };
+  if (a.heads > 1 && b.heads > 1 && a.head != b.head) {
+    for (int64_t i = 0; i < a.heads; ++i)
+      for (int64_t j = 0; j < b.heads; ++j)
+        if (meet(from + i * a.head - j * b.head)) return true;
+    return false;
+  }
+  const int64_t head = a.heads > 1 ? a.head : b.head;
+  for (int64_t h = 1 - b.heads; h < a.heads; ++h)
+    if (meet(from + h * head)) return true;
+  return false;
+}
+inline bool overlap(const Vectors& a, const Vectors& b) { return ranges_meet(a, b) && vectors_meet(a, b); }
 inline bool valid_norm(const spa_norm* n) {
   return !n || (n->kind >= SPA_NORM_NONE && n->kind <= SPA_NORM_LAYER);
 }
@@ -258,15 +305,49 @@ inline spa_status check_qk_norm_rope(const spa_heads* q, const spa_heads* k, con
   if (c ? !v || !valid_heads(v) || !valid_strides(v) || !slots : !k_out) return SPA_ERR_INVALID;
   if (k_out && (!valid_heads(k_out) || !valid_strides(k_out) || !apart(k_out, t, n_kv_heads, head_dim))) return SPA_ERR_INVALID;
   if (!apart(q_out, t, n_q_heads, head_dim)) return SPA_ERR_INVALID;
-  // in place means vector by vector
-  if (k_out && k_out->data == q_out->data) return SPA_ERR_INVALID;
-  if (q_out->data == k->data || (k_out && k_out->data == q->data)) return SPA_ERR_INVALID;
-  if (!in_place(q_out, q, t, n_q_heads) || (k_out && !in_place(k_out, k, t, n_kv_heads))) return SPA_ERR_INVALID;
-  if (c && (q_out->data == v->data || (k_out && k_out->data == v->data))) return SPA_ERR_INVALID;
   if (s != SPA_OK) return s;
   for (const spa_heads* h : {q, k, q_out, c ? v : q, k_out ? k_out : q})
     if (!built_heads(h)) return SPA_ERR_UNSUPPORTED;
-  return (int64_t)t * (n_q_heads + 2 * n_kv_heads) <= kMaxVectors ? SPA_OK : SPA_ERR_UNSUPPORTED;
+  if ((int64_t)t * (n_q_heads + 2 * n_kv_heads) > kMaxVectors) return SPA_ERR_UNSUPPORTED;
+  // What is written lies apart from everything else, but for vectors that are written where they were read: workgroups take their
+  // heads and rows in any order, and read ahead.
+  const Vectors from_q = vectors(q, t, n_q_heads, head_dim), from_k = vectors(k, t, n_kv_heads, head_dim);
+  const Vectors to_q = vectors(q_out, t, n_q_heads, head_dim);
+  const Vectors to_k = k_out ? vectors(k_out, t, n_kv_heads, head_dim) : kNoVectors;
+  Vectors out[6], in[10];
+  out[0] = to_q, out[1] = to_k, in[0] = from_q, in[1] = from_k;
+  int outs = 2, ins = 2;
+  if (rot) {
+    in[ins++] = block(positions, (int64_t)4 * t);
+    in[ins++] = block(rope->inv_freq, (int64_t)2 * rot);
+  }
+  for (const spa_norm* n : {q_norm, k_norm}) {
+    if (!n || n->kind == SPA_NORM_NONE) continue;
+    if (n->weight) in[ins++] = block(n->weight, (int64_t)2 * head_dim);
+    if (n->bias) in[ins++] = block(n->bias, (int64_t)2 * head_dim);
+  }
+  if (c) {
+    in[ins++] = vectors(v, t, n_kv_heads, head_dim);
+    in[ins++] = block(slots, (int64_t)4 * t);
+    const int64_t cells = (int64_t)c->n_pages * c->n_heads * c->page_size;
+    const int64_t codes = cells * head_dim / 2 * (c->format == SPA_KV_NATIVE ? 4 : c->format == SPA_KV_MXFP4 ? 1 : 2);
+    out[outs++] = block(c->k, codes);
+    out[outs++] = block(c->v, codes);
+    if (c->format != SPA_KV_NATIVE) {
+      const int64_t scales = cells * (c->format == SPA_KV_MXFP4 ? (head_dim + 31) / 32 : 4);
+      out[outs++] = block(c->k_scale, scales);
+      out[outs++] = block(c->v_scale, scales);
+    }
+  }
+  for (int o = 0; o < outs; ++o) {
+    for (int i = 0; i < ins; ++i) {
+      const bool in_place = o == i && o < 2 && same(out[o], in[i]);
+      if (!in_place && overlap(out[o], in[i])) return SPA_ERR_INVALID;
+    }
+    for (int x = 0; x < o && x < 2; ++x)
+      if (overlap(out[o], out[x])) return SPA_ERR_INVALID;
+  }
+  return SPA_OK;
 }
 
 // ---- norms ----

@@ -641,10 +641,12 @@ spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t 
  *  positions [device] [t] int32, any value (NULL without rotation)
  *  rope      NULL, or rotary_dim 0, for no rotation
  *  q_norm, k_norm  NULL: SPA_NORM_NONE
- *  q_out, k_out  where the vectors go (written through `data`; no two of them
- *            may overlap); may be q and k themselves, vector by vector, and
- *            otherwise must not overlap any input.  k_out may be NULL with a
- *            cache
+ *  q_out, k_out  where the vectors go (written through `data`); may be q and
+ *            k themselves, vector by vector.  k_out may be NULL with a cache.
+ *            A vector that is written must not overlap another one, the cache
+ *            or any other input: SPA_ERR_INVALID.  Views of one buffer with
+ *            equal row strides are told apart vector by vector; with others
+ *            the memory from their first vector to their last counts
  *  v, slots, cache  NULL, or: k's result and v's vectors are stored at the
  *            slots [t], just as spa_kv_write(k_out, v, ...) would store them
  *            (cache->dtype is dtype; its heads and head_dim are k's)
