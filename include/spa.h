@@ -634,8 +634,9 @@ spa_status gated_residual_norm(const void* x, int32_t dtype, int32_t t, int32_t 
  *   inv_freq[i]:  y_a = u_a cos p - u_b sin p,  y_b = u_a sin p + u_b cos p;
  *   the elements from rotary_dim on are y = u.
  * Float32 between input and output.  The angle is formed in float64 and its
- * whole turns taken off there, so far positions keep their precision: 2^-21
- * of a radian at any position times frequency below 2^31.
+ * whole turns taken off there, so far positions keep their precision: sine
+ * and cosine are those of an angle within 2^-21 + 2^-51 |position *
+ * inv_freq[i]| of a radian.
  *  q, k      t rows of n_q_heads and n_kv_heads vectors of dtype (SPA_F16 or
  *            SPA_BF16)
  *  positions [device] [t] int32, any value (NULL without rotation)
