@@ -6,9 +6,10 @@
 //         a lane's 16 bytes of a cached row and the scale byte beside them, as they are.  The B operand, the queries, is
 //         e4m3, cut into pieces that together hold them: of each 32 elements (the operand's own blocks) the largest is
 //         brought below 16, and a piece is the nearest integer, the next one 32 times what is left.  Integers up to 16
-//         times codes up to 6 are whole multiples of one half below 2^7, so a product of 128 elements is exact: the unit
-//         aligns the products of 16 elements to the largest and drops what is 2^-14 of it, which a plain split of the
-//         queries into e4m3 numbers loses bits to.  Four pieces hold an element to 2^-19 of the largest.
+//         times codes up to 6 are whole multiples of one half below 2^7, so the sum over 32 elements, which share the query's
+//         scale and the key's, is exact: the unit aligns the products of 16 elements to the largest and drops what is 2^-14 of
+//         it, which a plain split of the queries into e4m3 numbers loses bits to.  Blocks of 32 and pieces are added in
+//         float32.  Four pieces hold an element to 2^-19 of the largest.
 //   O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: values are unpacked, with their scales, by v_cvt_scalef32_pk_bf16_fp4 (exact: a
 //         code has two significant bits), pairs of positions brought together by byte permutes.  A softmax weight is taken as
 //         two bfloat16 numbers in two products (16 bits, and bfloat16 has the scales' range).  One, its 8 bits, would be off by
