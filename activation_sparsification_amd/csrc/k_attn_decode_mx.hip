@@ -13,11 +13,12 @@
 //   O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: values are unpacked, with their scales, by v_cvt_scalef32_pk_bf16_fp4 (exact: a
 //         code has two significant bits), pairs of positions brought together by byte permutes.  A softmax weight is taken as
 //         two bfloat16 numbers in two products (16 bits, and bfloat16 has the scales' range).  One, its 8 bits, would be off by
-//         more than the rounding of a bfloat16 output where values cancel, and save 2 to 8 % (64 ragged sequences of up to
+//         more than the rounding of a bfloat16 output where values cancel, and save 1 to 8 % (64 ragged sequences of up to
 //         8191 52.4 -> 50.6 us, 32 of up to 8000 by 16 + 4 heads of 96 23.7 -> 21.9).
 //
 // 64 ragged sequences of up to 8191 positions by 8 heads of 128: 52 us with the join, 4.7 TB/s; two of 200003 79 us, 5.5 TB/s (a
-// stream that is only read reaches 7.2); one of 61 6 us.
+// stream that is only read reaches 7.2); one of 61 5.6 us.  The choices below
+// were timed with a bfloat16 call's weights in one product.
 #include "spa_attn_decode.h"
 
 namespace spa {
@@ -30,7 +31,9 @@ constexpr int kGroup = 32;           // elements of one scale
 // What beginning a sequence costs a workgroup, in tiles: its query, the first loads' way, the join of the waves.  64 ragged
 // sequences of up to 8191 positions: 57.7 us without it, 54.8 with 6, 52.5 with 10 to 16; 40 of up to 1500: 23.5, 19.1, 18.6.
 constexpr int kStart = 12;
-// Tables of up to so many tiles to a sequence: a workgroup takes a sequence whole, and there is no join.  With 8 heads of 128, one
+// Tables of up to so many tiles to a sequence: a workgroup takes a sequence whole, and there is no join.  The table's width
+// decides, not the lengths in it, which the host does not know: in tables four times as wide one sequence of 500 takes 10.6 us
+// instead of 7.9, 128 of up to 500 by 20 heads 44.8 instead of 36.2.  With 8 heads of 128, one
 // sequence of 500 takes 7.5 us so and 10.5 divided, of 1000 11.2 and 11.2, of 2000 17.4 and 11.2; 16 ragged ones of up to 1000 11.7 and
 // 13.9, 128 of up to 500 by 20 heads 41.6 and 59.1.
 constexpr int kWholeTiles = 32;

@@ -7,9 +7,9 @@
 // a pair are in one lane: two runs of 4 elements, 4 i and r / 2 + 4 i (neighbours: 8 i and 8 i + 4).  Every byte moves once.
 // Angles are turns: position * (inv_freq / 2 pi) in float64 is off by at most 2^-51 of itself, 2^-22 of a turn at any 32-bit
 // position and frequency of one, where float32 would keep none at far ones; the whole turns go, and the sine and cosine of the
-// rest are float32.  A workgroup forms them once for
-// its tokens, in LDS, while its first rows are on their way.  8191 tokens of 32 + 8 heads of 128: 31 us, 5.4 TB/s; 48 of them, with
-// the values into the cache, 3.5 us on the GPU.
+// rest are float32.  A workgroup forms them once for its tokens, in LDS, while its first rows are on their way.  8191 tokens of
+// 32 + 8 heads of 128: 31 to 32 us a call among others, 5.3 TB/s, where a copy of as many bytes takes 29.7; 48 of them, with the
+// values into the cache, 3.6 us on the GPU.
 #include <algorithm>
 
 #include "spa_attn.h"
@@ -107,7 +107,7 @@ struct Eight {
 };
 
 // SIDE: the heads fill no more than half of the groups, and several rows of TOK tokens stand side by side (33229 tokens of 8 + 1
-// heads of 64 into the cache 30.1 -> 23.1 us).
+// heads of 64 into the cache 29.7 -> 22.4 us).
 // A lane group takes one head of TOK tokens at a time, then the next head that is the workgroup's groups further on: kind,
 // weights and addresses are found once for the TOK rows, whose loads are all in flight, and the next head's replace them as they
 // are worked on.
