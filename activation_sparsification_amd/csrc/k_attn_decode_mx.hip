@@ -17,8 +17,8 @@
 //         8191 52.4 -> 50.6 us, 32 of up to 8000 by 16 + 4 heads of 96 23.7 -> 21.9).
 //
 // 64 ragged sequences of up to 8191 positions by 8 heads of 128: 52 us with the join, 4.7 TB/s; two of 200003 79 us, 5.5 TB/s (a
-// stream that is only read reaches 7.2); one of 61 5.6 us.  The choices below
-// were timed with a bfloat16 call's weights in one product.
+// stream that is only read reaches 7.2); one of 61 5.6 us.  The choices below were timed with
+// a bfloat16 call's weights in one product.
 #include "spa_attn_decode.h"
 
 namespace spa {

@@ -109,7 +109,6 @@ void is(spa_status want, const char* name, F change) {
     if (got != want && g_fails++ < 20) std::printf("fail: %s (cache %d): status %d, not %d\n", name, (int)call.cached, (int)got, (int)want);
   }
 }
-// What a lane of the last head reads or writes lies within the vectors, so one byte of another argument is enough.
 template <typename F>
 void refused(const char* name, F change) { is(SPA_ERR_INVALID, name, change); }
 template <typename F>
